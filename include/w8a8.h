@@ -17,6 +17,9 @@
  *  q8_0_gemv_rms  the same read with an RMS-norm prologue: y = rs[t] * (x * gamma) @ w (same page,
  *              same section: the down kernel's R' * w_norm staging with the sums of squares).
  *
+ * and, between a layer's QKV product and its output projection: qk_norm_rope, kv8_append,
+ * kv8_attention and kv8_read, a key-value cache held in 8 bits with what fills and reads it.
+ *
  * Conventions for every entry point:
  *  - Data pointers are DEVICE pointers (cudaMalloc or equivalent) unless stated otherwise; the
  *    caller owns every buffer.  `stream` is a cudaStream_t passed as void* (NULL = legacy stream).
@@ -60,8 +63,11 @@ enum {
 enum {
     W8A8_DEV_WAIT_TIMEOUT = 1u,       /* a pipeline wait exceeded its bound (about one second);
                                          the kernel abandoned the call and returned */
-    W8A8_DEV_COUNTER_CORRUPT = 2u     /* an arrival counter held a value outside [0, arrivals):
+    W8A8_DEV_COUNTER_CORRUPT = 2u,    /* an arrival counter held a value outside [0, arrivals):
                                          the workspace was not zeroed, or calls overlapped */
+    W8A8_DEV_BAD_INDEX = 4u           /* qk_norm_rope and kv8_*: an index in device memory (row0,
+                                         kv_len, page_table, positions) was out of range; nothing
+                                         was read or written through it */
 };
 
 /* Launch flags of w8a8_gemm and q8_0_gemv. */
@@ -341,6 +347,137 @@ int q8_0_quantize(const void* w, int8_t* q, void* d, int K, int N, void* stream)
  * back.  The same bytes, reordered.  Limits and errors as for q8_0_quantize. */
 int q8_0_split_from_blocks(const void* blocks, int8_t* q, void* d, int K, int N, void* stream);
 int q8_0_blocks_from_split(const int8_t* q, const void* d, void* blocks, int K, int N, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Attention side of a decode step: rotation, the 8-bit paged key-value cache, attention over it.
+ * They go between the QKV product and the output projection of a layer, and serve single tokens,
+ * verify windows and prompts.  All of them: 16-bit values are bf16 or fp16 (`dtype`); head_dim 64,
+ * 128 or 256; 16-bit tensors are [rows][heads][head_dim] with contiguous heads and a row stride in
+ * elements (a multiple of 8, so that a slice of a fused QKV product can be passed as it is), 16-byte
+ * aligned.  Each call is one kernel launch on `stream`, a programmatic dependent of the work before
+ * it that touches no memory before that work has completed; no host synchronisation, allocation or
+ * memset; it can be captured into a CUDA graph, and the graph replayed with other lengths, page
+ * tables and positions, which live in device memory.
+ *
+ * `ws` is a workspace as above (zeroed once, used by one stream at a time) of at least
+ * kv8_workspace_bytes; it is not to be shared with the GEMM and Q8_0 calls, since attention leaves
+ * partial sums in it.  Indices in device memory cannot be checked on the host: the kernels check
+ * them before every use, leave out what they would have addressed, and record W8A8_DEV_BAD_INDEX
+ * (w8a8_workspace_status).
+ * ------------------------------------------------------------------------------------------- */
+
+enum { KV8_BF16 = 0, KV8_F16 = 1 };   /* dtype of the 16-bit tensors of a call */
+
+enum {
+    /* kv8_attention: every row sees every cached token of its sequence (window has to be 0). */
+    KV8_FLAG_NOT_CAUSAL = 1u
+};
+
+/* The cache of one layer.  A byte stands for (byte - 128) * scale with one fp32 scale for each
+ * (page, kv head); page_tokens is both the page size and the block of tokens that shares a scale.
+ *  k, v               uint8 [pages][kv_heads][page_tokens][head_dim], 16-byte aligned
+ *  k_scale, v_scale   fp32 [pages][kv_heads]
+ *  page_tokens 16, 32, 64 or 128; kv_heads <= 1024; pages * kv_heads * page_tokens < 2^31.
+ * Bytes and scales of slots that no append has filled are never used, whatever they hold. */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int pages;
+    int kv_heads;
+    int page_tokens;
+    int head_dim;
+} kv8_cache_t;
+
+/* The rows of one step.  Sequence b owns rows row0[b] ... row0[b + 1] - 1 (n of them, none is
+ * allowed) of the call's [tokens] rows; they are its last tokens, slots kv_len[b] - n ...
+ * kv_len[b] - 1 of its cache, so kv_len counts the tokens of the step.  Slot t of sequence b is
+ * token t % page_tokens of page page_table[b * table_width + t / page_tokens]; entries past the last
+ * slot are never read.
+ *  row0 [seqs + 1], kv_len [seqs], page_table [seqs][table_width]: int32, device memory
+ *  tokens      rows of the call (row0[seqs]); 0 makes the call a no-op
+ *  max_tokens  an upper bound of every sequence's rows (sizes the launch)
+ *  seqs <= 65535, tokens and max_tokens <= 2^22, table_width * page_tokens <= 2^30. */
+typedef struct {
+    const int32_t* row0;
+    const int32_t* kv_len;
+    const int32_t* page_table;
+    int seqs;
+    int tokens;
+    int max_tokens;
+    int table_width;
+} kv8_step_t;
+
+/* What a head's values go through before they are used: an RMS norm over the head, then the
+ * rotation by the position.
+ *  gamma_q, gamma_k  [head_dim] norm weights of the call's dtype (16-byte aligned); NULL: no norm
+ *  eps               finite and >= 0 (used with a gamma)
+ *  cos_sin           fp32 [max_pos][rot_dim]: a position's rot_dim / 2 cosines, then its sines,
+ *                    16-byte aligned (not used with rot_dim 0)
+ *  rot_dim           leading values of a head that rotate: a multiple of 16, 0 ... head_dim
+ *  interleaved       0: pairs (i, i + rot_dim / 2); else pairs (2 i, 2 i + 1) */
+typedef struct {
+    const void* gamma_q;
+    const void* gamma_k;
+    const float* cos_sin;
+    float eps;
+    int rot_dim;
+    int max_pos;
+    int interleaved;
+} qk_prep_t;
+
+/* Workspace bytes of every call below at these head counts (0 for arguments they would reject),
+ * whatever the step. */
+size_t kv8_workspace_bytes(int q_heads, int kv_heads, int head_dim);
+
+/* Queries and keys of `tokens` rows through `prep`, for a cache of another kind (kv8_append does the
+ * same on the way into the 8-bit cache).  y = turn(x * gamma / sqrt(mean x^2 + eps)) in fp32, rounded
+ * once.  positions [tokens] int32 (may be NULL with rot_dim 0).  q_heads or kv_heads may be 0.  In
+ * place (q_out = q, k_out = k, same strides) is allowed; other overlaps are not.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE_TOO_SMALL (256 bytes), CUDA. */
+int qk_norm_rope(const qk_prep_t* prep, const void* q, long long q_stride, int q_heads, const void* k,
+                 long long k_stride, int kv_heads, int head_dim, const int32_t* positions, int tokens,
+                 void* q_out, long long q_out_stride, void* k_out, long long k_out_stride, int dtype,
+                 void* ws, size_t ws_bytes, void* stream);
+
+/* Append the step's keys (through `prep`: norm and rotation; NULL: as they are) and values to the
+ * cache, and put its queries (q_heads of them; 0: none) through `prep` into q_out, in one launch.
+ *  positions  [tokens] int32 rotation positions, or NULL: each row's cache slot
+ * A page's scale is the largest magnitude given to it over 127: with r of its slots filled before
+ * the step, s = max(s_old, amax / 127) for r > 0, and amax / 127 for r = 0 (the page starts anew),
+ * amax over the step's values of the page and head.  A value x is held as
+ * 128 + clamp(round(x / s), -127, 127), halves away from zero (128 for s = 0), from fp32: nothing is
+ * rounded to 16 bits on the way.  Where s grows, the r earlier tokens are held again as
+ * 128 + round((byte - 128) * s_old / s).  So tokens taken back (a smaller kv_len, as after a verify
+ * window) are simply written over, at a scale that is large enough.  A NaN is held as 0, an infinity
+ * as the largest finite value.
+ * Every sequence needs n <= kv_len.  No page may belong to two sequences that append to it.
+ * Errors as above. */
+int kv8_append(const kv8_cache_t* cache, const kv8_step_t* step, const qk_prep_t* prep, const void* k,
+               long long k_stride, const void* v, long long v_stride, const void* q, long long q_stride,
+               int q_heads, void* q_out, long long q_out_stride, const int32_t* positions, int dtype,
+               void* ws, size_t ws_bytes, void* stream);
+
+/* Attention of the step's queries q [tokens][q_heads][head_dim] over the cache; query head h reads kv
+ * head h / (q_heads / kv_heads).  Row i of a sequence stands at slot p = kv_len - n + i and sees slots
+ * max(0, p - window + 1) ... p (window 0: all up to p), or all kv_len with KV8_FLAG_NOT_CAUSAL:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j       lse = log sum_j exp(scale * q . k_j)
+ * in one pass with fp32 sums and statistics, rounded once.  A row that sees nothing (kv_len 0, or
+ * n > kv_len) gets out = 0 and lse = -inf.
+ *  out  [tokens][q_heads][head_dim] of dtype;  lse  fp32 [tokens][q_heads] contiguous, or NULL
+ *  scale  finite and > 0
+ * Replays give the same bits.  Errors as above. */
+int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride,
+                  int q_heads, void* out, long long out_stride, float* lse, float scale, int window,
+                  unsigned flags, int dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* The step's tokens out of the cache as 16-bit values: row r of k_out and v_out
+ * ([tokens][kv_heads][head_dim]) is (byte - 128) * scale of that row's slot, rounded once.  Every
+ * sequence needs n <= kv_len; a step with other row0 than the append's reads any tail of it.
+ * Errors as above. */
+int kv8_read(const kv8_cache_t* cache, const kv8_step_t* step, void* k_out, long long k_stride, void* v_out,
+             long long v_stride, int dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* Measurement helper (not part of either operator): reads `bytes` (rounded down to a multiple of
  * 16) of device memory at `buf` once with 16-byte vector loads, on 2 x SM-count CTAs of 512

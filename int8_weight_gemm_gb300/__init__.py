@@ -37,6 +37,15 @@ __all__ = [
     "q8_0_split_from_blocks",
     "q8_0_blocks_from_split",
     "alloc_workspace",
+    "KV8Cache",
+    "KV8Step",
+    "QKPrep",
+    "kv8_cache",
+    "kv8_workspace_bytes",
+    "kv8_append",
+    "kv8_attention",
+    "kv8_read",
+    "qk_norm_rope",
 ]
 
 W8A8_OK = 0
@@ -45,6 +54,10 @@ W8A8_FLAG_TENSOR_MEMORY_ARM = 2
 W8A8_FLAG_TEST_STALL = 0x100
 W8A8_DEV_WAIT_TIMEOUT = 1
 W8A8_DEV_COUNTER_CORRUPT = 2
+W8A8_DEV_BAD_INDEX = 4
+KV8_BF16 = 0
+KV8_F16 = 1
+KV8_FLAG_NOT_CAUSAL = 1
 
 # Every symbol include/w8a8.h declares, with its ctypes signature.
 _c_p = ctypes.c_void_p
@@ -71,6 +84,23 @@ class PlanT(ctypes.Structure):
         ("split_unit", ctypes.c_int),
     ]
 
+
+class KV8CacheT(ctypes.Structure):
+    _fields_ = [("k", _c_p), ("v", _c_p), ("k_scale", _c_p), ("v_scale", _c_p), ("pages", _c_i), ("kv_heads", _c_i),
+                ("page_tokens", _c_i), ("head_dim", _c_i)]
+
+
+class KV8StepT(ctypes.Structure):
+    _fields_ = [("row0", _c_p), ("kv_len", _c_p), ("page_table", _c_p), ("seqs", _c_i), ("tokens", _c_i),
+                ("max_tokens", _c_i), ("table_width", _c_i)]
+
+
+class QKPrepT(ctypes.Structure):
+    _fields_ = [("gamma_q", _c_p), ("gamma_k", _c_p), ("cos_sin", _c_p), ("eps", ctypes.c_float), ("rot_dim", _c_i),
+                ("max_pos", _c_i), ("interleaved", _c_i)]
+
+
+_c_ll = ctypes.c_longlong
 
 SIGNATURES = {
     "w8a8_version": ([], _c_i),
@@ -100,6 +130,14 @@ SIGNATURES = {
     "q8_0_gemv": ([_c_p, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, ctypes.c_uint, _c_p, _c_sz, _c_p], _c_i),
     "q8_0_gemv_rms": ([_c_p, _c_p, ctypes.c_float, _c_p, _c_p, _c_p, _c_i, _c_i, _c_i, ctypes.c_uint, _c_p, _c_sz, _c_p],
                       _c_i),
+    "kv8_workspace_bytes": ([_c_i, _c_i, _c_i], _c_sz),
+    "qk_norm_rope": ([_c_p, _c_p, _c_ll, _c_i, _c_p, _c_ll, _c_i, _c_i, _c_p, _c_i, _c_p, _c_ll, _c_p, _c_ll, _c_i, _c_p,
+                      _c_sz, _c_p], _c_i),
+    "kv8_append": ([_c_p, _c_p, _c_p, _c_p, _c_ll, _c_p, _c_ll, _c_p, _c_ll, _c_i, _c_p, _c_ll, _c_p, _c_i, _c_p, _c_sz,
+                    _c_p], _c_i),
+    "kv8_attention": ([_c_p, _c_p, _c_p, _c_ll, _c_i, _c_p, _c_ll, _c_p, ctypes.c_float, _c_i, ctypes.c_uint, _c_i, _c_p,
+                       _c_sz, _c_p], _c_i),
+    "kv8_read": ([_c_p, _c_p, _c_p, _c_ll, _c_p, _c_ll, _c_i, _c_p, _c_sz, _c_p], _c_i),
 }
 
 _lib = None
@@ -424,3 +462,229 @@ def q8_0_blocks_from_split(q, d, blocks=None, stream=None):
     _on_cuda(q=q, d=d, blocks=blocks)
     _check("q8_0_blocks_from_split", lib().q8_0_blocks_from_split(_ptr(q), _ptr(d), _ptr(blocks), K, N, _stream(stream)))
     return blocks
+
+
+# ---------------------------------------------------------------------------------------------
+# Attention side: rotation, the 8-bit paged cache, attention.  A serving loop calls these once a layer and step, so
+# what does not change between calls (the cache, a step's index buffers, the norm weights and rotation table) is
+# checked once, in a handle that holds its tensors.
+
+class KV8Cache:
+    """One layer's cache: k, v uint8 [pages, kv_heads, page_tokens, head_dim], k_scale, v_scale fp32 [pages, kv_heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 4:
+            raise ValueError(f"k: expected [pages, kv_heads, page_tokens, head_dim], got {tuple(k.shape)}")
+        if v.shape != k.shape:
+            raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+        pages, heads, page_tokens, dim = k.shape
+        _dev(k, "k", esize=1)
+        _dev(v, "v", esize=1)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if tuple(t.shape) != (pages, heads):
+                raise ValueError(f"{name}: expected shape {(pages, heads)}, got {tuple(t.shape)}")
+            _dev(t, name, esize=4)
+        _on_cuda(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, page_tokens, dim
+        self.c = KV8CacheT(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page_tokens, dim)
+        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+
+
+def kv8_cache(pages: int, kv_heads: int, page_tokens: int, head_dim: int, device="cuda") -> KV8Cache:
+    """A new cache (its contents are undefined until they are appended)."""
+    import torch
+
+    k, v = (torch.empty((pages, kv_heads, page_tokens, head_dim), dtype=torch.uint8, device=device) for _ in range(2))
+    ks, vs = (torch.empty((pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2))
+    return KV8Cache(k, v, ks, vs)
+
+
+class KV8Step:
+    """The rows of a step: row0 [seqs + 1], kv_len [seqs], page_table [seqs, table_width], int32 tensors that may be
+    rewritten between calls; tokens rows in all, at most max_tokens of one sequence."""
+
+    def __init__(self, row0, kv_len, page_table, tokens: int, max_tokens: int):
+        if page_table.dim() != 2:
+            raise ValueError(f"page_table: expected [seqs, table_width], got {tuple(page_table.shape)}")
+        seqs, width = page_table.shape
+        for name, t, shape in (("row0", row0, (seqs + 1,)), ("kv_len", kv_len, (seqs,)), ("page_table", page_table, (seqs, width))):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+            _dev(t, name, esize=4)
+            if t.is_floating_point():
+                raise ValueError(f"{name}: expected int32, got {t.dtype}")
+        _on_cuda(row0=row0, kv_len=kv_len, page_table=page_table)
+        self.row0, self.kv_len, self.page_table = row0, kv_len, page_table
+        self.tokens = tokens
+        self.c = KV8StepT(row0.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs, tokens, max_tokens, width)
+        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+
+
+class QKPrep:
+    """Norm and rotation of queries and keys: cos_sin fp32 [max_pos, rot_dim] (cosines, then sines), gamma_q and
+    gamma_k [head_dim] of the calls' dtype or None."""
+
+    def __init__(self, cos_sin=None, rot_dim: int = 0, gamma_q=None, gamma_k=None, eps: float = 1e-6, interleaved: bool = False):
+        max_pos = 0
+        if rot_dim > 0:
+            if cos_sin is None or cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim:
+                raise ValueError(f"cos_sin: expected [max_pos, {rot_dim}], got {None if cos_sin is None else tuple(cos_sin.shape)}")
+            _dev(cos_sin, "cos_sin", esize=4)
+            max_pos = cos_sin.shape[0]
+        for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+            if g is not None:
+                _dev(g, name, esize=2)
+        _on_cuda(cos_sin=cos_sin if rot_dim > 0 else None, gamma_q=gamma_q, gamma_k=gamma_k)
+        self.cos_sin, self.gamma_q, self.gamma_k = cos_sin, gamma_q, gamma_k
+        gammas = [g for g in (gamma_q, gamma_k) if g is not None]
+        self.dtype, self.gamma_len = (gammas[0].dtype, min(g.numel() for g in gammas)) if gammas else (None, 0)
+        if any(g.dtype != self.dtype for g in gammas):
+            raise ValueError(f"gamma_k: expected {self.dtype}, got {gamma_k.dtype}")
+        self.c = QKPrepT(gamma_q.data_ptr() if gamma_q is not None else None, gamma_k.data_ptr() if gamma_k is not None else None,
+                         cos_sin.data_ptr() if rot_dim > 0 else None, float(eps), rot_dim, max_pos, int(interleaved))
+        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+
+    def check(self, dtype, head_dim):
+        if self.dtype is not None and (self.dtype != dtype or self.gamma_len < head_dim):
+            raise ValueError(f"gamma_q, gamma_k: expected {head_dim} of {dtype}, got {self.gamma_len} of {self.dtype}")
+
+
+_kv8_dtypes = None
+
+
+def _kv8_dtype(t, name):
+    global _kv8_dtypes
+    if _kv8_dtypes is None:
+        import torch
+
+        _kv8_dtypes = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16}
+    code = _kv8_dtypes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _heads(t, name, rows, heads, dim, dtype):
+    """A [rows, heads, dim] tensor whose rows may be strided (heads contiguous): its row stride."""
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name}: expected shape {(rows, heads, dim)}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != dim and heads > 1):
+        raise ValueError(f"{name}: expected contiguous heads (strides {tuple(t.stride())})")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    return s0 if rows > 1 else heads * dim
+
+
+def _positions(t, rows):
+    if t is None:
+        return None
+    _dev(t, "positions", 4 * rows, esize=4)
+    if t.is_floating_point():
+        raise ValueError(f"positions: expected int32, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _ws(ws):
+    if not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor (strides {tuple(ws.stride())})")
+    return ws.data_ptr(), ws.nbytes
+
+
+@functools.lru_cache(maxsize=1024)
+def kv8_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().kv8_workspace_bytes(q_heads, kv_heads, head_dim))
+
+
+def qk_norm_rope(prep, q, k, positions, ws, q_out=None, k_out=None, stream=None):
+    """(q, k) [tokens, heads, head_dim] through `prep` at `positions` [tokens] int32; q_out = q and k_out = k work in
+    place."""
+    import torch
+
+    rows, q_heads, dim = q.shape
+    kv_heads = k.shape[1]
+    dt = _kv8_dtype(q, "q")
+    if q_out is None:
+        q_out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((rows, kv_heads, dim), dtype=q.dtype, device=q.device)
+    prep.check(q.dtype, dim)
+    qs, ks = _heads(q, "q", rows, q_heads, dim, q.dtype), _heads(k, "k", rows, kv_heads, dim, q.dtype)
+    qo, ko = _heads(q_out, "q_out", rows, q_heads, dim, q.dtype), _heads(k_out, "k_out", rows, kv_heads, dim, q.dtype)
+    pos = _positions(positions, rows)
+    wp, wn = _ws(ws)
+    _on_cuda(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out, ws=ws)
+    rc = lib().qk_norm_rope(prep, q.data_ptr(), qs, q_heads, k.data_ptr(), ks, kv_heads, dim, pos, rows, q_out.data_ptr(), qo,
+                            k_out.data_ptr(), ko, dt, wp, wn, _stream(stream))
+    _check("qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def kv8_append(cache, step, prep, k, v, ws, q=None, q_out=None, positions=None, stream=None):
+    """Append k, v [tokens, kv_heads, head_dim] of the step to the cache, k through `prep` (None: as it is); q
+    [tokens, q_heads, head_dim] goes through `prep` into q_out, which is returned (None without q)."""
+    import torch
+
+    rows, heads, dim = step.tokens, cache.kv_heads, cache.head_dim
+    dt = _kv8_dtype(k, "k")
+    ks, vs = _heads(k, "k", rows, heads, dim, k.dtype), _heads(v, "v", rows, heads, dim, k.dtype)
+    if prep is not None:
+        prep.check(k.dtype, dim)
+    q_heads = qs = qo = 0
+    qp = qop = None
+    if q is not None:
+        q_heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+        qs, qo = _heads(q, "q", rows, q_heads, dim, k.dtype), _heads(q_out, "q_out", rows, q_heads, dim, k.dtype)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out: given without q")
+    pos = _positions(positions, rows)
+    wp, wn = _ws(ws)
+    _on_cuda(k=k, v=v, q=q, q_out=q_out, positions=positions, ws=ws)
+    rc = lib().kv8_append(cache, step, prep, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, q_heads, qop, qo, pos, dt, wp, wn,
+                          _stream(stream))
+    _check("kv8_append", rc)
+    return q_out
+
+
+def kv8_attention(cache, step, q, ws, out=None, lse=None, scale=None, window: int = 0, flags: int = 0, stream=None):
+    """softmax(scale q k^T) v of q [tokens, q_heads, head_dim] over the cache -> out (the same shape); lse fp32
+    [tokens, q_heads] is filled if given.  scale defaults to 1 / sqrt(head_dim)."""
+    import torch
+
+    rows, dim = step.tokens, cache.head_dim
+    dt = _kv8_dtype(q, "q")
+    q_heads = q.shape[1]
+    if out is None:
+        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+    qs, os_ = _heads(q, "q", rows, q_heads, dim, q.dtype), _heads(out, "out", rows, q_heads, dim, q.dtype)
+    lp = None
+    if lse is not None:
+        _dev(lse, "lse", 4 * rows * q_heads, esize=4)
+        lp = lse.data_ptr()
+    wp, wn = _ws(ws)
+    _on_cuda(q=q, out=out, lse=lse, ws=ws)
+    rc = lib().kv8_attention(cache, step, q.data_ptr(), qs, q_heads, out.data_ptr(), os_, lp,
+                             dim ** -0.5 if scale is None else scale, window, flags, dt, wp, wn, _stream(stream))
+    _check("kv8_attention", rc)
+    return out
+
+
+def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
+    """The step's tokens out of the cache: (k, v) [tokens, kv_heads, head_dim], bf16 unless k_out or dtype says otherwise."""
+    import torch
+
+    rows, heads, dim = step.tokens, cache.kv_heads, cache.head_dim
+    if k_out is None:
+        k_out = torch.empty((rows, heads, dim), dtype=dtype or torch.bfloat16, device=cache.k.device)
+    if v_out is None:
+        v_out = torch.empty((rows, heads, dim), dtype=k_out.dtype, device=cache.k.device)
+    dt = _kv8_dtype(k_out, "k_out")
+    ks, vs = _heads(k_out, "k_out", rows, heads, dim, k_out.dtype), _heads(v_out, "v_out", rows, heads, dim, k_out.dtype)
+    wp, wn = _ws(ws)
+    _on_cuda(k_out=k_out, v_out=v_out, ws=ws)
+    _check("kv8_read", lib().kv8_read(cache, step, k_out.data_ptr(), ks, v_out.data_ptr(), vs, dt, wp, wn, _stream(stream)))
+    return k_out, v_out
