@@ -5,22 +5,28 @@
 //   o = sum_j softmax_j(scale q . k_j) v_j,   k_j = (byte - 128) * k_scale[page], v_j alike.
 //
 // What bounds it: every cached byte feeds 2 (rows / kv heads) multiply-adds, a handful for single
-// tokens, so the cache has to stream at HBM speed and everything else has to hide behind it.
+// tokens, so the cache has to stream at HBM speed and everything else has to hide behind it: at 6.8
+// TB/s an SM has about 700 issue slots for a granule (16 tokens of a head, keys and values: 4 KiB at
+// head_dim 128).
 //
-// Mathematics.  The n * G rows that share a kv head (n tokens, G query heads) are the rows of 16-row
-// tiles; 16 cached tokens are a granule.
-//  * Scores on mma.sync m16n8k16, fp16 x fp16 -> fp32.  A cached byte b is used as the fp16 subnormal
-//    b * 2^-24 (one byte permute makes two of them, nothing is subtracted); 128 * sum_d q comes off
-//    each score once.  A query row is scaled by a power of two (exact) that takes its largest value to
+// Mathematics.  The n * G rows that share a kv head (n tokens, G query heads) are the columns of 8-wide
+// tiles, the cached tokens the rows: S^T = K Q^T and O^T = V^T P^T on mma.sync m16n8k16 (fp16 x fp16 ->
+// fp32).  Rows as the narrow side make a tile of 8 where the other way round it would be 16: half the
+// matrix instructions, exponentials and accumulators for up to 8 rows.
+//  * Scores.  A cached byte b is used as the fp16 subnormal b * 2^-24 (one instruction makes two of
+//    them, nothing is subtracted); 128 * sum_d q comes off each score in the multiply-add that applies
+//    the scales.  A query row is scaled by a power of two (exact) that takes its largest value to
 //    [2^13, 2^14), so bf16 queries lose nothing in fp16 down to 2^-27 of the row's largest.  The order
-//    of d inside the matrix product is free, and is chosen so that a lane's bytes are 16 contiguous ones.
+//    of d inside the product is free, and is chosen so that a lane's bytes are contiguous.
 //  * One pass with running references.  p = 2^(s - m) sums to l in fp32.  The values' scale belongs to
 //    the weights: w = 2^(s - m) * (v_scale * 2^(m - r)), rounded to fp16 (11 bits, against 8 for bf16:
 //    with bf16 weights the error of a sum of independent values equals the output's own rounding), and
-//    o = sum w (b - 128), the bytes converted exactly.  r follows the largest w as m follows the largest
-//    s, so neither a page of tiny values under the largest score nor the reverse loses bits.  Both
-//    references move only when a row's largest score or weight passes them by 2^8: w stays inside
-//    fp16's range, and the sums are rescaled a few times per pass instead of at every granule.
+//    o = sum w (b - 128), the bytes converted exactly (the offset is not left to a subtraction at the
+//    end: 128 sum w would be a thousand times the sum of a long cache's values).  r follows the largest
+//    w as m follows the largest s, so neither a page of tiny values under the largest score nor the
+//    reverse loses bits.  Both references move only when a score or weight passes them by 2^8: w stays
+//    inside fp16's range, the sums are rescaled a few times per pass instead of at every granule, and
+//    in between no lane needs another lane's maximum.
 //  * Parts (warps of a CTA, CTAs of a split sequence) join as o 2^(r_i - r), l 2^(m_i - m), in a fixed
 //    order whatever the order of arrival, so replays give the same bits.
 //
@@ -28,11 +34,10 @@
 // of head, whose hardware swizzle makes both operands' shared-memory reads conflict-free.  Every warp
 // is its own pipeline (its ring of granules, its mbarriers, its running sums), so nothing in the loop
 // waits for another warp; the page number and scales of its next 32 granules are one load a lane.
-// The work is cut over all (sequence, row tile, kv head) items laid end to end, in units of 64 tokens,
-// into equal runs, one for each CTA: lengths live on the device, so each CTA finds its run from a scan
-// of kv_len.  An item cut across CTAs is finished by the last of them to arrive.  Three CTAs of four
-// warps share an SM (two where the accumulators are larger), so that one CTA's start, join and drain
-// hide behind the others' streams.
+// The work is cut over all (sequence, row tile, kv head) items laid end to end, in units of one
+// granule for each warp, into equal runs, one for each CTA: lengths live on the device, so each CTA
+// finds its run from a scan of kv_len.  An item cut across CTAs is finished by the last of them to
+// arrive.  Two CTAs share an SM, so that one's start, join and drain hide behind the other's stream.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -43,31 +48,39 @@
 namespace w8a8 {
 namespace attn {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kGranule = 16;         // tokens of a warp's step
-constexpr int kUnit = 64;            // tokens of the split's unit: a granule for each warp
 constexpr float kFloor = -3.0e38f;   // reference of a row that has seen nothing
 constexpr float kSlack = 8.f;        // a reference moves when it is passed by this much (powers of two)
 constexpr float kSpan = 120.f;       // largest distance of the two references
 
-// R: 16-row tiles a warp holds.
-template <int D, int R>
+// NT: 8-row tiles a warp holds.  A lane holds D NT / 4 sums, so the warps that an SM can hold follow
+// from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in two CTAs.
+template <int D, int NT>
 struct Layout {
+  static constexpr int kWarps = D * NT <= 128 ? 8 : D * NT <= 256 ? 6 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtas = 2;                       // CTAs on an SM
+  static constexpr int kUnit = kGranule * kWarps;       // tokens of the split's unit
+  static constexpr int kRows = 8 * NT;
   static constexpr int kBoxes = D > 128 ? D / 128 : 1;
   static constexpr int kBoxBytes = kGranule * (D > 128 ? 128 : D);
   static constexpr int kSide = kBoxes * kBoxBytes;      // keys (or values) of a granule
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kCtas = D * R > 128 ? 2 : 3;      // CTAs on an SM
-  static constexpr int kStages = (kCtas == 3 ? 16384 : 24576) / kStage;   // a warp's ring
-  static constexpr int kRow = D + 4;                    // floats of a row in the join buffer
+  static constexpr int kStages = 98304 / (kWarps * kStage);   // a warp's ring
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kSmem = 1024 + kRing;
-  static constexpr int kRows = 16 * R;
-  // A part of a split item in the workspace: kRows x D sums, then m, l, r of each row.
+  // The queries' fragments are the same for every warp: in shared memory where registers are short.
+  static constexpr bool kQShared = D * NT > 256;
+  static constexpr int kQBytes = kQShared ? NT * (D / 16) * 32 * 8 : 0;
+  static constexpr int kSmem = 1024 + kRing + kQBytes;
+  static constexpr int kRow = D + 4;                    // floats of a row in the join buffer
+  // What an item costs beside its tokens (queries, first copies, join), in units: each item's place in
+  // the split is that much longer, so a run that crosses into another item gets fewer tokens.
+  static constexpr int kLead = 2;
+  // A part of a split item in the workspace: kRows x D sums, then (m, l, r, -) of each row.
   static constexpr int kPart = kRows * (D + 4);
-  static_assert(kWarps * 16 * kRow * 4 <= kRing, "the join buffer lies over the rings");
+  static_assert(kWarps * kRows * kRow * 4 <= kRing, "the join buffer lies over the rings");
   static_assert(kStages >= 2 && kStages <= 16, "ring depth");
+  static_assert(kCtas * (kSmem + 4096) <= 232448, "shared memory of an SM");
 };
 
 struct Params {
@@ -97,47 +110,79 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// Transpose of an 8 x 8 matrix of 16-bit values held as two of row lane / 4 by each lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t t;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+  return t;
+}
+
+// a / b for a >= 0, b > 0: a 64-bit division is a long subroutine, and hardly ever needed.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // What the rows of a sequence cover: items of `tiles` row tiles and kv heads, each of `units` units
-// from token `lo` (a granule's start) to `hi`.
+// from token `lo` (a granule's start) to `hi`; `span` = the lead and the units, its length in the split.
 struct Span {
   Seq s;
-  int tiles, units, lo, hi;
+  int tiles, units, span, lo, hi;
 };
 
-template <int kRows>
+template <typename L>
 __device__ __forceinline__ Span load_span(const Params& p, int b) {
   Span x;
   load_seq(p.step, b, 1 << p.page_shift, false, p.status, x.s);
-  x.tiles = (int)(((long long)x.s.n * p.group + kRows - 1) / kRows);
+  x.tiles = (int)quotient((long long)x.s.n * p.group + L::kRows - 1, L::kRows);
   x.hi = x.s.len;
   x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : 0;
-  x.units = max(1, (x.hi - x.lo + kUnit - 1) / kUnit);   // one that sees nothing still writes its rows
+  x.units = max(1, (x.hi - x.lo + L::kUnit - 1) / L::kUnit);   // one that sees nothing still writes its rows
+  x.span = L::kLead + x.units;
   return x;
 }
 
 // The equal runs: U units over `ctas`, the first U % ctas one longer.
 struct Runs {
   long long a, r;
-  __device__ Runs(long long U, int ctas) : a(U / ctas), r(U % ctas) {}
+  __device__ Runs(long long U, int ctas) : a(quotient(U, ctas)), r(U - a * ctas) {}
   __device__ long long begin(int i) const { return i * a + (i < r ? i : r); }
   __device__ int owner(long long u) const {
     const long long head = r * (a + 1);
-    return (int)(u < head ? u / (a + 1) : r + (u - head) / a);
+    return (int)(u < head ? quotient(u, a + 1) : r + quotient(u - head, a));
   }
 };
 
-template <bool kF16, int D, int R>
-__global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_kernel(const __grid_constant__ Params p) {
-  using L = Layout<D, R>;
+// Four output values at d of one joined query row, and with the first of them the row's lse.
+template <bool kF16>
+__device__ __forceinline__ void store_row(const Params& p, int row0, int ri, int h, int d, int D, float4 acc, float M, float lt,
+                                          float Rf) {
+  const int orow = row0 + ri / p.group, head = h * p.group + ri % p.group;
+  const float z = lt == 0.f ? 0.f : __fdividef(1.f, lt) * ex2(Rf - M);
+  *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + head * D + d) =
+      make_uint2(pack2<kF16>(acc.x * z, acc.y * z), pack2<kF16>(acc.z * z, acc.w * z));
+  if (p.lse && d == 0) p.lse[(size_t)orow * p.q_heads + head] = lt == 0.f ? -INFINITY : (M + lg2(lt)) * 0.69314718056f;
+}
+
+template <bool kF16, int D, int NT>
+__global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
+    kv8_attention_kernel(const __grid_constant__ Params p) {
+  using L = Layout<D, NT>;
   constexpr int NS = L::kStages;
-  constexpr int kSteps = D / 16;    // k16 steps of a score
-  constexpr int kCols = D / 8;      // n8 tiles of the output
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
+  constexpr int kSteps = D / 16;    // k16 steps of a score; 16-row tiles of the output
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][NS];
-  __shared__ long long scan_sm[kWarps + 3];
-  __shared__ float mlr_sm[kWarps][16][3];
+  __shared__ long long scan_sm[kWarps];
+  __shared__ struct {
+    Span x;
+    int b;
+    long long u;
+  } start_sm;
+  __shared__ float4 mlr_sm[kWarps][L::kRows];   // (m, l, r, -) of each warp's rows
+  __shared__ float2 qstat_sm[L::kQShared ? L::kRows : 1];   // (multiplier, offset) of each row
   __shared__ int last_sm, abort_flag;
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint2* const qsm = reinterpret_cast<uint2*>(ring + L::kRing);   // [NT][kSteps][32] fragments
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -160,9 +205,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
   const int per = (p.step.seqs + kThreads - 1) / kThreads;   // sequences a thread scans
   const int s0 = min(p.step.seqs, (int)threadIdx.x * per), s1 = min(p.step.seqs, s0 + per);
   long long mine = 0;
+  Span x;   // the last sequence that this thread looked at
   for (int b = s0; b < s1; ++b) {
-    const Span x = load_span<L::kRows>(p, b);
-    mine += (long long)x.tiles * x.units;
+    x = load_span<L>(p, b);
+    mine += (long long)x.tiles * x.span;
   }
   mine *= p.kv_heads;
   long long incl = mine;
@@ -186,35 +232,37 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
   if (u0 >= before && u0 < before + mine) {
     // The sequence of this thread's that holds u0.
     long long at = before;
-    for (int b = s0; b < s1; ++b) {
-      const Span x = load_span<L::kRows>(p, b);
-      const long long n = (long long)x.tiles * x.units * p.kv_heads;
-      if (u0 < at + n) {
-        scan_sm[kWarps] = b;
-        scan_sm[kWarps + 1] = at;
-        break;
-      }
+    int b = s0;
+    for (; per > 1; ++b) {
+      x = load_span<L>(p, b);
+      const long long n = (long long)x.tiles * x.span * p.kv_heads;
+      if (u0 < at + n) break;
       at += n;
     }
+    start_sm.x = x;
+    start_sm.b = b;
+    start_sm.u = at;
   }
   __syncthreads();
-  int b = (int)scan_sm[kWarps];
-  long long seq_u0 = scan_sm[kWarps + 1];   // first unit of sequence b
-  Span x = load_span<L::kRows>(p, b);
+  x = start_sm.x;
+  int b = start_sm.b;
+  long long seq_u0 = start_sm.u;            // first unit of sequence b
   uint32_t count = 0;                       // granules this warp has taken (ring position and phase)
   bool dead = false;                        // a wait ran out: only the bookkeeping goes on
 
   for (long long u = u0; u < u1;) {
     // ---------------------------------------------------------------- the next segment: one item's part of the run
-    while (u >= seq_u0 + (long long)x.tiles * x.units * p.kv_heads) {
-      seq_u0 += (long long)x.tiles * x.units * p.kv_heads;
-      x = load_span<L::kRows>(p, ++b);
+    while (u >= seq_u0 + (long long)x.tiles * x.span * p.kv_heads) {
+      seq_u0 += (long long)x.tiles * x.span * p.kv_heads;
+      x = load_span<L>(p, ++b);
     }
-    const int item = (int)((u - seq_u0) / x.units);
-    const long long item_u0 = seq_u0 + (long long)item * x.units;
-    const int ub = (int)(u - item_u0), ue = (int)min((long long)x.units, u1 - item_u0);
+    const int item = (int)quotient(u - seq_u0, x.span);
+    const long long item_u0 = seq_u0 + (long long)item * x.span;   // its lead, then its units
+    const int ub = max((int)(u - item_u0) - L::kLead, 0), ue = (int)min((long long)x.span, u1 - item_u0) - L::kLead;
+    u = item_u0 + L::kLead + ue;
+    if (ue <= ub) continue;   // the run ends within the lead
     const int h = item % p.kv_heads, tile = item / p.kv_heads;
-    const int T0 = x.lo + ub * kUnit, T1 = min(x.hi, x.lo + ue * kUnit);
+    const int T0 = x.lo + ub * L::kUnit, T1 = min(x.hi, x.lo + ue * L::kUnit);
     const int granules = (T1 - T0 + kGranule - 1) / kGranule;
     const int mine_n = granules > warp ? (granules - warp + kWarps - 1) / kWarps : 0;
     const int rows_left = x.s.n * p.group - tile * L::kRows;   // rows of the tile that exist
@@ -261,89 +309,118 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
         }
       }
     };
+    // ---------------------------------------------------------------- this segment's queries
+    // Fragment B of step s, column g: slots (2c, 2c + 1) hold d0, d0 + 2 and slots (2c + 8, 2c + 9) hold
+    // d0 + 1, d0 + 3, d0 = the first of the lane's word s: the order in which a key's four bytes come
+    // apart.  A lane's words: D / 4 contiguous values (D = 256: 32 of each half).
+    uint32_t qb[L::kQShared ? 1 : NT][kSteps][2];
+    float rowmul[NT][2], offs[NT][2], m[NT][2], l[NT][2], r[NT][2], hs[NT][2];
+    int beg[NT][2], end[NT][2];
+    int full_lo = 0, full_hi = 0x7fffffff;   // tokens that every row sees
+    // The loads of the queries go out before the first copies of the cache, which would delay them by
+    // everything that the rings hold.
+    // (Shared fragments: warp w prepares tile w; every warp holds its own otherwise.)
+    constexpr int kMine = L::kQShared ? 1 : NT;
+    static_assert(!L::kQShared || NT <= kWarps, "a warp for each shared tile");
+    uint4 rows_raw[kMine][D / 32];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int row = (L::kQShared ? warp : i) * 8 + g;
+      const bool live = row < rows_left && row < L::kRows;
+      const int ri = tile * L::kRows + (live ? row : 0);
+      const uint16_t* const src = p.q + (x.s.row0 + ri / p.group) * p.q_stride + (h * p.group + ri % p.group) * D;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const int d = D == 256 ? 128 * (w >> 2) + 32 * c + 8 * (w & 3) : (D / 4) * c + 8 * w;
+        rows_raw[i][w] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
     if (!dead && mine_n > 0) {
       fetch(0);
 #pragma unroll
       for (int j = 0; j < NS; ++j)
         if (j < mine_n) issue(j);
     }
-
-    // ---------------------------------------------------------------- this segment's queries
-    // Fragment A of step s: slots (2c, 2c + 1) hold d0, d0 + 2 and slots (2c + 8, 2c + 9) hold d0 + 1,
-    // d0 + 3, where d0 = dq(s): the order in which a key's four bytes come apart.
-    uint32_t qa[R][kSteps][4];
-    float rowmul[R][2], offs[R][2], m[R][2], l[R][2], r[R][2], hs[R][2];
-    int beg[R][2], end[R][2];
-    int full_lo = 0, full_hi = 0x7fffffff;   // tokens that every row sees
+    float mul_r[kMine], of_r[kMine];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < kMine; ++i) {
+      if (L::kQShared && warp >= NT) break;
+      const uint4 (&raw)[D / 32] = rows_raw[i];
+      float amax = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = i * 16 + e * 8 + g;
-        const bool live = row < rows_left;
-        const int ri = tile * L::kRows + (live ? row : 0);
-        const int tok = ri / p.group, head = h * p.group + ri % p.group;
-        const uint16_t* const src = p.q + (x.s.row0 + tok) * p.q_stride + head * D;
-        uint4 raw[D / 32];
+      for (int w = 0; w < D / 32; ++w) {
+        float f[8];
+        unpack8<kF16>(raw[w], f);
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          // D <= 128: D / 4 contiguous values a lane; D = 256: 32 of each half.
-          const int d = D == 256 ? 128 * (w >> 2) + 32 * c + 8 * (w & 3) : (D / 4) * c + 8 * w;
-          raw[w] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+      }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 13, -100);
+      const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        float f[8];
+        unpack8<kF16>(raw[w], f);
+        __half hf[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          hf[k] = __float2half_rn(f[k] * down);
+          sum += __half2float(hf[k]);
         }
-        float amax = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          float f[8];
-          unpack8<kF16>(raw[w], f);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 13, -100);
-        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          float f[8];
-          unpack8<kF16>(raw[w], f);
-          __half hf[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            hf[k] = __float2half_rn(f[k] * down);
-            sum += __half2float(hf[k]);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const __half2 lo = __halves2half2(hf[4 * k], hf[4 * k + 2]), hi = __halves2half2(hf[4 * k + 1], hf[4 * k + 3]);
-            qa[i][2 * w + k][e] = *reinterpret_cast<const uint32_t*>(&lo);
-            qa[i][2 * w + k][2 + e] = *reinterpret_cast<const uint32_t*>(&hi);
+        for (int k = 0; k < 2; ++k) {
+          const __half2 lo = __halves2half2(hf[4 * k], hf[4 * k + 2]), hi = __halves2half2(hf[4 * k + 1], hf[4 * k + 3]);
+          const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&lo), b1 = *reinterpret_cast<const uint32_t*>(&hi);
+          if (L::kQShared) {
+            qsm[(warp * kSteps + 2 * w + k) * 32 + lane] = make_uint2(b0, b1);
+          } else {
+            qb[L::kQShared ? 0 : i][2 * w + k][0] = b0;
+            qb[L::kQShared ? 0 : i][2 * w + k][1] = b1;
           }
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        offs[i][e] = sum * (128.f / 16777216.f);
-        // score (in powers of two) = (acc - offs) * 2^24 * k_scale * scale * log2 e * 2^ex
-        rowmul[i][e] = p.scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 + ex) << 23);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      // score (in powers of two) = (acc - offs) * rowmul * k_scale
+      of_r[i] = sum * (128.f / 16777216.f);
+      mul_r[i] = p.scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 + ex) << 23);
+      if (L::kQShared && c == 0) qstat_sm[(L::kQShared ? warp * 8 : 0) + g] = make_float2(mul_r[i], of_r[i]);
+    }
+    if (L::kQShared) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {   // this lane's scores are of rows 2c and 2c + 1
+        if (L::kQShared) {
+          const float2 t = qstat_sm[L::kQShared ? i * 8 + 2 * c + e : 0];
+          rowmul[i][e] = t.x;
+          offs[i][e] = t.y;
+        } else {
+          rowmul[i][e] = __shfl_sync(0xffffffffu, mul_r[L::kQShared ? 0 : i], 4 * (2 * c + e));
+          offs[i][e] = __shfl_sync(0xffffffffu, of_r[L::kQShared ? 0 : i], 4 * (2 * c + e));
+        }
         m[i][e] = kFloor;
         r[i][e] = kFloor;
         l[i][e] = 0.f;
         hs[i][e] = 0.f;
-        const int pos = x.s.len - x.s.n + tok;
-        end[i][e] = !live ? 0x7fffffff : p.causal ? pos + 1 : x.s.len;
+        const int row = i * 8 + 2 * c + e;
+        const bool live = row < rows_left;
+        const int pos = x.s.len - x.s.n + (tile * L::kRows + row) / p.group;
+        end[i][e] = !live ? 0x7fffffff : p.causal ? min(pos + 1, x.s.len) : x.s.len;
         beg[i][e] = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
-        full_hi = min(full_hi, live ? min(end[i][e], x.s.len) : 0x7fffffff);
+        full_hi = min(full_hi, end[i][e]);
         full_lo = max(full_lo, beg[i][e]);
       }
     }
     full_hi = __reduce_min_sync(0xffffffffu, full_hi);
     full_lo = __reduce_max_sync(0xffffffffu, full_lo);
-    float o[R][kCols][4];
+    float o[NT][kSteps][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int n = 0; n < kCols; ++n)
+      for (int n = 0; n < kSteps; ++n)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
 
@@ -367,12 +444,14 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
       const float vs = __shfl_sync(0xffffffffu, par ? vs_r[1] : vs_r[0], j & 31);
       const bool bad = ((par ? bad_r[1] : bad_r[0]) >> (j & 31)) & 1u;
 
-      // Scores of tokens T + 8 t + 2 c (+ 1), rows g and g + 8.
-      float s[R][2][4];
+      // Scores of tokens T + g and T + g + 8, rows 2c and 2c + 1 of each tile: two chains of products
+      // where one tile alone would wait for each of its own.
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float s[NT][kChains][4];
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+      for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < kChains; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[i][t][k] = 0.f;
 #pragma unroll
@@ -386,49 +465,51 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          const uint32_t w0 = k == 0 ? kb[0].x : k == 1 ? kb[0].y : k == 2 ? kb[0].z : kb[0].w;
+          const uint32_t w1 = k == 0 ? kb[1].x : k == 1 ? kb[1].y : k == 2 ? kb[1].z : kb[1].w;
+          const uint32_t a0 = w0 & 0x00FF00FFu, a1 = w1 & 0x00FF00FFu;
+          const uint32_t a2 = __byte_perm(w0, 0u, 0x4341), a3 = __byte_perm(w1, 0u, 0x4341);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t word = k == 0 ? kb[t].x : k == 1 ? kb[t].y : k == 2 ? kb[t].z : kb[t].w;
-            const uint32_t b0 = word & 0x00FF00FFu, b1 = __byte_perm(word, 0u, 0x4341);
-#pragma unroll
-            for (int i = 0; i < R; ++i) {
-              const uint32_t* a = qa[i][4 * w + k];
-              mma_f16_16816(s[i][t], a[0], a[1], a[2], a[3], b0, b1);
-            }
+          for (int i = 0; i < NT; ++i) {
+            uint2 q;
+            if (L::kQShared) q = qsm[(i * kSteps + 4 * w + k) * 32 + lane];
+            else q = make_uint2(qb[L::kQShared ? 0 : i][4 * w + k][0], qb[L::kQShared ? 0 : i][4 * w + k][1]);
+            mma_f16_16816(s[i][k % kChains], a0, a1, a2, a3, q.x, q.y);
           }
         }
       }
       const bool edge = T < full_lo || T + kGranule > full_hi || bad;
       const float lvs = lg2(vs);
-      uint32_t pa[R][4];
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float mx[2];
+      for (int i = 0; i < NT; ++i) {
+        float mx[2], z[4];   // z: scores in powers of two
+        bool move = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float c1 = ks * rowmul[i][e];
+          const float c0 = -offs[i][e] * c1;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) s[i][t][2 * e + k] = (s[i][t][2 * e + k] - offs[i][e]) * c1;
+          for (int t = 0; t < 2; ++t) {
+            float a = s[i][0][2 * t + e];
+            if (kChains == 2) a += s[i][kChains - 1][2 * t + e];
+            z[2 * t + e] = fmaf(a, c1, c0);
+          }
           if (edge) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int tok = T + 8 * t + 2 * c + k;
-                if (bad || tok < beg[i][e] || tok >= end[i][e] || tok >= x.s.len) s[i][t][2 * e + k] = -INFINITY;
-              }
+            for (int t = 0; t < 2; ++t) {
+              const int tok = T + 8 * t + g;
+              if (bad || tok < beg[i][e] || tok >= end[i][e]) z[2 * t + e] = -INFINITY;
+            }
           }
-          mx[e] = fmaxf(fmaxf(s[i][0][2 * e], s[i][0][2 * e + 1]), fmaxf(s[i][1][2 * e], s[i][1][2 * e + 1]));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 1));
-          mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 2));
+          mx[e] = fmaxf(z[e], z[2 + e]);
+          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kSlack;
         }
-        const bool move = mx[0] > m[i][0] + kSlack || mx[1] > m[i][1] + kSlack || mx[0] + lvs > r[i][0] + kSlack ||
-                          mx[1] + lvs > r[i][1] + kSlack;
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], w));
             if (mx[e] > m[i][e] + kSlack) {
               l[i][e] *= ex2(m[i][e] - mx[e]);
               m[i][e] = mx[e];
@@ -440,32 +521,32 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
             r[i][e] = rn;
             hs[i][e] = ex2(m[i][e] - rn);
 #pragma unroll
-            for (int n = 0; n < kCols; ++n) {
-              o[i][n][2 * e] *= a;
-              o[i][n][2 * e + 1] *= a;
+            for (int n = 0; n < kSteps; ++n) {
+              o[i][n][e] *= a;
+              o[i][n][2 + e] *= a;
             }
           }
         }
+        float w[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float f = hs[i][e] * vs;
-          float w[2][2];
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 2; ++t) {
+            const float pr = ex2(z[2 * t + e] - m[i][e]);
+            l[i][e] += pr;
+            w[2 * t + e] = pr * f;
+          }
+        }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float pr = ex2(s[i][t][2 * e + k] - m[i][e]);
-              l[i][e] += pr;
-              w[t][k] = pr * f;
-            }
-          const __half2 lo = __floats2half2_rn(w[0][0], w[0][1]), hi = __floats2half2_rn(w[1][0], w[1][1]);
-          pa[i][e] = *reinterpret_cast<const uint32_t*>(&lo);
-          pa[i][2 + e] = *reinterpret_cast<const uint32_t*>(&hi);
+        for (int t = 0; t < 2; ++t) {
+          const __half2 v = __floats2half2_rn(w[2 * t], w[2 * t + 1]);
+          pb[i][t] = transpose8(*reinterpret_cast<const uint32_t*>(&v));   // tokens 2c, 2c + 1 (+ 8 t) of row g
         }
       }
 
-      // Values: the lane takes 16 (8 for D = 64) contiguous d of tokens 2c, 2c + 1, 2c + 8, 2c + 9, so
-      // column n of tile q is d = 16 n + q (8 n + q): a lane's outputs are contiguous too.
+      // Values: the lane takes 16 (8 for D = 64) contiguous d of tokens 2c, 2c + 1, 2c + 8, 2c + 9; a
+      // matrix instruction's 16 rows are two of each lane's d, so its sums are contiguous too.
       constexpr int kWords = D == 64 ? 2 : 4;
 #pragma unroll
       for (int bx = 0; bx < L::kBoxes; ++bx) {
@@ -501,10 +582,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
             offset_bytes_to_half2_pairs(x23, bf[t][2], bf[t][3]);
           }
 #pragma unroll
-          for (int d = 0; d < 4; ++d)
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-              mma_f16_16816(o[i][bx * 4 * kWords + wd * 4 + d], pa[i][0], pa[i][1], pa[i][2], pa[i][3], bf[0][d], bf[1][d]);
+            for (int i = 0; i < NT; ++i)
+              mma_f16_16816(o[i][(bx * kWords + wd) * 2 + k], bf[0][2 * k], bf[0][2 * k + 1], bf[1][2 * k], bf[1][2 * k + 1], pb[i][0],
+                            pb[i][1]);
         }
       }
     }
@@ -512,134 +594,174 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
 
     // ---------------------------------------------------------------- join the warps, then the CTAs
     const bool whole = ub == 0 && ue == x.units;
-    const int slot = u == u0 ? 0 : 1;
+    const int slot = item_u0 <= u0 ? 0 : 1;   // the run's first segment, or its last
     float* const part = p.parts + ((size_t)blockIdx.x * 2 + slot) * L::kPart;
     float* const buf = reinterpret_cast<float*>(ring);
-    // The rings hold no copy in flight: every granule issued has been waited for.
-    __syncthreads();
+    const int rows = min(rows_left, L::kRows);
+    __syncthreads();   // the rings hold no copy in flight: every granule issued has been waited for
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (i * 16 >= rows_left) break;
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float t = l[i][e];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        if (c == 0) {
-          mlr_sm[warp][8 * e + g][0] = m[i][e];
-          mlr_sm[warp][8 * e + g][1] = t;
-          mlr_sm[warp][8 * e + g][2] = r[i][e];
-        }
-        // A lane's sums of a row: D / 4 contiguous ones (D = 256: 32 of each half).
-        if (i * 16 + 8 * e + g < rows_left) {
-          float* const dst = buf + (warp * 16 + 8 * e + g) * L::kRow;
-          constexpr int kHalf = D == 64 ? 8 : 16;
 #pragma unroll
-          for (int n = 0; n < kCols; n += 4) {
-            const int base = (n / kHalf) * 128 + 2 * kHalf * c + (n % kHalf);
+        for (int w = 4; w < 32; w <<= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+        const int row = 8 * i + 2 * c + e;
+        if (g == 0) mlr_sm[warp][row] = make_float4(m[i][e], t, r[i][e], 0.f);
+        if (row < rows) {
+          // A lane's sums of a row: D / 8 contiguous ones (D = 256: 16 of each half).
+          float* const dst = buf + (warp * L::kRows + row) * L::kRow;
+          constexpr int kTiles = D == 64 ? 4 : 8;   // output tiles of a box
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-              *reinterpret_cast<float4*>(dst + base + y * kHalf) =
-                  make_float4(o[i][n][2 * e + y], o[i][n + 1][2 * e + y], o[i][n + 2][2 * e + y], o[i][n + 3][2 * e + y]);
-          }
+          for (int n = 0; n < kSteps; n += 2)
+            *reinterpret_cast<float4*>(dst + (n / kTiles) * 128 + 2 * kTiles * g + 2 * (n % kTiles)) =
+                make_float4(o[i][n][e], o[i][n][2 + e], o[i][n + 1][e], o[i][n + 1][2 + e]);
         }
       }
-      __syncthreads();
-      constexpr int kVec = D / 8;   // threads of a row, eight values each
-      for (int row = threadIdx.x / kVec; row < 16 && i * 16 + row < rows_left; row += kThreads / kVec) {
-        const int d = 8 * (threadIdx.x % kVec);
-        float M = kFloor, Rf = kFloor;
+    }
+    __syncthreads();
+    constexpr int kVec = D / 4;   // threads of a row, four values each
+    for (int i = threadIdx.x; i < rows * kVec; i += kThreads) {
+      const int row = i / kVec, d = 4 * (i % kVec);
+      float M = kFloor, Rf = kFloor;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          M = fmaxf(M, mlr_sm[w][row][0]);
-          Rf = fmaxf(Rf, mlr_sm[w][row][2]);
-        }
-        float lt = 0.f, acc[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          lt += mlr_sm[w][row][1] * ex2(mlr_sm[w][row][0] - M);
-          const float a = ex2(mlr_sm[w][row][2] - Rf);
-          const float4 v0 = *reinterpret_cast<const float4*>(buf + (w * 16 + row) * L::kRow + d);
-          const float4 v1 = *reinterpret_cast<const float4*>(buf + (w * 16 + row) * L::kRow + d + 4);
-          const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], a, acc[k]);
-        }
-        if (whole) {
-          const int ri = tile * L::kRows + i * 16 + row;
-          const int orow = x.s.row0 + ri / p.group, head = h * p.group + ri % p.group;
-          const float z = lt == 0.f ? 0.f : __fdividef(1.f, lt) * ex2(Rf - M);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] *= z;
-          *reinterpret_cast<uint4*>(p.out + orow * p.out_stride + head * D + d) = pack8<kF16>(acc);
-          if (p.lse && d == 0)
-            p.lse[(size_t)orow * p.q_heads + head] = lt == 0.f ? -INFINITY : (M + lg2(lt)) * 0.69314718056f;
-        } else {
-          float4* const dst = reinterpret_cast<float4*>(part + (i * 16 + row) * D + d);
-          dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-          if (d == 0) *reinterpret_cast<float4*>(part + L::kRows * D + (i * 16 + row) * 4) = make_float4(M, lt, Rf, 0.f);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, mlr_sm[w][row].x);
+        Rf = fmaxf(Rf, mlr_sm[w][row].z);
       }
-      if (i + 1 < R) __syncthreads();
+      float lt = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        lt += mlr_sm[w][row].y * ex2(mlr_sm[w][row].x - M);
+        const float a = ex2(mlr_sm[w][row].z - Rf);
+        const float4 v = *reinterpret_cast<const float4*>(buf + (w * L::kRows + row) * L::kRow + d);
+        acc.x = fmaf(v.x, a, acc.x), acc.y = fmaf(v.y, a, acc.y), acc.z = fmaf(v.z, a, acc.z), acc.w = fmaf(v.w, a, acc.w);
+      }
+      if (whole) {
+        store_row<kF16>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc, M, lt, Rf);
+      } else {
+        *reinterpret_cast<float4*>(part + row * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float4*>(part + L::kRows * D + row * 4) = make_float4(M, lt, Rf, 0.f);
+      }
     }
     if (!whole) {
       // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.
-      const int first = runs.owner(item_u0), last = runs.owner(item_u0 + x.units - 1);
-      __threadfence();
+      const int first = runs.owner(item_u0 + L::kLead), n = runs.owner(item_u0 + x.span - 1) - first + 1;
+      // (The barrier orders the CTA's stores before thread 0's release, and its acquire before the reads.)
       __syncthreads();
       if (threadIdx.x == 0) {
-        const uint32_t n = (uint32_t)(last - first + 1);
         const uint32_t old = atom_add_acq_rel_u32(p.counters + first, 1u);
-        if (old >= n) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
-        if (old == n - 1) p.counters[first] = 0u;   // ready for the next call
-        last_sm = old == n - 1;
+        if (old >= (uint32_t)n) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
+        if (old == (uint32_t)n - 1) p.counters[first] = 0u;   // ready for the next call
+        last_sm = old == (uint32_t)n - 1;
       }
       __syncthreads();
       if (last_sm) {
-        __threadfence();
-        constexpr int kVec = D / 8;
-        const int rows = min(rows_left, L::kRows);
-        // The first CTA's part is its last segment unless the item begins its run.
-        const int first_slot = runs.begin(first) == item_u0 ? 0 : 1;
-        for (int row = threadIdx.x / kVec; row < rows; row += kThreads / kVec) {
-          const int d = 8 * (threadIdx.x % kVec);
-          float M = kFloor, Rf = kFloor;
-          for (int i = first; i <= last; ++i) {
-            const float* src = p.parts + ((size_t)i * 2 + (i == first ? first_slot : 0)) * L::kPart;
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(src + L::kRows * D + row * 4));
-            M = fmaxf(M, t.x);
-            Rf = fmaxf(Rf, t.z);
+        const int first_slot = item_u0 <= runs.begin(first) ? 0 : 1;
+        const float* const parts = p.parts + ((size_t)first * 2 + first_slot) * L::kPart;   // part i > 0: CTA first + i, slot 0
+        auto part_of = [&](int i) { return i == 0 ? parts : p.parts + (size_t)(first + i) * 2 * L::kPart; };
+        // As many rows at a time as have their statistics in shared memory: (m, l, r) of each part, then
+        // in their place the factor of its sums.
+        float4* const st = reinterpret_cast<float4*>(ring);
+        constexpr int kRoom = (L::kRing - kThreads * 16) / 16;
+        float4* const half = st + kRoom;   // [kThreads] sums to be added
+        __shared__ float4 row_sm[L::kRows];
+        const int chunk = min(rows, kRoom / n);
+        for (int r0 = 0; r0 < rows; r0 += chunk) {
+          const int nr = min(chunk, rows - r0);
+          for (int i = threadIdx.x; i < n * nr; i += kThreads) {
+            const int pi = i / nr, row = i - pi * nr;
+            st[row * n + pi] = __ldcg(reinterpret_cast<const float4*>(part_of(pi) + L::kRows * D) + r0 + row);
           }
-          float lt = 0.f, acc[8];
+          __syncthreads();
+          // Few parts: a thread for a row; many: a warp for a row.
+          const bool few = n <= 16;
+          for (int row = few ? threadIdx.x : warp; row < nr; row += few ? kThreads : kWarps) {
+            float M = kFloor, Rf = kFloor, lt = 0.f;
+            const int i0 = few ? 0 : lane, di = few ? 1 : 32;
+            for (int i = i0; i < n; i += di) {
+              M = fmaxf(M, st[row * n + i].x);
+              Rf = fmaxf(Rf, st[row * n + i].z);
+            }
+            if (!few) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = 0.f;
-#pragma unroll 4
-          for (int i = first; i <= last; ++i) {
-            const float* src = p.parts + ((size_t)i * 2 + (i == first ? first_slot : 0)) * L::kPart;
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(src + L::kRows * D + row * 4));
-            const float4 v0 = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
-            const float4 v1 = __ldcg(reinterpret_cast<const float4*>(src + row * D + d + 4));
-            lt += t.y * ex2(t.x - M);
-            const float a = ex2(t.z - Rf);
-            const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+              for (int w = 16; w > 0; w >>= 1) {
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+                Rf = fmaxf(Rf, __shfl_xor_sync(0xffffffffu, Rf, w));
+              }
+            }
+            for (int i = i0; i < n; i += di) {
+              const float4 t = st[row * n + i];
+              lt += t.y * ex2(t.x - M);
+              st[row * n + i].x = ex2(t.z - Rf);
+            }
+            if (!few) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], a, acc[k]);
+              for (int w = 16; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
+            }
+            if (few || lane == 0) row_sm[row] = make_float4(M, lt, Rf, 0.f);
           }
-          const int ri = tile * L::kRows + row;
-          const int orow = x.s.row0 + ri / p.group, head = h * p.group + ri % p.group;
-          const float z = lt == 0.f ? 0.f : __fdividef(1.f, lt) * ex2(Rf - M);
+          __syncthreads();
+          // Threads take four values at each of kPlaces places; where the rows leave threads over, they
+          // share the parts.  Eight loads or more of a thread are in flight.
+          constexpr int kPlaces = (L::kRows * (D / 4) + kThreads - 1) / kThreads;
+          constexpr int kAhead = kPlaces >= 8 ? 1 : 8 / kPlaces;
+          const int places = nr * (D / 4);
+          const int share = places < kThreads ? kThreads / places : 1;
+          const int k = share > 1 ? (int)threadIdx.x / places : 0;
+          const int at0 = share > 1 ? (int)threadIdx.x - k * places : (int)threadIdx.x;
+          const int i1 = k < share ? n * (k + 1) / share : 0;
+          float4 acc[kPlaces];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] *= z;
-          *reinterpret_cast<uint4*>(p.out + orow * p.out_stride + head * D + d) = pack8<kF16>(acc);
-          if (p.lse && d == 0)
-            p.lse[(size_t)orow * p.q_heads + head] = lt == 0.f ? -INFINITY : (M + lg2(lt)) * 0.69314718056f;
+          for (int y = 0; y < kPlaces; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = n * k / share; i < i1; i += kAhead) {
+            float4 v[kAhead][kPlaces];
+#pragma unroll
+            for (int z = 0; z < kAhead; ++z)
+#pragma unroll
+              for (int y = 0; y < kPlaces; ++y) {
+                const int at = at0 + y * kThreads;
+                v[z][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i + z < i1 && at < places) v[z][y] = __ldcg(reinterpret_cast<const float4*>(part_of(i + z) + r0 * D) + at);
+              }
+#pragma unroll
+            for (int z = 0; z < kAhead; ++z)
+#pragma unroll
+              for (int y = 0; y < kPlaces; ++y) {
+                const int at = at0 + y * kThreads;
+                if (i + z < i1 && at < places) {
+                  const float a = st[(at / (D / 4)) * n + i + z].x;
+                  acc[y].x = fmaf(v[z][y].x, a, acc[y].x), acc[y].y = fmaf(v[z][y].y, a, acc[y].y);
+                  acc[y].z = fmaf(v[z][y].z, a, acc[y].z), acc[y].w = fmaf(v[z][y].w, a, acc[y].w);
+                }
+              }
+          }
+          if (share > 1) {
+            half[threadIdx.x] = acc[0];
+            __syncthreads();
+            if (k == 0) {
+              for (int y = 1; y < share; ++y) {
+                const float4 v = half[y * places + at0];
+                acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+              }
+            }
+          }
+          if (k == 0) {
+#pragma unroll
+            for (int y = 0; y < kPlaces; ++y) {
+              const int at = at0 + y * kThreads;
+              if (at < places) {
+                const int row = at / (D / 4);
+                const float4 t = row_sm[row];
+                store_row<kF16>(p, x.s.row0, tile * L::kRows + r0 + row, h, 4 * (at % (D / 4)), D, acc[y], t.x, t.y, t.z);
+              }
+            }
+          }
+          __syncthreads();
         }
       }
     }
-    u = item_u0 + ue;
     if (u < u1) {
       // The join buffer lies over the rings: plain accesses to it come before the next copies.
       fence_async_shared();
@@ -648,19 +770,19 @@ __global__ void __launch_bounds__(kThreads, Layout<D, R>::kCtas) kv8_attention_k
   }
 }
 
-template <bool kF16, int D, int R>
+template <bool kF16, int D, int NT>
 static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
-  // No more CTAs than units there can be (lengths are known to the device alone).
-  using L = Layout<D, R>;
-  auto kern = kv8_attention_kernel<kF16, D, R>;
+  using L = Layout<D, NT>;
+  auto kern = kv8_attention_kernel<kF16, D, NT>;
   cudaError_t e = ensure_smem_attribute((const void*)kern, L::kSmem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
+  // No more CTAs than units there can be (lengths are known to the device alone).
   const long long tiles = ((long long)p.step.max_tokens * p.group + L::kRows - 1) / L::kRows;
-  const long long units = (((long long)p.step.table_width << p.page_shift) + kUnit - 1) / kUnit;
+  const long long units = (((long long)p.step.table_width << p.page_shift) + L::kUnit - 1) / L::kUnit;
   const long long most = tiles * units >= sms * L::kCtas ? sms * L::kCtas : tiles * units * p.step.seqs * p.kv_heads;
+  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(most < sms * L::kCtas ? most : sms * L::kCtas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(L::kThreads);
   cfg.dynamicSmemBytes = (size_t)L::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -672,14 +794,27 @@ static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Bytes of the parts of every variant of a head size.
-template <int D, int R>
-static size_t parts_bytes(int sms) {
-  using L = Layout<D, R>;
-  return (size_t)sms * L::kCtas * 2 * L::kPart * sizeof(float);
+// The narrowest variant that holds a sequence's rows in one tile, else the widest.
+template <bool kF16>
+static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
+  const long long rows = (long long)p.step.max_tokens * p.group;
+  if (head_dim == 64)
+    return rows <= 8 ? launch_few<kF16, 64, 1>(p, sms, s) : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s) : launch_few<kF16, 64, 4>(p, sms, s);
+  if (head_dim == 128)
+    return rows <= 8    ? launch_few<kF16, 128, 1>(p, sms, s)
+           : rows <= 16 ? launch_few<kF16, 128, 2>(p, sms, s)
+           : rows <= 24 ? launch_few<kF16, 128, 3>(p, sms, s)
+                        : launch_few<kF16, 128, 4>(p, sms, s);
+  return rows <= 8 ? launch_few<kF16, 256, 1>(p, sms, s) : launch_few<kF16, 256, 2>(p, sms, s);
 }
 
-constexpr size_t counters_bytes(int sms) { return ((size_t)sms * 3 * sizeof(uint32_t) + 255) / 256 * 256; }
+// Two parts of the widest variant's rows for each CTA.
+static size_t parts_bytes(int head_dim, int sms) {
+  const int part = head_dim == 64 ? Layout<64, 4>::kPart : head_dim == 128 ? Layout<128, 4>::kPart : Layout<256, 2>::kPart;
+  return (size_t)sms * 2 * 2 * part * sizeof(float);
+}
+
+constexpr size_t counters_bytes(int sms) { return ((size_t)sms * 2 * sizeof(uint32_t) + 255) / 256 * 256; }
 
 }  // namespace attn
 }  // namespace w8a8
@@ -689,12 +824,7 @@ using namespace w8a8;
 extern "C" size_t kv8_workspace_bytes(int q_heads, int kv_heads, int head_dim) {
   if (kv8_check_dims(kv_heads, head_dim) != W8A8_OK || q_heads < 0 || q_heads > 4096) return 0;
   const int sms = device_sm_count();
-  size_t parts = 0;
-  auto add = [&](size_t n) { parts = n > parts ? n : parts; };
-  if (head_dim == 64) add(attn::parts_bytes<64, 1>(sms)), add(attn::parts_bytes<64, 2>(sms));
-  else if (head_dim == 128) add(attn::parts_bytes<128, 1>(sms)), add(attn::parts_bytes<128, 2>(sms));
-  else add(attn::parts_bytes<256, 1>(sms));
-  return kWsHeaderBytes + attn::counters_bytes(sms) + parts;
+  return kWsHeaderBytes + attn::counters_bytes(sms) + attn::parts_bytes(head_dim, sms);
 }
 
 extern "C" int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride, int q_heads,
@@ -743,13 +873,7 @@ extern "C" int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, c
   p.status = reinterpret_cast<uint32_t*>(w);
   p.counters = reinterpret_cast<uint32_t*>(w + kWsHeaderBytes);
   p.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + attn::counters_bytes(sms));
-  const bool f16 = dtype == KV8_F16;
-  const bool few = (long long)step->max_tokens * p.group <= 16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-#define KV8_FEW(D, R) (f16 ? attn::launch_few<true, D, R>(p, sms, s) : attn::launch_few<false, D, R>(p, sms, s))
-  if (D == 64) e = few ? KV8_FEW(64, 1) : KV8_FEW(64, 2);
-  else if (D == 128) e = few ? KV8_FEW(128, 1) : KV8_FEW(128, 2);
-  else e = KV8_FEW(256, 1);
-#undef KV8_FEW
+  e = dtype == KV8_F16 ? attn::launch_rows<true>(p, D, sms, s) : attn::launch_rows<false>(p, D, sms, s);
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention");
 }
