@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libw8a8_gb300.so")
 SOURCES = ["api.cu", "w8a8_gemm.cu", "w8a8_gemm_tc.cu", "q8_0_gemv.cu", "no_alloc.cu", "read_probe.cu", "quantize.cu",
-           "kv8_append.cu", "kv8_attention.cu"]
+           "kv8_append.cu", "kv8_attention.cu", "kv8_attention_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-Xptxas", "-v"]
 

@@ -38,20 +38,10 @@
 // granule for each warp, into equal runs, one for each CTA: lengths live on the device, so each CTA
 // finds its run from a scan of kv_len.  An item cut across CTAs is finished by the last of them to
 // arrive.  Two CTAs share an SM, so that one's start, join and drain hide behind the other's stream.
-#include <cuda.h>
-#include <cuda_runtime.h>
-
-#include "internal.h"
-#include "kv8.cuh"
-#include "kv8.h"
+#include "kv8_attention.cuh"
 
 namespace w8a8 {
 namespace attn {
-
-constexpr int kGranule = 16;         // tokens of a warp's step
-constexpr float kFloor = -3.0e38f;   // reference of a row that has seen nothing
-constexpr float kSlack = 8.f;        // a reference moves when it is passed by this much (powers of two)
-constexpr float kSpan = 120.f;       // largest distance of the two references
 
 // NT: 8-row tiles a warp holds.  A lane holds D NT / 4 sums, so the warps that an SM can hold follow
 // from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in two CTAs.
@@ -75,7 +65,7 @@ struct Layout {
   static constexpr int kRow = D + 4;                    // floats of a row in the join buffer
   // What an item costs beside its tokens (queries, first copies, join), in units: each item's place in
   // the split is that much longer, so a run that crosses into another item gets fewer tokens.
-  static constexpr int kLead = 2;
+  static constexpr int kLead = 3;
   // A part of a split item in the workspace: kRows x D sums, then (m, l, r, -) of each row.
   static constexpr int kPart = kRows * (D + 4);
   static_assert(kWarps * kRows * kRow * 4 <= kRing, "the join buffer lies over the rings");
@@ -83,74 +73,12 @@ struct Layout {
   static_assert(kCtas * (kSmem + 4096) <= 232448, "shared memory of an SM");
 };
 
-struct Params {
-  CUtensorMap kmap, vmap;   // the cache as rows of D bytes, boxes of 16 rows
-  Kv8Step step;
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;
-  long long q_stride, out_stride;
-  const float* ks;
-  const float* vs;
-  int pages, page_shift, q_heads, kv_heads, group, window, causal;
-  float scale_log2;        // scale * log2 e
-  uint32_t* status;
-  uint32_t* counters;      // [CTA] arrivals at the item that crosses the end of its run, zero between calls
-  float* parts;            // [CTA][2] parts of split items
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Transpose of an 8 x 8 matrix of 16-bit values held as two of row lane / 4 by each lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t t;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
   return t;
 }
-
-// a / b for a >= 0, b > 0: a 64-bit division is a long subroutine, and hardly ever needed.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// What the rows of a sequence cover: items of `tiles` row tiles and kv heads, each of `units` units
-// from token `lo` (a granule's start) to `hi`; `span` = the lead and the units, its length in the split.
-struct Span {
-  Seq s;
-  int tiles, units, span, lo, hi;
-};
-
-template <typename L>
-__device__ __forceinline__ Span load_span(const Params& p, int b) {
-  Span x;
-  load_seq(p.step, b, 1 << p.page_shift, false, p.status, x.s);
-  x.tiles = (int)quotient((long long)x.s.n * p.group + L::kRows - 1, L::kRows);
-  x.hi = x.s.len;
-  x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : 0;
-  x.units = max(1, (x.hi - x.lo + L::kUnit - 1) / L::kUnit);   // one that sees nothing still writes its rows
-  x.span = L::kLead + x.units;
-  return x;
-}
-
-// The equal runs: U units over `ctas`, the first U % ctas one longer.
-struct Runs {
-  long long a, r;
-  __device__ Runs(long long U, int ctas) : a(quotient(U, ctas)), r(U - a * ctas) {}
-  __device__ long long begin(int i) const { return i * a + (i < r ? i : r); }
-  __device__ int owner(long long u) const {
-    const long long head = r * (a + 1);
-    return (int)(u < head ? quotient(u, a + 1) : r + quotient(u - head, a));
-  }
-};
 
 // Four output values at d of one joined query row, and with the first of them the row's lse.
 template <bool kF16>
@@ -483,8 +411,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       uint32_t pb[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
-        float mx[2], z[4];   // z: scores in powers of two
-        bool move = false;
+        float mx[2], f[2], z[4];   // z: scores in powers of two
+        bool move = false, far = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float c1 = ks * rowmul[i][e];
@@ -503,7 +431,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             }
           }
           mx[e] = fmaxf(z[e], z[2 + e]);
-          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kSlack;
+          f[e] = hs[i][e] * vs;
+          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kSlack || f[e] > kFar;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -520,22 +449,24 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             const float a = ex2(r[i][e] - rn);
             r[i][e] = rn;
             hs[i][e] = ex2(m[i][e] - rn);
+            f[e] = hs[i][e] * vs;
 #pragma unroll
             for (int n = 0; n < kSteps; ++n) {
               o[i][n][e] *= a;
               o[i][n][2 + e] *= a;
             }
           }
+          far = __any_sync(0xffffffffu, f[0] > kFar || f[1] > kFar);
         }
         float w[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = hs[i][e] * vs;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const float pr = ex2(z[2 * t + e] - m[i][e]);
             l[i][e] += pr;
-            w[2 * t + e] = pr * f;
+            w[2 * t + e] = pr * f[e];
+            if (far && f[e] > kFar) w[2 * t + e] = ex2(z[2 * t + e] + lvs - r[i][e]);
           }
         }
 #pragma unroll
@@ -794,10 +725,14 @@ static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Rows of a sequence and kv head up to which this file's kernel runs.
+constexpr long long kFewRows = 32;
+
 // The narrowest variant that holds a sequence's rows in one tile, else the widest.
 template <bool kF16>
 static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
   const long long rows = (long long)p.step.max_tokens * p.group;
+  if (head_dim <= 128 && rows > kFewRows) return launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
     return rows <= 8 ? launch_few<kF16, 64, 1>(p, sms, s) : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s) : launch_few<kF16, 64, 4>(p, sms, s);
   if (head_dim == 128)
@@ -811,7 +746,8 @@ static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStrea
 // Two parts of the widest variant's rows for each CTA.
 static size_t parts_bytes(int head_dim, int sms) {
   const int part = head_dim == 64 ? Layout<64, 4>::kPart : head_dim == 128 ? Layout<128, 4>::kPart : Layout<256, 2>::kPart;
-  return (size_t)sms * 2 * 2 * part * sizeof(float);
+  const size_t few = (size_t)sms * 2 * 2 * part * sizeof(float), many = many_parts_bytes(head_dim, sms);
+  return few > many ? few : many;
 }
 
 constexpr size_t counters_bytes(int sms) { return ((size_t)sms * 2 * sizeof(uint32_t) + 255) / 256 * 256; }

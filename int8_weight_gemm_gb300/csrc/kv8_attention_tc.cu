@@ -1,0 +1,839 @@
+// Attention over the 8-bit paged key-value cache: many query rows (prompts, long verify windows), on the
+// fifth-generation tensor cores (tcgen05, sm_103a).  The operator is that of kv8_attention.cu.
+//
+// What bounds it: a cached byte feeds 2 (rows that share its head) multiply-adds, so from some 300 rows
+// on the products do: a block of 128 tokens against 128 rows is 2 x 128 x 128 x D multiply-adds, 1024
+// tensor cycles at D = 128, beside 16384 exponentials.
+//
+// Mathematics.  A tile is 128 of the n * G rows that share a kv head, a block 128 cached tokens.
+//  S = Q K^T: both operands fp16 in shared memory (128-byte swizzle, K-major), fp32 accumulators in
+//  tensor memory.  A query row is scaled by a power of two into [2^13, 2^14) (exact); keys and values are
+//  the integers b - 128 (exact), their signs turned where a page's scale is negative.
+//  Weights: p = 2^(s - m) sums to l in fp32, w = p * (v_scale * 2^(m - r)), rounded to fp16, goes back into
+//  tensor memory over the scores it came from and is the first operand of O += W V.  The references m and r
+//  of a row are those of the other kernel, for the same reasons: they move when a score or weight passes
+//  them by 2^8, and only then is O (and the weights already written of that block) rescaled, once the
+//  products that add to O have completed.
+//
+// Layout and split.  One CTA an SM, all of its tensor memory: two streams of scores and outputs, each with
+// four softmax warps (a thread is a row).  With more than 128 rows the streams are two row tiles over the
+// same blocks; with up to 128 they are the even and the odd blocks of one tile, joined at the end, so that
+// one stream's exponentials always run under the other's products.  Further warps:
+//  - producer: page numbers and scales of four blocks in one load a lane, then a tensor-map box a granule
+//    into a ring of 8-bit blocks (keys and values in turn);
+//  - four converter warps: 8 bits -> fp16 operands, two blocks of each ahead of the products;
+//  - one thread issues the products: W V of a block, then, when those have completed (the other stream's
+//    are in the pipe meanwhile), the next scores into the same tensor memory.
+// The work is cut like that of the other kernel: items (row tile, kv head) laid end to end in units of a
+// block and cut into equal runs; an item cut across CTAs is finished by the last to arrive, parts joined
+// in the CTAs' order, so replays give the same bits.
+#include "kv8_attention.cuh"
+
+namespace w8a8 {
+namespace attn {
+
+constexpr int kBlock = 128;       // tokens of a block
+constexpr int kTileRows = 128;    // rows of a tile
+constexpr int kSoftWarps = 8;     // four for each stream
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kConvWarps = 4;
+constexpr int kProducerWarp = kSoftWarps + kConvWarps;
+constexpr int kMmaWarp = kProducerWarp + 1;
+constexpr int kTcThreads = 32 * (kMmaWarp + 1);
+constexpr int kGrans = kBlock / kGranule;   // granules of a block
+constexpr int kScales = 8;        // blocks whose scales are held
+
+template <int D, int kTiles>
+struct TcLayout {
+  static constexpr int kRows = kTiles * kTileRows;
+  static constexpr int kUnit = kBlock;
+  static constexpr int kLead = 3;
+  static constexpr int kQBytes = kTileRows * D * 2;
+  static constexpr int kBlk16 = kBlock * D * 2;       // an fp16 block
+  static constexpr int kSlot = kBlock * D;            // an 8-bit block
+  // 8-bit blocks in flight: with one tile the cache comes from HBM at the pace of the products.
+  static constexpr int kSlots = kTiles == 2 ? 2 : 4;
+  static constexpr int kBytes = 1024 + kTiles * kQBytes + 4 * kBlk16 + kSlots * kSlot;
+  static constexpr int kSCol = 0, kOCol = kBlock, kStreamCols = 256;   // tensor-memory columns of a stream
+  static constexpr int kPart = kRows * (D + 4);       // floats: sums, then (m, l, r, -) of each row
+  static_assert(kBytes + 2048 <= 232448, "shared memory");
+};
+
+// One tile's tokens.
+struct TileSpan {
+  int lo, hi, units;
+};
+
+template <typename L>
+__device__ __forceinline__ TileSpan tile_span(const Params& p, const Seq& s, int tile) {
+  TileSpan t;
+  const int first = (int)quotient((long long)tile * L::kRows, p.group);
+  const int last = min(s.n - 1, (int)quotient((long long)tile * L::kRows + L::kRows - 1, p.group));
+  t.hi = p.causal ? max(0, s.len - s.n + last + 1) : s.len;
+  t.lo = p.window > 0 ? max(0, s.len - s.n + first - p.window + 1) & ~(kGranule - 1) : 0;
+  t.units = max(1, (t.hi - t.lo + kBlock - 1) / kBlock);
+  return t;
+}
+
+template <typename L>
+__device__ __forceinline__ int tiles_of(const Params& p, const Seq& s) {
+  return (int)quotient((long long)s.n * p.group + L::kRows - 1, L::kRows);
+}
+
+// A run's segments, one item's part each.  Items are ordered by sequence, kv head, row tile.
+template <typename L>
+struct Walk {
+  long long u, u1, item_u0;
+  Seq s;
+  TileSpan t;
+  int b, h, tile, tiles, ub, ue;
+  // Set on the item (b, h, tile) that begins at item_u0 at or before u.
+  __device__ bool next(const Params& p) {
+    while (u < u1) {
+      while (u >= item_u0 + L::kLead + t.units) {
+        item_u0 += L::kLead + t.units;
+        if (++tile == tiles) {
+          tile = 0;
+          if (++h == p.kv_heads) {
+            h = 0;
+            do {
+              load_seq(p.step, ++b, 1 << p.page_shift, false, p.status, s);
+              tiles = tiles_of<L>(p, s);
+            } while (tiles == 0);
+          }
+        }
+        t = tile_span<L>(p, s, tile);
+      }
+      const int span = L::kLead + t.units;
+      ub = max((int)(u - item_u0) - L::kLead, 0);
+      ue = (int)min((long long)span, u1 - item_u0) - L::kLead;
+      u = item_u0 + L::kLead + ue;
+      if (ue > ub) return true;   // else the run ends within the lead
+    }
+    return false;
+  }
+  __device__ bool whole() const { return ub == 0 && ue == t.units; }
+};
+
+// 32 consecutive tensor-memory columns of this thread's lane (warp-wide); no wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Wait for this thread's loads; the registers of one of them are operands, so that nothing that uses them
+// is moved before it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]), "+r"(v[16]),
+                 "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]), "+r"(v[24]),
+                 "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+// D[tmem_d] (+)= A[desc_a] * B[desc_b]^T, both operands in shared memory.  Issued by one thread.
+__device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint64_t desc_a, uint64_t desc_b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(tmem_d),
+      "l"(desc_a), "l"(desc_b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptors with the 128-byte swizzle (rows of 128 bytes, atoms of 8 rows, 1024-byte
+// aligned; version 1 in bits 46..47, layout 2 in bits 61..63).  K-major: the rows are the operand's rows,
+// 64 of k each; atoms of rows 1024 bytes apart (stride field).
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+// MN-major: the rows are k, 64 of n each; atoms of 8 k are 1024 bytes apart (stride field), the next 64 of
+// n `lead` bytes (leading-dimension field).
+__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+         ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  const bool ok = mbar_wait(bar, parity, abort, status);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Granule scales of a block, as the softmax and converter warps use them.
+struct GranScale {
+  float ks, vs;    // magnitudes
+  float bias;      // of the scores: 0, or -inf where the granule is left out
+  uint32_t turn;   // fp16 factors of the keys (low half) and the values: 1 or -1
+};
+
+template <bool kF16, int D, int kTiles>
+__global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const __grid_constant__ Params p) {
+  using L = TcLayout<D, kTiles>;
+  constexpr int kSlots = L::kSlots;
+  constexpr int kHalfBytes = kBlock * 128;   // 64 fp16 of each of 128 rows
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t slot_full[kSlots], slot_empty[kSlots];   // 8-bit blocks
+  __shared__ __align__(8) uint64_t sc_full[kScales];                        // scales of a block
+  __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // fp16 blocks
+  __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_ready[2], pv_done[2];   // of each stream
+  __shared__ __align__(8) uint64_t join_bar, final_bar;
+  __shared__ __align__(16) GranScale scales[kScales][kGrans];
+  __shared__ long long scan_sm[kTcThreads / 32];
+  __shared__ struct {
+    Seq s;
+    int b;
+    long long u;
+  } start_sm;
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag, last_sm;
+
+  uint8_t* const qtile = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const k16 = qtile + kTiles * L::kQBytes;   // [2]
+  uint8_t* const v16 = k16 + 2 * L::kBlk16;           // [2]
+  uint8_t* const ring = v16 + 2 * L::kBlk16;          // [kSlots] 8-bit blocks
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) mbar_init(&slot_full[i], 1), mbar_init(&slot_empty[i], kConvWarps);
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) mbar_init(&sc_full[i], 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], kConvWarps), mbar_init(&v_full[i], kConvWarps);
+      mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
+      mbar_init(&q_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(&join_bar, kSoftWarps);
+    mbar_init(&final_bar, 1);
+    abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_desc(&p.kmap);
+    tma_prefetch_desc(&p.vmap);
+  }
+  if (warp == kMmaWarp) tmem_alloc(&tmem_base, 512);
+  tc_fence_before();
+  pdl_trigger();
+  pdl_wait();
+
+  // ---------------------------------------------------------------- this CTA's run of units
+  const int per = (p.step.seqs + kTcThreads - 1) / kTcThreads;   // sequences a thread scans
+  const int s0 = min(p.step.seqs, (int)threadIdx.x * per), s1 = min(p.step.seqs, s0 + per);
+  long long mine = 0;
+  auto seq_units = [&](int b, Seq& s) {
+    load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+    const int tiles = tiles_of<L>(p, s);
+    long long n = 0;
+    for (int t = 0; t < tiles; ++t) n += L::kLead + tile_span<L>(p, s, t).units;
+    return n * p.kv_heads;
+  };
+  for (int b = s0; b < s1; ++b) {
+    Seq s;
+    mine += seq_units(b, s);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scan_sm[warp] = incl;
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  long long before = incl - mine, U = 0;
+#pragma unroll
+  for (int w = 0; w < kTcThreads / 32; ++w) {
+    if (w < warp) before += scan_sm[w];
+    U += scan_sm[w];
+  }
+  const int ctas = (int)min((long long)gridDim.x, U);
+  const bool active = (int)blockIdx.x < ctas;
+  const Runs runs(U, max(ctas, 1));
+  const long long u0 = active ? runs.begin(blockIdx.x) : 0, u1 = active ? runs.begin(blockIdx.x + 1) : 0;
+  if (active && u0 >= before && u0 < before + mine) {
+    long long at = before;
+    for (int b = s0; b < s1; ++b) {
+      Seq s;
+      const long long n = seq_units(b, s);
+      if (u0 < at + n) {
+        start_sm.s = s;
+        start_sm.b = b;
+        start_sm.u = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+
+  Walk<L> wk;
+  wk.u = u0;
+  wk.u1 = u1;
+  if (active) {
+    wk.s = start_sm.s;
+    wk.b = start_sm.b;
+    wk.tiles = tiles_of<L>(p, wk.s);
+    long long head = 0;
+    for (int t = 0; t < wk.tiles; ++t) head += L::kLead + tile_span<L>(p, wk.s, t).units;
+    wk.h = (int)quotient(u0 - start_sm.u, head);
+    wk.item_u0 = start_sm.u + wk.h * head;
+    wk.tile = 0;
+    wk.t = tile_span<L>(p, wk.s, 0);
+  }
+
+  if (warp == kProducerWarp) {
+    // ---------------------------------------------------------------- producer
+    uint32_t blk = 0;   // blocks of the CTA before this segment
+    bool ok = true;
+    uint32_t copies = 0;   // slots filled
+    while (ok && wk.next(p)) {
+      const int nb = wk.ue - wk.ub;
+      const int T0 = wk.t.lo + wk.ub * kBlock, T1 = min(wk.t.hi, wk.t.lo + wk.ue * kBlock);
+      const int* const table = p.step.page_table + (size_t)wk.b * p.step.table_width;
+      for (int base = 0; ok && base < nb; base += 4) {
+        // Lane: granule lane % 8 of block base + lane / 8.
+        const int t = T0 + base * kBlock + lane * kGranule;
+        GranScale sc{0.f, 0.f, -INFINITY, 0x3C003C00u};
+        int row = 0;
+        bool live = t < T1;
+        if (live) {
+          const int page = __ldg(table + (t >> p.page_shift));
+          if (page < 0 || page >= p.pages) {
+            atomicOr(p.status, W8A8_DEV_BAD_INDEX);
+            live = false;
+          } else {
+            const size_t at = (size_t)page * p.kv_heads + wk.h;
+            row = (int)(at << p.page_shift) + (t & ((1 << p.page_shift) - 1));
+            const float ks = __ldg(p.ks + at), vs = __ldg(p.vs + at);
+            sc.ks = fabsf(ks);
+            sc.vs = fabsf(vs);
+            sc.bias = 0.f;
+            sc.turn = (ks < 0.f ? 0xBC00u : 0x3C00u) | ((vs < 0.f ? 0xBC00u : 0x3C00u) << 16);
+          }
+        }
+        const uint32_t lives = __ballot_sync(0xffffffffu, live);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (base + i >= nb) break;
+          const uint32_t n = blk + base + i;
+          const bool own = (lane >> 3) == i;
+          if (own) scales[n % kScales][lane & 7] = sc;
+          arrive_warp(&sc_full[n % kScales]);
+          const uint32_t bytes = (uint32_t)__popc((lives >> (8 * i)) & 0xFFu) * kGranule * D;
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
+            if (use > 0 && !wait_all(&slot_empty[slot], (use - 1) & 1u, &abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], bytes);
+            ++copies;
+            __syncwarp();
+            if (own && live)
+              tma_load_2d(ring + slot * L::kSlot + (lane & 7) * kGranule * D, side ? &p.vmap : &p.kmap, 0, row, &slot_full[slot]);
+          }
+          if (!ok) break;
+        }
+      }
+      blk += nb;
+    }
+    // Every copy issued must land before the CTA may exit.
+    if (lane == 0) {
+      for (uint32_t s = 0; s < kSlots && s < copies; ++s) mbar_wait_drain(&slot_full[s], ((copies - 1 - s) / kSlots) & 1u, p.status);
+    }
+  } else if (warp >= kSoftWarps && warp < kProducerWarp) {
+    // ---------------------------------------------------------------- converters
+    const int cw = warp - kSoftWarps;
+    uint32_t n = 0;   // block of the CTA
+    bool ok = true;
+    while (ok && wk.next(p)) {
+      for (int j = wk.ub; ok && j < wk.ue; ++j, ++n) {
+        if (!wait_all(&sc_full[n % kScales], (n / kScales) & 1u, &abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
+          const uint8_t* const src = ring + slot * L::kSlot;
+          uint8_t* const dst = (side ? v16 : k16) + (n & 1) * L::kBlk16;
+          if (!wait_all(&slot_full[slot], use & 1u, &abort_flag, p.status) ||
+              (n >= 2 && !wait_all(side ? &v_empty[n & 1] : &k_empty[n & 1], ((n >> 1) - 1) & 1u, &abort_flag, p.status))) {
+            ok = false;
+            break;
+          }
+          // A warp takes 32 tokens: eight rows by four 16-byte pieces at a time, so that neither the
+          // reads (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t turn = scales[n % kScales][2 * cw + (i >> 1)].turn;
+            const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
+            const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
+            const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
+            const int t = (4 * cw + i) * 8 + (lane & 7);
+#pragma unroll
+            for (int y = 0; y < D / 64; ++y) {
+              const int piece = (lane >> 3) + 4 * y;
+              const uint4 w = D == 64 ? *reinterpret_cast<const uint4*>(src + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4))
+                                      : *reinterpret_cast<const uint4*>(src + t * 128 + ((piece ^ (t & 7)) << 4));
+              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+              uint32_t out[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                // fp16 0x6400 | b = 1024 + b, so (1024 + b) sg - 1152 sg = sg (b - 128), exactly.
+                const uint32_t a = __byte_perm(in[k], 0x64646464u, 0x4140), c = __byte_perm(in[k], 0x64646464u, 0x4342);
+                const __half2 ha = __hfma2(*reinterpret_cast<const __half2*>(&a), sg, of);
+                const __half2 hc = __hfma2(*reinterpret_cast<const __half2*>(&c), sg, of);
+                out[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                out[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hc);
+              }
+              uint8_t* const row = dst + (piece >> 2) * kHalfBytes + t * 128;
+              const int ch = 2 * (piece & 3);
+              *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+            }
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&slot_empty[slot]);
+            mbar_arrive(side ? &v_full[n & 1] : &k_full[n & 1]);
+          }
+        }
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- issuer (one thread)
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
+      constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
+      uint32_t blk = 0, seg = 0, cnt[2] = {0u, 0u};   // products issued of each stream
+      bool ok = true;
+      while (ok && wk.next(p)) {
+        const int nb = wk.ue - wk.ub;
+        const int ns[2] = {kTiles == 2 ? nb : (nb + 1) / 2, kTiles == 2 ? nb : nb / 2};
+        auto block_of = [&](int s, int i) { return blk + (uint32_t)(kTiles == 2 ? i : 2 * i + s); };
+        auto scores = [&](int s, int i) {
+          const uint32_t n = block_of(s, i);
+          if (!mbar_wait(&k_full[n & 1], (n >> 1) & 1u, &abort_flag, p.status)) return false;
+          tc_fence_after();
+          const uint32_t qa = smem_addr(qtile + (kTiles == 2 ? s : 0) * L::kQBytes), ka = smem_addr(k16 + (n & 1) * L::kBlk16);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
+            umma_f16_ss(tmem + (uint32_t)(s * L::kStreamCols + L::kSCol), desc_kmajor(qa + off), desc_kmajor(ka + off), idesc_s, k > 0);
+          }
+          umma_commit(&s_full[s]);
+          if (kTiles == 1 || s == 1) umma_commit(&k_empty[n & 1]);
+          return true;
+        };
+        ok = mbar_wait(&q_full[0], seg & 1u, &abort_flag, p.status) &&
+             (kTiles == 1 || mbar_wait(&q_full[1], seg & 1u, &abort_flag, p.status));
+        ok = ok && scores(0, 0) && (ns[1] == 0 || scores(1, 0));
+        for (int i = 0; ok && i < ns[0]; ++i) {
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (!ok || i >= ns[s]) continue;
+            const uint32_t n = block_of(s, i);
+            ok = mbar_wait(&v_full[n & 1], (n >> 1) & 1u, &abort_flag, p.status) &&
+                 mbar_wait(&p_ready[s], cnt[s] & 1u, &abort_flag, p.status);
+            if (!ok) continue;
+            tc_fence_after();
+            const uint32_t va = smem_addr(v16 + (n & 1) * L::kBlk16);
+            const uint32_t t = tmem + (uint32_t)(s * L::kStreamCols);
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              umma_f16_tmem_a(t + L::kOCol, t + (uint32_t)(L::kSCol + 8 * k), desc_mnmajor(va + (uint32_t)(k * 16 * 128), kHalfBytes),
+                              idesc_o, i > 0 || k > 0);
+            umma_commit(&pv_done[s]);
+            if (kTiles == 1 || s == 1) umma_commit(&v_empty[n & 1]);
+            // The next scores take the tensor memory of the weights that these products read.
+            if (i + 1 < ns[s])
+              ok = mbar_wait(&pv_done[s], cnt[s] & 1u, &abort_flag, p.status) && scores(s, i + 1);
+            ++cnt[s];
+          }
+        }
+        blk += nb;
+        ++seg;
+      }
+      // Every product issued completes before tensor memory is freed.
+      umma_commit(&final_bar);
+      mbar_wait_drain(&final_bar, 0, p.status);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax warps
+    const int st = warp >> 2, quad = warp & 3;
+    const int row = 32 * quad + lane;                              // of the tile
+    const int irow = kTiles == 2 ? st * kTileRows + row : row;     // of the item
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(st * L::kStreamCols);
+    const uint32_t t_s = t_lane + L::kSCol, t_o = t_lane + L::kOCol;
+    uint32_t blk = 0, cnt = 0, join_phase = 0;
+    auto meet = [&]() {   // bounded meeting of the softmax warps
+      arrive_warp(&join_bar);
+      const bool ok = wait_all(&join_bar, join_phase, &abort_flag, p.status);
+      join_phase ^= 1u;
+      return ok;
+    };
+    bool ok = true;
+    while (ok && wk.next(p)) {
+      const int nb = wk.ue - wk.ub;
+      const int ns = kTiles == 2 ? nb : st == 0 ? (nb + 1) / 2 : nb / 2;
+      const int T0 = wk.t.lo + wk.ub * kBlock;
+      const int rows_left = wk.s.n * p.group - wk.tile * L::kRows;   // rows of the item that exist
+      const bool live = irow < rows_left;
+      const int ri = wk.tile * L::kRows + (live ? irow : 0);
+      const int tok = ri / p.group, head = wk.h * p.group + ri % p.group;
+      const bool warp_live = (kTiles == 2 ? st * kTileRows : 0) + 32 * quad < rows_left;
+
+      // ------------------------------------------------ queries: fp16, scaled by a power of two
+      float rowmul;
+      {
+        const uint4* const src = reinterpret_cast<const uint4*>(p.q + (wk.s.row0 + tok) * p.q_stride + head * D);
+        uint4 raw[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          float f[8];
+          unpack8<kF16>(raw[i], f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
+        }
+        const int ex = max((int)(__float_as_uint(amax) >> 23) - 127 - 13, -100);
+        const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+        rowmul = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
+        if (kTiles == 2 || st == 0) {
+          uint8_t* const dst = qtile + (kTiles == 2 ? st : 0) * L::kQBytes + row * 128;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            float f[8];
+            unpack8<kF16>(raw[i], f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] *= down;
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * kHalfBytes + (((i & 7) ^ (row & 7)) << 4)) = pack8<true>(f);
+          }
+          fence_async_shared();
+          arrive_warp(&q_full[kTiles == 2 ? st : 0]);
+        }
+      }
+      const int pos = wk.s.len - wk.s.n + tok;
+      const int end = !live ? 0x7fffffff : p.causal ? min(pos + 1, wk.s.len) : wk.s.len;
+      const int beg = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      const int full_hi = __reduce_min_sync(0xffffffffu, end), full_lo = __reduce_max_sync(0xffffffffu, beg);
+
+      // ------------------------------------------------ blocks
+      float m = kFloor, r = kFloor, hs = 0.f, l = 0.f;
+      for (int i = 0; ok && i < ns; ++i, ++cnt) {
+        const int j = kTiles == 2 ? i : 2 * i + st;
+        const uint32_t n = blk + (uint32_t)j;
+        const int T = T0 + j * kBlock;
+        if (!wait_all(&sc_full[n % kScales], (n / kScales) & 1u, &abort_flag, p.status) ||
+            !wait_all(&s_full[st], cnt & 1u, &abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        if (warp_live) {
+          tc_fence_after();
+          const bool edge = T < full_lo || T + kBlock > full_hi;
+          const GranScale* const sc = scales[n % kScales];
+          uint32_t buf[2][32];
+          tmem_ld32(t_s, buf[0]);
+#pragma unroll
+          for (int ch = 0; ch < kBlock / 32; ++ch) {
+            uint32_t (&a)[32] = buf[ch & 1];
+            tmem_wait_ld32(a);
+            if (ch + 1 < kBlock / 32) tmem_ld32(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
+            if (edge) {
+              // Scores that the row does not see.
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                const int t = T + 32 * ch + k;
+                if (t < beg || t >= end) a[k] = 0xFF800000u;
+              }
+            }
+            // Score a of granule y in powers of two: a * c1 + bias.
+            float c1[2], mx = -INFINITY, mw = -INFINITY, f[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              // (A factor of zero would make a hidden score's -inf a NaN.)
+              c1[y] = fmaxf(sc[2 * ch + y].ks * rowmul, 1e-37f);
+              float t = __uint_as_float(a[16 * y]);
+#pragma unroll
+              for (int k = 1; k < 16; ++k) t = fmaxf(t, __uint_as_float(a[16 * y + k]));
+              t = fmaf(t, c1[y], sc[2 * ch + y].bias);
+              mx = fmaxf(mx, t);
+              mw = fmaxf(mw, t + lg2(sc[2 * ch + y].vs));
+              f[y] = hs * sc[2 * ch + y].vs;
+            }
+            bool far = false;
+            if (__any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar)) {
+              // Some row's reference moves: its sums so far are rescaled, and with them the weights of
+              // this block that are already written.
+              if (mx > m + kSlack) {
+                l *= ex2(m - mx);
+                m = mx;
+              }
+              float rn = mw > r + kSlack ? mw : r;
+              rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
+              const float down = ex2(r - rn);
+              r = rn;
+              hs = ex2(m - rn);
+              f[0] = hs * sc[2 * ch].vs;
+              f[1] = hs * sc[2 * ch + 1].vs;
+              far = __any_sync(0xffffffffu, fmaxf(f[0], f[1]) > kFar);
+              if (ch + 1 < kBlock / 32) tmem_wait_ld32(buf[(ch + 1) & 1]);
+              if (i > 0) {
+                if (!wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(t_o + c0, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
+                  tmem_st16(t_o + c0, o);
+                }
+              }
+              tmem_wait_st();
+#pragma unroll
+              for (int c0 = 0; c0 < ch; ++c0) {
+                uint32_t o[16];
+                tmem_ld16(t_s + 16 * c0, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                  const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+                  o[k] = pack2<true>(w.x * down, w.y * down);
+                }
+                tmem_st16(t_s + 16 * c0, o);
+              }
+              tmem_wait_st();
+            }
+            uint32_t w16[16];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float c0 = sc[2 * ch + y].bias - m;
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float p0 = ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], c0));
+                const float p1 = ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], c0));
+                l += p0;
+                l += p1;
+                w16[8 * y + k / 2] = pack2<true>(p0 * f[y], p1 * f[y]);
+              }
+              if (far && f[y] > kFar) {
+                const float d0 = sc[2 * ch + y].bias + lg2(sc[2 * ch + y].vs) - r;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2)
+                  w16[8 * y + k / 2] = pack2<true>(ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], d0)),
+                                                   ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], d0)));
+              }
+            }
+            tmem_st16(t_s + 16 * ch, w16);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        arrive_warp(&p_ready[st]);
+      }
+      blk += nb;
+      if (!ok) break;
+
+      // ------------------------------------------------ the segment's end
+      if (ns > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float scale_own = 1.f, scale_other = 0.f;   // of the two streams' sums (one tile: they join here)
+      // The second stream's (m, l, r), then kX columns of its sums at a time ([kX][128]), go over through the
+      // queries' shared memory (every score has been computed).
+      constexpr int kX = L::kQBytes / (kTileRows * 4);
+      float* const xch = reinterpret_cast<float*>(qtile);
+      if (kTiles == 1) {
+        bool met = meet();   // the other stream's scores too
+        if (st == 1) xch[row] = m, xch[kTileRows + row] = l, xch[2 * kTileRows + row] = r;
+        met = met && meet();
+        if (st == 0) {
+          const float om = xch[row], ol = xch[kTileRows + row], orr = xch[2 * kTileRows + row];
+          const float mn = fmaxf(m, om), rn = fmaxf(r, orr);
+          l = l * ex2(m - mn) + ol * ex2(om - mn);
+          scale_own = ex2(r - rn);
+          scale_other = ex2(orr - rn);
+          m = mn;
+          r = rn;
+        }
+        if (!met) {
+          ok = false;
+          break;
+        }
+      }
+      const bool whole = wk.whole();
+      float* const part = p.parts + ((size_t)blockIdx.x * 2 + (wk.item_u0 <= u0 ? 0 : 1)) * L::kPart;
+      const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(r - m);
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        if (kTiles == 1 && c0 % kX == 0) {
+          if (!meet()) ok = false;
+          if (st == 1) {
+#pragma unroll 1
+            for (int c = 0; c < kX; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(t_o + c0 + c, o);
+              tmem_wait_ld32(o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) xch[(c + k) * kTileRows + row] = ns > 0 ? __uint_as_float(o[k]) : 0.f;
+            }
+          }
+          if (!meet()) ok = false;
+          if (!ok) break;
+        }
+        if (kTiles == 1 && st == 1) continue;
+        uint32_t o[32];
+        tmem_ld32(t_o + c0, o);
+        tmem_wait_ld32(o);
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          v[k] = __uint_as_float(o[k]);
+          if (kTiles == 1) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
+        }
+        if (live && whole) {
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + (wk.s.row0 + tok) * p.out_stride + head * D + c0);
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = v[k + e] * z;
+            if (l == 0.f) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] = 0.f;
+            }
+            dst[k / 8] = pack8<kF16>(y);
+          }
+        } else if (live) {
+          float4* const dst = reinterpret_cast<float4*>(part + irow * D + c0);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        }
+      }
+      if (!ok) break;
+      if (live && (kTiles == 2 || st == 0)) {
+        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
+        else if (p.lse) p.lse[(size_t)(wk.s.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
+      }
+      tc_fence_before();
+      if (!whole) {
+        // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.
+        const int first = runs.owner(wk.item_u0 + L::kLead), np = runs.owner(wk.item_u0 + L::kLead + wk.t.units - 1) - first + 1;
+        __threadfence();
+        if (!meet()) {
+          ok = false;
+          break;
+        }
+        if (threadIdx.x == 0) {
+          const uint32_t old = atom_add_acq_rel_u32(p.counters + first, 1u);
+          if (old >= (uint32_t)np) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
+          if (old == (uint32_t)np - 1) p.counters[first] = 0u;   // ready for the next call
+          last_sm = old == (uint32_t)np - 1;
+        }
+        if (!meet()) {
+          ok = false;
+          break;
+        }
+        if (last_sm) {
+          __threadfence();
+          const float* const part0 = p.parts + ((size_t)first * 2 + (wk.item_u0 <= runs.begin(first) ? 0 : 1)) * L::kPart;
+          auto part_of = [&](int i) { return i == 0 ? part0 : p.parts + (size_t)(first + i) * 2 * L::kPart; };
+          const int rows = min(rows_left, L::kRows);
+          constexpr int kVec = D / 4;   // threads of a row, four values each
+          for (int at = threadIdx.x; at < rows * kVec; at += kSoftThreads) {
+            const int rw = at / kVec, d = 4 * (at % kVec);
+            float mm = kFloor, rm = kFloor;
+#pragma unroll 4
+            for (int i = 0; i < np; ++i) {
+              const float4 s = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + rw);
+              mm = fmaxf(mm, s.x);
+              rm = fmaxf(rm, s.z);
+            }
+            float lt = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < np; ++i) {
+              const float4 s = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + rw);
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(i) + rw * D + d));
+              const float f = ex2(s.z - rm);
+              lt += s.y * ex2(s.x - mm);
+              acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+            }
+            const int oi = wk.tile * L::kRows + rw;
+            const int orow = wk.s.row0 + oi / p.group, oh = wk.h * p.group + oi % p.group;
+            const float zz = lt == 0.f ? 0.f : __fdividef(1.f, lt) * ex2(rm - mm);
+            *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
+                make_uint2(pack2<kF16>(acc.x * zz, acc.y * zz), pack2<kF16>(acc.z * zz, acc.w * zz));
+            if (p.lse && d == 0) p.lse[(size_t)orow * p.q_heads + oh] = lt == 0.f ? -INFINITY : (mm + lg2(lt)) * 0.69314718056f;
+          }
+        }
+      }
+      if (kTiles == 1 && !meet()) ok = false;   // the exchange is over: the next queries may take its place
+    }
+  }
+
+  // Every role ends here; then the allocating warp returns the tensor memory.
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <bool kF16, int D, int kTiles>
+static cudaError_t launch_tc(const Params& p, int sms, cudaStream_t stream) {
+  using L = TcLayout<D, kTiles>;
+  auto kern = kv8_attention_tc_kernel<kF16, D, kTiles>;
+  cudaError_t e = ensure_smem_attribute((const void*)kern, L::kBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = (size_t)L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s) {
+  const bool one = (long long)p.step.max_tokens * p.group <= kTileRows;
+  if (head_dim == 64)
+    return f16 ? (one ? launch_tc<true, 64, 1>(p, sms, s) : launch_tc<true, 64, 2>(p, sms, s))
+               : (one ? launch_tc<false, 64, 1>(p, sms, s) : launch_tc<false, 64, 2>(p, sms, s));
+  return f16 ? (one ? launch_tc<true, 128, 1>(p, sms, s) : launch_tc<true, 128, 2>(p, sms, s))
+             : (one ? launch_tc<false, 128, 1>(p, sms, s) : launch_tc<false, 128, 2>(p, sms, s));
+}
+
+size_t many_parts_bytes(int head_dim, int sms) {
+  if (head_dim > 128) return 0;
+  const int part = head_dim == 64 ? TcLayout<64, 2>::kPart : TcLayout<128, 2>::kPart;
+  return (size_t)sms * 2 * part * sizeof(float);
+}
+
+}  // namespace attn
+}  // namespace w8a8

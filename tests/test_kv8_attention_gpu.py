@@ -108,6 +108,20 @@ def test_page_scales_of_every_size(ns, lens):
     c.check_attention(out, lse, scale)
 
 
+@pytest.mark.parametrize("ns,lens", [([1, 2], [150, 333]), ([20], [222]), ([80], [300])])
+@pytest.mark.parametrize("small,large", [(0.0, 1e12), (1e-30, 1e8), (0.0, 1.0)])
+def test_values_far_from_the_largest_score(ns, lens, small, large):
+    # The pages with the largest scores (by up to 2^150) hold values of no or next to no size: what the output
+    # is made of has probabilities that leave fp32's range long before the sums do.
+    c = Case(ns, lens, 8, 2, 128, 16, "bf16", seed=18)
+    used = c.table[c.table >= 0]
+    c.ks[used[::3]] *= 25.0
+    c.vs[used[::3]] *= small
+    c.vs[used[1::3]] *= large
+    out, lse, scale = _run(c)
+    c.check_attention(out, lse, scale)
+
+
 @pytest.mark.parametrize("ns,lens", [([3, 2], [180, 67]), ([70], [150])])
 def test_query_magnitudes(ns, lens):
     # Rows of very large, very small, zero and one-sided queries.
