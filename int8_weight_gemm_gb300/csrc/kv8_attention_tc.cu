@@ -80,6 +80,18 @@ __device__ __forceinline__ int tiles_of(const Params& p, const Seq& s) {
   return (int)quotient((long long)s.n * p.group + L::kRows - 1, L::kRows);
 }
 
+// One segment, as the producer hands it to the other roles (nb = 0: the run is over).
+struct Segment {
+  int nb;                    // blocks
+  int T0;                    // first token
+  int row0, pos0, len;       // of the sequence: first row, position of its first row, cached tokens
+  int h, tile, rows;         // kv head, row tile, rows of the tile that exist
+  int whole;                 // the item's only part
+  int slot;                  // else: its place among this CTA's parts,
+  int first, parts, slot0;   //   and the item's first CTA, number of CTAs, and place in the first one
+};
+constexpr int kSegments = 4;   // segments under way
+
 // A run's segments, one item's part each.  Items are ordered by sequence, kv head, row tile.
 template <typename L>
 struct Walk {
@@ -146,6 +158,18 @@ __device__ __forceinline__ void umma_f16_ss(uint32_t tmem_d, uint64_t desc_a, ui
       : "memory");
 }
 
+// One lane of the converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(on));
+  return on != 0;
+}
+
+template <int N>
+struct Const {
+  static constexpr int value = N;
+};
+
 // Shared-memory descriptors with the 128-byte swizzle (rows of 128 bytes, atoms of 8 rows, 1024-byte
 // aligned; version 1 in bits 46..47, layout 2 in bits 61..63).  K-major: the rows are the operand's rows,
 // 64 of k each; atoms of rows 1024 bytes apart (stride field).
@@ -169,6 +193,63 @@ __device__ __forceinline__ void arrive_warp(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
+// Two fp32 operations in one instruction (each rounded as the scalar one).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The rare step of a softmax warp when some row's reference r has moved: the sums O (`cols` columns; 0 for a
+// first block) and the `chunks` x 16 columns of weights already written of this block, times the row's factor.
+__device__ __noinline__ void rescale(uint32_t t_o, int cols, uint32_t t_w, int chunks, float down) {
+  tc_fence_after();
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t o[16];
+    tmem_ld16(t_o + c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
+    tmem_st16(t_o + c, o);
+  }
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t o[16];
+    tmem_ld16(t_w + 16 * c, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
+      o[k] = pack2<true>(w.x * down, w.y * down);
+    }
+    tmem_st16(t_w + 16 * c, o);
+  }
+  tmem_wait_st();
+}
+
 // Granule scales of a block, as the softmax and converter warps use them.
 struct GranScale {
   float ks, vs;    // magnitudes
@@ -186,7 +267,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   __shared__ __align__(8) uint64_t sc_full[kScales];                        // scales of a block
   __shared__ __align__(8) uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];   // fp16 blocks
   __shared__ __align__(8) uint64_t q_full[2], s_full[2], p_ready[2], pv_done[2];   // of each stream
+  __shared__ __align__(8) uint64_t seg_full[kSegments], seg_empty[kSegments];
   __shared__ __align__(8) uint64_t join_bar, final_bar;
+  __shared__ Segment segs[kSegments];
   __shared__ __align__(16) GranScale scales[kScales][kGrans];
   __shared__ long long scan_sm[kTcThreads / 32];
   __shared__ struct {
@@ -214,6 +297,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       mbar_init(&k_empty[i], 1), mbar_init(&v_empty[i], 1);
       mbar_init(&q_full[i], 4), mbar_init(&s_full[i], 1), mbar_init(&p_ready[i], 4), mbar_init(&pv_done[i], 1);
     }
+#pragma unroll
+    for (int i = 0; i < kSegments; ++i) mbar_init(&seg_full[i], 1), mbar_init(&seg_empty[i], kConvWarps + 1 + kSoftWarps);
     mbar_init(&join_bar, kSoftWarps);
     mbar_init(&final_bar, 1);
     abort_flag = 0;
@@ -250,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   if (lane == 31) scan_sm[warp] = incl;
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = 0;   // all 512 columns are this CTA's: they begin at the first
   long long before = incl - mine, U = 0;
 #pragma unroll
   for (int w = 0; w < kTcThreads / 32; ++w) {
@@ -277,28 +362,58 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   }
   __syncthreads();
 
-  Walk<L> wk;
-  wk.u = u0;
-  wk.u1 = u1;
-  if (active) {
-    wk.s = start_sm.s;
-    wk.b = start_sm.b;
-    wk.tiles = tiles_of<L>(p, wk.s);
-    long long head = 0;
-    for (int t = 0; t < wk.tiles; ++t) head += L::kLead + tile_span<L>(p, wk.s, t).units;
-    wk.h = (int)quotient(u0 - start_sm.u, head);
-    wk.item_u0 = start_sm.u + wk.h * head;
-    wk.tile = 0;
-    wk.t = tile_span<L>(p, wk.s, 0);
-  }
+  // The next segment's place (of a role other than the producer), or null at the end of the run.
+  uint32_t seg = 0;
+  auto next_segment = [&]() -> const Segment* {
+    if (!wait_all(&seg_full[seg % kSegments], (seg / kSegments) & 1u, &abort_flag, p.status)) return nullptr;
+    const Segment* g = &segs[seg % kSegments];
+    return g->nb > 0 ? g : nullptr;
+  };
+  auto end_segment = [&]() {
+    arrive_warp(&seg_empty[seg % kSegments]);
+    ++seg;
+  };
 
   if (warp == kProducerWarp) {
     // ---------------------------------------------------------------- producer
+    Walk<L> wk;
+    wk.u = u0;
+    wk.u1 = u1;
+    if (active) {
+      wk.s = start_sm.s;
+      wk.b = start_sm.b;
+      wk.tiles = tiles_of<L>(p, wk.s);
+      long long head = 0;
+      for (int t = 0; t < wk.tiles; ++t) head += L::kLead + tile_span<L>(p, wk.s, t).units;
+      wk.h = (int)quotient(u0 - start_sm.u, head);
+      wk.item_u0 = start_sm.u + wk.h * head;
+      wk.tile = 0;
+      wk.t = tile_span<L>(p, wk.s, 0);
+    }
     uint32_t blk = 0;   // blocks of the CTA before this segment
     bool ok = true;
     uint32_t copies = 0;   // slots filled
-    while (ok && wk.next(p)) {
-      const int nb = wk.ue - wk.ub;
+    for (uint32_t seg = 0; ok; ++seg) {
+      const bool more = wk.next(p);
+      if (seg >= kSegments && !wait_all(&seg_empty[seg % kSegments], (seg / kSegments - 1) & 1u, &abort_flag, p.status)) break;
+      const int nb = more ? wk.ue - wk.ub : 0;
+      if (lane == 0) {
+        Segment g{};
+        if (more) {
+          g.nb = nb;
+          g.T0 = wk.t.lo + wk.ub * kBlock;
+          g.row0 = wk.s.row0, g.pos0 = wk.s.len - wk.s.n, g.len = wk.s.len;
+          g.h = wk.h, g.tile = wk.tile, g.rows = (int)min((long long)L::kRows, (long long)wk.s.n * p.group - (long long)wk.tile * L::kRows);
+          g.whole = wk.whole();
+          g.slot = wk.item_u0 <= u0 ? 0 : 1;
+          g.first = runs.owner(wk.item_u0 + L::kLead);
+          g.parts = runs.owner(wk.item_u0 + L::kLead + wk.t.units - 1) - g.first + 1;
+          g.slot0 = wk.item_u0 <= runs.begin(g.first) ? 0 : 1;
+        }
+        segs[seg % kSegments] = g;
+      }
+      arrive_warp(&seg_full[seg % kSegments]);
+      if (!more) break;
       const int T0 = wk.t.lo + wk.ub * kBlock, T1 = min(wk.t.hi, wk.t.lo + wk.ue * kBlock);
       const int* const table = p.step.page_table + (size_t)wk.b * p.step.table_width;
       for (int base = 0; ok && base < nb; base += 4) {
@@ -358,8 +473,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     const int cw = warp - kSoftWarps;
     uint32_t n = 0;   // block of the CTA
     bool ok = true;
-    while (ok && wk.next(p)) {
-      for (int j = wk.ub; ok && j < wk.ue; ++j, ++n) {
+    while (const Segment* g = ok ? next_segment() : nullptr) {
+      const int nb = g->nb;
+      end_segment();
+      for (int j = 0; ok && j < nb; ++j, ++n) {
         if (!wait_all(&sc_full[n % kScales], (n / kScales) & 1u, &abort_flag, p.status)) {
           ok = false;
           break;
@@ -415,64 +532,85 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       }
     }
   } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- issuer (one thread)
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
-      constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
-      uint32_t blk = 0, seg = 0, cnt[2] = {0u, 0u};   // products issued of each stream
-      bool ok = true;
-      while (ok && wk.next(p)) {
-        const int nb = wk.ue - wk.ub;
-        const int ns[2] = {kTiles == 2 ? nb : (nb + 1) / 2, kTiles == 2 ? nb : nb / 2};
-        auto block_of = [&](int s, int i) { return blk + (uint32_t)(kTiles == 2 ? i : 2 * i + s); };
-        auto scores = [&](int s, int i) {
-          const uint32_t n = block_of(s, i);
-          if (!mbar_wait(&k_full[n & 1], (n >> 1) & 1u, &abort_flag, p.status)) return false;
-          tc_fence_after();
-          const uint32_t qa = smem_addr(qtile + (kTiles == 2 ? s : 0) * L::kQBytes), ka = smem_addr(k16 + (n & 1) * L::kBlk16);
+    // ---------------------------------------------------------------- issuer
+    // The whole warp walks the blocks and one elected lane issues, with every address a constant of the
+    // unrolled code: an instruction's operands then come from uniform registers.  (With one thread on a
+    // branch of its own, and the buffers' addresses computed, an instruction of 64 tensor cycles took 165 to
+    // issue, and bounded the kernel.)
+    constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
+    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
+    const uint32_t q_addr = smem_addr(qtile), k_addr = smem_addr(k16), v_addr = smem_addr(v16);
+    uint32_t blk = 0, cnt[2] = {0u, 0u};   // products issued of each stream
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &abort_flag, p.status); };
+    auto scores_of = [&](auto stream, auto buffer) {
+      constexpr int s = decltype(stream)::value, u = decltype(buffer)::value;
+      if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
-            umma_f16_ss(tmem + (uint32_t)(s * L::kStreamCols + L::kSCol), desc_kmajor(qa + off), desc_kmajor(ka + off), idesc_s, k > 0);
-          }
-          umma_commit(&s_full[s]);
-          if (kTiles == 1 || s == 1) umma_commit(&k_empty[n & 1]);
-          return true;
-        };
-        ok = mbar_wait(&q_full[0], seg & 1u, &abort_flag, p.status) &&
-             (kTiles == 1 || mbar_wait(&q_full[1], seg & 1u, &abort_flag, p.status));
-        ok = ok && scores(0, 0) && (ns[1] == 0 || scores(1, 0));
-        for (int i = 0; ok && i < ns[0]; ++i) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (!ok || i >= ns[s]) continue;
-            const uint32_t n = block_of(s, i);
-            ok = mbar_wait(&v_full[n & 1], (n >> 1) & 1u, &abort_flag, p.status) &&
-                 mbar_wait(&p_ready[s], cnt[s] & 1u, &abort_flag, p.status);
-            if (!ok) continue;
-            tc_fence_after();
-            const uint32_t va = smem_addr(v16 + (n & 1) * L::kBlk16);
-            const uint32_t t = tmem + (uint32_t)(s * L::kStreamCols);
-#pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              umma_f16_tmem_a(t + L::kOCol, t + (uint32_t)(L::kSCol + 8 * k), desc_mnmajor(va + (uint32_t)(k * 16 * 128), kHalfBytes),
-                              idesc_o, i > 0 || k > 0);
-            umma_commit(&pv_done[s]);
-            if (kTiles == 1 || s == 1) umma_commit(&v_empty[n & 1]);
-            // The next scores take the tensor memory of the weights that these products read.
-            if (i + 1 < ns[s])
-              ok = mbar_wait(&pv_done[s], cnt[s] & 1u, &abort_flag, p.status) && scores(s, i + 1);
-            ++cnt[s];
-          }
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
+          umma_f16_ss((uint32_t)(s * L::kStreamCols + L::kSCol), desc_kmajor(q_addr + (kTiles == 2 ? s : 0) * L::kQBytes + off),
+                      desc_kmajor(k_addr + u * L::kBlk16 + off), idesc_s, k > 0);
         }
-        blk += nb;
-        ++seg;
+        umma_commit(&s_full[s]);
+        if (kTiles == 1 || s == 1) umma_commit(&k_empty[u]);
       }
-      // Every product issued completes before tensor memory is freed.
+      __syncwarp();
+    };
+    auto sums_of = [&](auto stream, auto buffer, bool first) {
+      constexpr int s = decltype(stream)::value, u = decltype(buffer)::value;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)
+          umma_f16_tmem_a((uint32_t)(s * L::kStreamCols + L::kOCol), (uint32_t)(s * L::kStreamCols + L::kSCol + 8 * k),
+                          desc_mnmajor(v_addr + (uint32_t)(u * L::kBlk16 + k * 16 * 128), kHalfBytes), idesc_o, k > 0 || !first);
+        umma_commit(&pv_done[s]);
+        if (kTiles == 1 || s == 1) umma_commit(&v_empty[u]);
+      }
+      __syncwarp();
+    };
+    while (const Segment* g = ok ? next_segment() : nullptr) {
+      const int nb = g->nb;
+      const uint32_t q_use = seg & 1u;
+      end_segment();
+      const int ns[2] = {kTiles == 2 ? nb : (nb + 1) / 2, kTiles == 2 ? nb : nb / 2};
+      auto block_of = [&](int s, int i) { return blk + (uint32_t)(kTiles == 2 ? i : 2 * i + s); };
+      auto scores = [&](auto stream, int i) {
+        const uint32_t n = block_of(decltype(stream)::value, i);
+        if (!wait(&k_full[n & 1], (n >> 1) & 1u)) return false;
+        tc_fence_after();
+        if (n & 1) scores_of(stream, Const<1>{});
+        else scores_of(stream, Const<0>{});
+        return true;
+      };
+      auto step = [&](auto stream, int i) {
+        constexpr int s = decltype(stream)::value;
+        if (!ok || i >= ns[s]) return;
+        const uint32_t n = block_of(s, i);
+        ok = wait(&v_full[n & 1], (n >> 1) & 1u) && wait(&p_ready[s], cnt[s] & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        if (n & 1) sums_of(stream, Const<1>{}, i == 0);
+        else sums_of(stream, Const<0>{}, i == 0);
+        // The next scores take the tensor memory of the weights that these products read.
+        if (i + 1 < ns[s]) ok = wait(&pv_done[s], cnt[s] & 1u) && scores(stream, i + 1);
+        ++cnt[s];
+      };
+      ok = wait(&q_full[0], q_use) && (kTiles == 1 || wait(&q_full[1], q_use));
+      ok = ok && scores(Const<0>{}, 0) && (ns[1] == 0 || scores(Const<1>{}, 0));
+      for (int i = 0; ok && i < ns[0]; ++i) {
+        step(Const<0>{}, i);
+        step(Const<1>{}, i);
+      }
+      blk += nb;
+    }
+    // Every product issued completes before tensor memory is freed.
+    if (elect_one()) {
       umma_commit(&final_bar);
       mbar_wait_drain(&final_bar, 0, p.status);
     }
-  } else {
+    __syncwarp();
+  } else if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax warps
     const int st = warp >> 2, quad = warp & 3;
     const int row = 32 * quad + lane;                              // of the tile
@@ -487,28 +625,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       return ok;
     };
     bool ok = true;
-    while (ok && wk.next(p)) {
-      const int nb = wk.ue - wk.ub;
+    while (const Segment* g = ok ? next_segment() : nullptr) {
+      const int nb = g->nb;
       const int ns = kTiles == 2 ? nb : st == 0 ? (nb + 1) / 2 : nb / 2;
-      const int T0 = wk.t.lo + wk.ub * kBlock;
-      const int rows_left = wk.s.n * p.group - wk.tile * L::kRows;   // rows of the item that exist
-      const bool live = irow < rows_left;
-      const int ri = wk.tile * L::kRows + (live ? irow : 0);
-      const int tok = ri / p.group, head = wk.h * p.group + ri % p.group;
-      const bool warp_live = (kTiles == 2 ? st * kTileRows : 0) + 32 * quad < rows_left;
+      const int T0 = g->T0;
+      const bool live = irow < g->rows;
+      const int ri = g->tile * L::kRows + (live ? irow : 0);
+      const int tok = ri / p.group, head = g->h * p.group + ri % p.group;
+      const bool warp_live = (kTiles == 2 ? st * kTileRows : 0) + 32 * quad < g->rows;
 
       // ------------------------------------------------ queries: fp16, scaled by a power of two
       float rowmul;
       {
-        const uint4* const src = reinterpret_cast<const uint4*>(p.q + (wk.s.row0 + tok) * p.q_stride + head * D);
-        uint4 raw[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4* const src = reinterpret_cast<const uint4*>(p.q + (g->row0 + tok) * p.q_stride + head * D);
         float amax = 0.f;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < D / 8; ++i) {
           float f[8];
-          unpack8<kF16>(raw[i], f);
+          unpack8<kF16>(live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
           for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(f[k]));
         }
@@ -517,10 +651,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         rowmul = p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23);
         if (kTiles == 2 || st == 0) {
           uint8_t* const dst = qtile + (kTiles == 2 ? st : 0) * L::kQBytes + row * 128;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
+#pragma unroll 4
+          for (int i = 0; i < D / 8; ++i) {   // (out of the L1 cache now)
             float f[8];
-            unpack8<kF16>(raw[i], f);
+            unpack8<kF16>(live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] *= down;
             *reinterpret_cast<uint4*>(dst + (i >> 3) * kHalfBytes + (((i & 7) ^ (row & 7)) << 4)) = pack8<true>(f);
@@ -529,8 +663,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           arrive_warp(&q_full[kTiles == 2 ? st : 0]);
         }
       }
-      const int pos = wk.s.len - wk.s.n + tok;
-      const int end = !live ? 0x7fffffff : p.causal ? min(pos + 1, wk.s.len) : wk.s.len;
+      const int pos = g->pos0 + tok;
+      const int end = !live ? 0x7fffffff : p.causal ? min(pos + 1, g->len) : g->len;
       const int beg = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
       const int full_hi = __reduce_min_sync(0xffffffffu, end), full_lo = __reduce_max_sync(0xffffffffu, beg);
 
@@ -549,101 +683,86 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           tc_fence_after();
           const bool edge = T < full_lo || T + kBlock > full_hi;
           const GranScale* const sc = scales[n % kScales];
-          uint32_t buf[2][32];
-          tmem_ld32(t_s, buf[0]);
-#pragma unroll
-          for (int ch = 0; ch < kBlock / 32; ++ch) {
-            uint32_t (&a)[32] = buf[ch & 1];
-            tmem_wait_ld32(a);
-            if (ch + 1 < kBlock / 32) tmem_ld32(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
-            if (edge) {
-              // Scores that the row does not see.
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const int t = T + 32 * ch + k;
-                if (t < beg || t >= end) a[k] = 0xFF800000u;
-              }
-            }
-            // Score a of granule y in powers of two: a * c1 + bias.
-            float c1[2], mx = -INFINITY, mw = -INFINITY, f[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              // (A factor of zero would make a hidden score's -inf a NaN.)
-              c1[y] = fmaxf(sc[2 * ch + y].ks * rowmul, 1e-37f);
-              float t = __uint_as_float(a[16 * y]);
-#pragma unroll
-              for (int k = 1; k < 16; ++k) t = fmaxf(t, __uint_as_float(a[16 * y + k]));
-              t = fmaf(t, c1[y], sc[2 * ch + y].bias);
-              mx = fmaxf(mx, t);
-              mw = fmaxf(mw, t + lg2(sc[2 * ch + y].vs));
-              f[y] = hs * sc[2 * ch + y].vs;
-            }
-            bool far = false;
-            if (__any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar)) {
-              // Some row's reference moves: its sums so far are rescaled, and with them the weights of
-              // this block that are already written.
-              if (mx > m + kSlack) {
-                l *= ex2(m - mx);
-                m = mx;
-              }
-              float rn = mw > r + kSlack ? mw : r;
-              rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
-              const float down = ex2(r - rn);
-              r = rn;
-              hs = ex2(m - rn);
-              f[0] = hs * sc[2 * ch].vs;
-              f[1] = hs * sc[2 * ch + 1].vs;
-              far = __any_sync(0xffffffffu, fmaxf(f[0], f[1]) > kFar);
-              if (ch + 1 < kBlock / 32) tmem_wait_ld32(buf[(ch + 1) & 1]);
-              if (i > 0) {
-                if (!wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
-                tc_fence_after();
+          // 32 tokens a turn.  (Not unrolled, and no load ahead: the warps of all roles together have to
+          // stay inside the instruction cache, and a spilled register's home is far behind a shared memory
+          // that leaves the L1 cache next to nothing.)
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(t_o + c0, o);
-                  tmem_wait_ld();
+          for (int ch = 0; ch < kBlock / 32; ++ch) {
+            {
+              uint32_t a[32];
+              tmem_ld32(t_s + 32 * ch, a);
+              tmem_wait_ld32(a);
+              if (edge) {
+                // Scores that the row does not see.
+                const int t0 = T + 32 * ch;
 #pragma unroll
-                  for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * down);
-                  tmem_st16(t_o + c0, o);
+                for (int k = 0; k < 32; ++k)
+                  if (t0 + k < beg || t0 + k >= end) a[k] = 0xFF800000u;
+              }
+              const float4 g0 = *reinterpret_cast<const float4*>(&sc[2 * ch]), g1 = *reinterpret_cast<const float4*>(&sc[2 * ch + 1]);
+              // Score a of a granule in powers of two: a * c1 + bias.  (A factor of zero would make a
+              // hidden score's -inf a NaN.)
+              const float c1[2] = {fmaxf(g0.x * rowmul, 1e-37f), fmaxf(g1.x * rowmul, 1e-37f)};
+              const float vs[2] = {g0.y, g1.y}, bias[2] = {g0.z, g1.z};
+              float mx = -INFINITY, mw = -INFINITY, f[2];
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float t = max3(__uint_as_float(a[16 * y]), __uint_as_float(a[16 * y + 1]), __uint_as_float(a[16 * y + 2]));
+#pragma unroll
+                for (int k = 3; k < 15; k += 2) t = max3(t, __uint_as_float(a[16 * y + k]), __uint_as_float(a[16 * y + k + 1]));
+                t = fmaf(fmaxf(t, __uint_as_float(a[16 * y + 15])), c1[y], bias[y]);
+                mx = fmaxf(mx, t);
+                mw = fmaxf(mw, t + lg2(vs[y]));
+                f[y] = hs * vs[y];
+              }
+              bool far = false;
+              if (__any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar)) {
+                // Some row's reference moves: its sums so far are rescaled, and with them the weights of
+                // this block that are already written.
+                if (mx > m + kSlack) {
+                  l *= ex2(m - mx);
+                  m = mx;
+                }
+                float rn = mw > r + kSlack ? mw : r;
+                rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
+                const float down = ex2(r - rn);
+                r = rn;
+                hs = ex2(m - rn);
+                f[0] = hs * vs[0];
+                f[1] = hs * vs[1];
+                far = __any_sync(0xffffffffu, fmaxf(f[0], f[1]) > kFar);
+                if (i > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
+                if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
+              }
+              uint32_t w16[16];
+              uint64_t sum = 0;   // (0, 0)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const float c0 = bias[y] - m;
+                const uint64_t c1p = pair(c1[y], c1[y]), c0p = pair(c0, c0), fp = pair(f[y], f[y]);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  float e0, e1;
+                  unpair(fma2(pair(__uint_as_float(a[16 * y + k]), __uint_as_float(a[16 * y + k + 1])), c1p, c0p), e0, e1);
+                  const uint64_t pr = pair(ex2(e0), ex2(e1));
+                  sum = add2(sum, pr);
+                  float w0, w1;
+                  unpair(mul2(pr, fp), w0, w1);
+                  w16[8 * y + k / 2] = pack2<true>(w0, w1);
+                }
+                if (far && f[y] > kFar) {
+                  const float d0 = bias[y] + lg2(vs[y]) - r;
+#pragma unroll
+                  for (int k = 0; k < 16; k += 2)
+                    w16[8 * y + k / 2] = pack2<true>(ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], d0)),
+                                                     ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], d0)));
                 }
               }
-              tmem_wait_st();
-#pragma unroll
-              for (int c0 = 0; c0 < ch; ++c0) {
-                uint32_t o[16];
-                tmem_ld16(t_s + 16 * c0, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  const float2 w = __half22float2(*reinterpret_cast<const __half2*>(&o[k]));
-                  o[k] = pack2<true>(w.x * down, w.y * down);
-                }
-                tmem_st16(t_s + 16 * c0, o);
-              }
-              tmem_wait_st();
+              float l0, l1;
+              unpair(sum, l0, l1);
+              l += l0 + l1;
+              tmem_st16(t_s + 16 * ch, w16);
             }
-            uint32_t w16[16];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float c0 = sc[2 * ch + y].bias - m;
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float p0 = ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], c0));
-                const float p1 = ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], c0));
-                l += p0;
-                l += p1;
-                w16[8 * y + k / 2] = pack2<true>(p0 * f[y], p1 * f[y]);
-              }
-              if (far && f[y] > kFar) {
-                const float d0 = sc[2 * ch + y].bias + lg2(sc[2 * ch + y].vs) - r;
-#pragma unroll
-                for (int k = 0; k < 16; k += 2)
-                  w16[8 * y + k / 2] = pack2<true>(ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], d0)),
-                                                   ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], d0)));
-              }
-            }
-            tmem_st16(t_s + 16 * ch, w16);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -682,8 +801,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           break;
         }
       }
-      const bool whole = wk.whole();
-      float* const part = p.parts + ((size_t)blockIdx.x * 2 + (wk.item_u0 <= u0 ? 0 : 1)) * L::kPart;
+      const bool whole = g->whole;
+      float* const part = p.parts + ((size_t)blockIdx.x * 2 + g->slot) * L::kPart;
       const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(r - m);
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -713,7 +832,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (kTiles == 1) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
         }
         if (live && whole) {
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + (wk.s.row0 + tok) * p.out_stride + head * D + c0);
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             float y[8];
@@ -734,21 +853,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       if (!ok) break;
       if (live && (kTiles == 2 || st == 0)) {
         if (!whole) *reinterpret_cast<float4*>(part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
-        else if (p.lse) p.lse[(size_t)(wk.s.row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
+        else if (p.lse) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
       }
       tc_fence_before();
       if (!whole) {
-        // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.
-        const int first = runs.owner(wk.item_u0 + L::kLead), np = runs.owner(wk.item_u0 + L::kLead + wk.t.units - 1) - first + 1;
-        __threadfence();
+        // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.  (The
+        // meeting orders the warps' stores before thread 0's release, and its acquire before their reads.)
+        const int np = g->parts;
         if (!meet()) {
           ok = false;
           break;
         }
         if (threadIdx.x == 0) {
-          const uint32_t old = atom_add_acq_rel_u32(p.counters + first, 1u);
+          const uint32_t old = atom_add_acq_rel_u32(p.counters + g->first, 1u);
           if (old >= (uint32_t)np) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
-          if (old == (uint32_t)np - 1) p.counters[first] = 0u;   // ready for the next call
+          if (old == (uint32_t)np - 1) p.counters[g->first] = 0u;   // ready for the next call
           last_sm = old == (uint32_t)np - 1;
         }
         if (!meet()) {
@@ -756,40 +875,76 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           break;
         }
         if (last_sm) {
-          __threadfence();
-          const float* const part0 = p.parts + ((size_t)first * 2 + (wk.item_u0 <= runs.begin(first) ? 0 : 1)) * L::kPart;
-          auto part_of = [&](int i) { return i == 0 ? part0 : p.parts + (size_t)(first + i) * 2 * L::kPart; };
-          const int rows = min(rows_left, L::kRows);
-          constexpr int kVec = D / 4;   // threads of a row, four values each
-          for (int at = threadIdx.x; at < rows * kVec; at += kSoftThreads) {
-            const int rw = at / kVec, d = 4 * (at % kVec);
-            float mm = kFloor, rm = kFloor;
+          const float* const part0 = p.parts + ((size_t)g->first * 2 + g->slot0) * L::kPart;
+          const float* const part1 = p.parts + (size_t)g->first * 2 * L::kPart;   // part i > 0: 2 i places on
+          auto part_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * L::kPart; };
+          const int rows = g->rows;
+          // A thread for each row's statistics, then a warp for a row's sums, kAt rows at a time.
+          float4* const row_sm = reinterpret_cast<float4*>(qtile);   // (m, l, r, -)
+          if (irow < rows && (kTiles == 2 || st == 0)) {
+            float mm = kFloor, rm = kFloor, lt = 0.f;
 #pragma unroll 4
             for (int i = 0; i < np; ++i) {
-              const float4 s = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + rw);
-              mm = fmaxf(mm, s.x);
-              rm = fmaxf(rm, s.z);
+              const float4 t = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + irow);
+              const float mn = fmaxf(mm, t.x);
+              lt = lt * ex2(mm - mn) + t.y * ex2(t.x - mn);
+              mm = mn;
+              rm = fmaxf(rm, t.z);
             }
-            float lt = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int i = 0; i < np; ++i) {
-              const float4 s = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + rw);
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(i) + rw * D + d));
-              const float f = ex2(s.z - rm);
-              lt += s.y * ex2(s.x - mm);
-              acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-            }
-            const int oi = wk.tile * L::kRows + rw;
-            const int orow = wk.s.row0 + oi / p.group, oh = wk.h * p.group + oi % p.group;
-            const float zz = lt == 0.f ? 0.f : __fdividef(1.f, lt) * ex2(rm - mm);
-            *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
-                make_uint2(pack2<kF16>(acc.x * zz, acc.y * zz), pack2<kF16>(acc.z * zz, acc.w * zz));
-            if (p.lse && d == 0) p.lse[(size_t)orow * p.q_heads + oh] = lt == 0.f ? -INFINITY : (mm + lg2(lt)) * 0.69314718056f;
+            row_sm[irow] = make_float4(mm, lt, rm, 0.f);
           }
+          if (!meet()) ok = false;
+          constexpr int kVec = D / 4, kAt = 4;   // threads of a row, four values each
+          for (int at0 = threadIdx.x; at0 < rows * kVec; at0 += kAt * kSoftThreads) {
+            float4 acc[kAt];
+#pragma unroll
+            for (int y = 0; y < kAt; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int i = 0; i < np; ++i) {
+              const float* const src = part_of(i);
+              float4 v[kAt];
+              float rr[kAt];
+#pragma unroll
+              for (int y = 0; y < kAt; ++y) {
+                const int at = at0 + y * kSoftThreads;
+                v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                rr[y] = 0.f;
+                if (at < rows * kVec) {
+                  v[y] = __ldcg(reinterpret_cast<const float4*>(src) + at);
+                  rr[y] = __ldcg(src + L::kRows * D + (at / kVec) * 4 + 2);
+                }
+              }
+#pragma unroll
+              for (int y = 0; y < kAt; ++y) {
+                const int at = at0 + y * kSoftThreads;
+                if (at < rows * kVec) {
+                  const float f = ex2(rr[y] - row_sm[at / kVec].z);
+                  acc[y].x = fmaf(v[y].x, f, acc[y].x), acc[y].y = fmaf(v[y].y, f, acc[y].y);
+                  acc[y].z = fmaf(v[y].z, f, acc[y].z), acc[y].w = fmaf(v[y].w, f, acc[y].w);
+                }
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < kAt; ++y) {
+              const int at = at0 + y * kSoftThreads;
+              if (at < rows * kVec) {
+                const int rw = at / kVec, d = 4 * (at % kVec);
+                const float4 t = row_sm[rw];
+                const int oi = g->tile * L::kRows + rw;
+                const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
+                const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
+                *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
+                    make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
+                if (p.lse && d == 0)
+                  p.lse[(size_t)orow * p.q_heads + oh] = t.y == 0.f ? -INFINITY : (t.x + lg2(t.y)) * 0.69314718056f;
+              }
+            }
+          }
+          if (!meet()) ok = false;   // the statistics' place is the next queries'
         }
       }
       if (kTiles == 1 && !meet()) ok = false;   // the exchange is over: the next queries may take its place
+      end_segment();
     }
   }
 
@@ -797,7 +952,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem_base, 512);
 }
 
 template <bool kF16, int D, int kTiles>
