@@ -251,10 +251,10 @@ __device__ __noinline__ void rescale(uint32_t t_o, int cols, uint32_t t_w, int c
 }
 
 // Granule scales of a block, as the softmax and converter warps use them.
-struct GranScale {
-  float ks, vs;    // magnitudes
-  float bias;      // of the scores: 0, or -inf where the granule is left out
-  uint32_t turn;   // fp16 factors of the keys (low half) and the values: 1 or -1
+struct alignas(16) GranScale {
+  float ks, vs;   // magnitudes
+  float lvs;      // log2 vs
+  float bias;     // of the scores: 0, or -inf where the granule is left out
 };
 
 template <bool kF16, int D, int kTiles>
@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   __shared__ __align__(8) uint64_t seg_full[kSegments], seg_empty[kSegments];
   __shared__ __align__(8) uint64_t join_bar, final_bar;
   __shared__ Segment segs[kSegments];
-  __shared__ __align__(16) GranScale scales[kScales][kGrans];
+  __shared__ GranScale scales[kScales][kGrans];
+  __shared__ uint32_t turns[kScales][kGrans];   // fp16 factors of a granule's keys (low half) and values: 1 or -1
   __shared__ long long scan_sm[kTcThreads / 32];
   __shared__ struct {
     Seq s;
@@ -419,7 +420,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       for (int base = 0; ok && base < nb; base += 4) {
         // Lane: granule lane % 8 of block base + lane / 8.
         const int t = T0 + base * kBlock + lane * kGranule;
-        GranScale sc{0.f, 0.f, -INFINITY, 0x3C003C00u};
+        GranScale sc{0.f, 0.f, -INFINITY, -INFINITY};
+        uint32_t turn = 0x3C003C00u;
         int row = 0;
         bool live = t < T1;
         if (live) {
@@ -433,8 +435,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             const float ks = __ldg(p.ks + at), vs = __ldg(p.vs + at);
             sc.ks = fabsf(ks);
             sc.vs = fabsf(vs);
+            sc.lvs = lg2(sc.vs);
             sc.bias = 0.f;
-            sc.turn = (ks < 0.f ? 0xBC00u : 0x3C00u) | ((vs < 0.f ? 0xBC00u : 0x3C00u) << 16);
+            turn = (ks < 0.f ? 0xBC00u : 0x3C00u) | ((vs < 0.f ? 0xBC00u : 0x3C00u) << 16);
           }
         }
         const uint32_t lives = __ballot_sync(0xffffffffu, live);
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (base + i >= nb) break;
           const uint32_t n = blk + base + i;
           const bool own = (lane >> 3) == i;
-          if (own) scales[n % kScales][lane & 7] = sc;
+          if (own) scales[n % kScales][lane & 7] = sc, turns[n % kScales][lane & 7] = turn;
           arrive_warp(&sc_full[n % kScales]);
           const uint32_t bytes = (uint32_t)__popc((lives >> (8 * i)) & 0xFFu) * kGranule * D;
 #pragma unroll
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           ok = false;
           break;
         }
-#pragma unroll
+#pragma unroll 1
         for (int side = 0; side < 2; ++side) {
           const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
           const uint8_t* const src = ring + slot * L::kSlot;
@@ -493,9 +496,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           }
           // A warp takes 32 tokens: eight rows by four 16-byte pieces at a time, so that neither the
           // reads (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
-            const uint32_t turn = scales[n % kScales][2 * cw + (i >> 1)].turn;
+            const uint32_t turn = turns[n % kScales][2 * cw + (i >> 1)];
             const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
             const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
             const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
@@ -533,74 +536,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- issuer
-    // The whole warp walks the blocks and one elected lane issues, with every address a constant of the
-    // unrolled code: an instruction's operands then come from uniform registers.  (With one thread on a
-    // branch of its own, and the buffers' addresses computed, an instruction of 64 tensor cycles took 165 to
-    // issue, and bounded the kernel.)
+    // The whole warp walks the blocks and one elected lane issues.  A descriptor's low word is its start
+    // address in 16 bytes and moves by constants.  (One warp for both streams: with one each, the products of
+    // two accumulators mix in the pipe and each takes longer; prompt chunk 441 -> 521 us.)
     constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
     constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
-    const uint32_t q_addr = smem_addr(qtile), k_addr = smem_addr(k16), v_addr = smem_addr(v16);
-    uint32_t blk = 0, cnt[2] = {0u, 0u};   // products issued of each stream
+    const uint64_t dq = desc_kmajor(smem_addr(qtile)), dk = desc_kmajor(smem_addr(k16)), dv = desc_mnmajor(smem_addr(v16), kHalfBytes);
+    const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
+    auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); };
+    uint32_t blk = 0, cnt = 0;   // blocks of the CTA before this segment; steps of the first stream
+    uint32_t cnt1 = 0;           // of the second
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_all(bar, parity, &abort_flag, p.status); };
-    auto scores_of = [&](auto stream, auto buffer) {
-      constexpr int s = decltype(stream)::value, u = decltype(buffer)::value;
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * kHalfBytes + (k & 3) * 32);
-          umma_f16_ss((uint32_t)(s * L::kStreamCols + L::kSCol), desc_kmajor(q_addr + (kTiles == 2 ? s : 0) * L::kQBytes + off),
-                      desc_kmajor(k_addr + u * L::kBlk16 + off), idesc_s, k > 0);
-        }
-        umma_commit(&s_full[s]);
-        if (kTiles == 1 || s == 1) umma_commit(&k_empty[u]);
-      }
-      __syncwarp();
-    };
-    auto sums_of = [&](auto stream, auto buffer, bool first) {
-      constexpr int s = decltype(stream)::value, u = decltype(buffer)::value;
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          umma_f16_tmem_a((uint32_t)(s * L::kStreamCols + L::kOCol), (uint32_t)(s * L::kStreamCols + L::kSCol + 8 * k),
-                          desc_mnmajor(v_addr + (uint32_t)(u * L::kBlk16 + k * 16 * 128), kHalfBytes), idesc_o, k > 0 || !first);
-        umma_commit(&pv_done[s]);
-        if (kTiles == 1 || s == 1) umma_commit(&v_empty[u]);
-      }
-      __syncwarp();
-    };
     while (const Segment* g = ok ? next_segment() : nullptr) {
       const int nb = g->nb;
       const uint32_t q_use = seg & 1u;
       end_segment();
-      const int ns[2] = {kTiles == 2 ? nb : (nb + 1) / 2, kTiles == 2 ? nb : nb / 2};
-      auto block_of = [&](int s, int i) { return blk + (uint32_t)(kTiles == 2 ? i : 2 * i + s); };
-      auto scores = [&](auto stream, int i) {
-        const uint32_t n = block_of(decltype(stream)::value, i);
-        if (!wait(&k_full[n & 1], (n >> 1) & 1u)) return false;
-        tc_fence_after();
-        if (n & 1) scores_of(stream, Const<1>{});
-        else scores_of(stream, Const<0>{});
-        return true;
-      };
-      auto step = [&](auto stream, int i) {
-        constexpr int s = decltype(stream)::value;
-        if (!ok || i >= ns[s]) return;
-        const uint32_t n = block_of(s, i);
-        ok = wait(&v_full[n & 1], (n >> 1) & 1u) && wait(&p_ready[s], cnt[s] & 1u);
-        if (!ok) return;
-        tc_fence_after();
-        if (n & 1) sums_of(stream, Const<1>{}, i == 0);
-        else sums_of(stream, Const<0>{}, i == 0);
-        // The next scores take the tensor memory of the weights that these products read.
-        if (i + 1 < ns[s]) ok = wait(&pv_done[s], cnt[s] & 1u) && scores(stream, i + 1);
-        ++cnt[s];
-      };
+      const int n0 = kTiles == 2 ? nb : (nb + 1) / 2, n1 = kTiles == 2 ? nb : nb / 2;
+      // Steps in order: (stream, turn) = (0, -1), (1, -1), (0, 0), (1, 0), ...: the products of a turn's weights
+      // with its values, then, where there is one, the next turn's scores.
       ok = wait(&q_full[0], q_use) && (kTiles == 1 || wait(&q_full[1], q_use));
-      ok = ok && scores(Const<0>{}, 0) && (ns[1] == 0 || scores(Const<1>{}, 0));
-      for (int i = 0; ok && i < ns[0]; ++i) {
-        step(Const<0>{}, i);
-        step(Const<1>{}, i);
+#pragma unroll 1
+      for (int x = -2; ok && x < 2 * n0; ++x) {
+        const int s = x & 1, i = (x + 2) / 2 - 1;
+        if (i >= (s ? n1 : n0)) continue;
+        const uint32_t t = (uint32_t)(s * L::kStreamCols);
+        const bool more = i + 1 < (s ? n1 : n0);
+        const uint32_t nn = blk + (uint32_t)(kTiles == 2 ? i + 1 : 2 * (i + 1) + s), ub = nn & 1u;   // the next turn's block
+        if (i >= 0) {
+          const uint32_t n = nn - (kTiles == 2 ? 1u : 2u), u = n & 1u, c = s ? cnt1 : cnt;
+          ok = wait(&v_full[u], (n >> 1) & 1u) && wait(&p_ready[s], c & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t lo = v_lo + u * (uint32_t)(L::kBlk16 >> 4);
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              umma_f16_tmem_a(t + L::kOCol, t + (uint32_t)(L::kSCol + 8 * k), desc(lo + (uint32_t)(k * 16 * 128 >> 4), v_hi), idesc_o, i > 0 || k > 0);
+            umma_commit(&pv_done[s]);
+            if (kTiles == 1 || s == 1) umma_commit(&v_empty[u]);
+          }
+          __syncwarp();
+          if (s) ++cnt1;
+          else ++cnt;
+          // The next scores take the tensor memory of the weights that these products read.
+          if (more) ok = wait(&k_full[ub], (nn >> 1) & 1u) && wait(&pv_done[s], c & 1u);
+        } else if (more) {
+          ok = wait(&k_full[ub], (nn >> 1) & 1u);
+        }
+        if (!ok || !more) continue;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t ql = q_lo + (kTiles == 2 ? s : 0) * (uint32_t)(L::kQBytes >> 4), kl = k_lo + ub * (uint32_t)(L::kBlk16 >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (uint32_t)(((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
+            umma_f16_ss(t + L::kSCol, desc(ql + off, k_hi), desc(kl + off, k_hi), idesc_s, k > 0);
+          }
+          umma_commit(&s_full[s]);
+          if (kTiles == 1 || s == 1) umma_commit(&k_empty[ub]);
+        }
+        __syncwarp();
       }
       blk += nb;
     }
@@ -685,12 +681,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           const GranScale* const sc = scales[n % kScales];
           // 32 tokens a turn.  (Not unrolled, and no load ahead: the warps of all roles together have to
           // stay inside the instruction cache, and a spilled register's home is far behind a shared memory
-          // that leaves the L1 cache next to nothing.)
+          // that leaves the L1 cache next to nothing.)  The weights are worked out beside the maxima, as if
+          // no reference moved, and once more where one does.
 #pragma unroll 1
           for (int ch = 0; ch < kBlock / 32; ++ch) {
             {
               uint32_t a[32];
               tmem_ld32(t_s + 32 * ch, a);
+              const float4 g0 = *reinterpret_cast<const float4*>(&sc[2 * ch]), g1 = *reinterpret_cast<const float4*>(&sc[2 * ch + 1]);
               tmem_wait_ld32(a);
               if (edge) {
                 // Scores that the row does not see.
@@ -699,65 +697,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                 for (int k = 0; k < 32; ++k)
                   if (t0 + k < beg || t0 + k >= end) a[k] = 0xFF800000u;
               }
-              const float4 g0 = *reinterpret_cast<const float4*>(&sc[2 * ch]), g1 = *reinterpret_cast<const float4*>(&sc[2 * ch + 1]);
               // Score a of a granule in powers of two: a * c1 + bias.  (A factor of zero would make a
               // hidden score's -inf a NaN.)
               const float c1[2] = {fmaxf(g0.x * rowmul, 1e-37f), fmaxf(g1.x * rowmul, 1e-37f)};
-              const float vs[2] = {g0.y, g1.y}, bias[2] = {g0.z, g1.z};
-              float mx = -INFINITY, mw = -INFINITY, f[2];
+              const float vs[2] = {g0.y, g1.y}, lvs[2] = {g0.z, g1.z}, bias[2] = {g0.w, g1.w};
+              float mx, mw;
+              {
+                float t[2];
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                float t = max3(__uint_as_float(a[16 * y]), __uint_as_float(a[16 * y + 1]), __uint_as_float(a[16 * y + 2]));
+                for (int y = 0; y < 2; ++y) {
+                  const uint32_t* const v = a + 16 * y;
+                  float q[4];
 #pragma unroll
-                for (int k = 3; k < 15; k += 2) t = max3(t, __uint_as_float(a[16 * y + k]), __uint_as_float(a[16 * y + k + 1]));
-                t = fmaf(fmaxf(t, __uint_as_float(a[16 * y + 15])), c1[y], bias[y]);
-                mx = fmaxf(mx, t);
-                mw = fmaxf(mw, t + lg2(vs[y]));
-                f[y] = hs * vs[y];
-              }
-              bool far = false;
-              if (__any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar)) {
-                // Some row's reference moves: its sums so far are rescaled, and with them the weights of
-                // this block that are already written.
-                if (mx > m + kSlack) {
-                  l *= ex2(m - mx);
-                  m = mx;
+                  for (int k = 0; k < 4; ++k) q[k] = max3(__uint_as_float(v[k]), __uint_as_float(v[4 + k]), __uint_as_float(v[8 + k]));
+                  const float e = max3(__uint_as_float(v[12]), __uint_as_float(v[13]), __uint_as_float(v[14]));
+                  t[y] = fmaf(max3(max3(q[0], q[1], q[2]), max3(q[3], e, __uint_as_float(v[15])), -INFINITY), c1[y], bias[y]);
                 }
-                float rn = mw > r + kSlack ? mw : r;
-                rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
-                const float down = ex2(r - rn);
-                r = rn;
-                hs = ex2(m - rn);
-                f[0] = hs * vs[0];
-                f[1] = hs * vs[1];
-                far = __any_sync(0xffffffffu, fmaxf(f[0], f[1]) > kFar);
-                if (i > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
-                if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
+                mx = fmaxf(t[0], t[1]);
+                mw = fmaxf(t[0] + lvs[0], t[1] + lvs[1]);
               }
               uint32_t w16[16];
-              uint64_t sum = 0;   // (0, 0)
+              uint64_t sum;
+              bool far = false, moved;
+#pragma unroll 1
+              do {
+                sum = 0;   // (0, 0)
+                const float f[2] = {hs * vs[0], hs * vs[1]};
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float c0 = bias[y] - m;
-                const uint64_t c1p = pair(c1[y], c1[y]), c0p = pair(c0, c0), fp = pair(f[y], f[y]);
+                for (int y = 0; y < 2; ++y) {
+                  const float c0 = bias[y] - m;
+                  const uint64_t c1p = pair(c1[y], c1[y]), c0p = pair(c0, c0), fp = pair(f[y], f[y]);
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  float e0, e1;
-                  unpair(fma2(pair(__uint_as_float(a[16 * y + k]), __uint_as_float(a[16 * y + k + 1])), c1p, c0p), e0, e1);
-                  const uint64_t pr = pair(ex2(e0), ex2(e1));
-                  sum = add2(sum, pr);
-                  float w0, w1;
-                  unpair(mul2(pr, fp), w0, w1);
-                  w16[8 * y + k / 2] = pack2<true>(w0, w1);
+                  for (int k = 0; k < 16; k += 2) {
+                    float e0, e1;
+                    unpair(fma2(pair(__uint_as_float(a[16 * y + k]), __uint_as_float(a[16 * y + k + 1])), c1p, c0p), e0, e1);
+                    const uint64_t pr = pair(ex2(e0), ex2(e1));
+                    sum = add2(sum, pr);
+                    float w0, w1;
+                    unpair(mul2(pr, fp), w0, w1);
+                    w16[8 * y + k / 2] = pack2<true>(w0, w1);
+                  }
                 }
-                if (far && f[y] > kFar) {
-                  const float d0 = bias[y] + lg2(vs[y]) - r;
+                if (far) {
 #pragma unroll
-                  for (int k = 0; k < 16; k += 2)
-                    w16[8 * y + k / 2] = pack2<true>(ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], d0)),
-                                                     ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], d0)));
+                  for (int y = 0; y < 2; ++y) {
+                    if (f[y] > kFar) {
+                      const float d0 = bias[y] + lvs[y] - r;
+#pragma unroll
+                      for (int k = 0; k < 16; k += 2)
+                        w16[8 * y + k / 2] = pack2<true>(ex2(fmaf(__uint_as_float(a[16 * y + k]), c1[y], d0)),
+                                                         ex2(fmaf(__uint_as_float(a[16 * y + k + 1]), c1[y], d0)));
+                    }
+                  }
+                  break;
                 }
-              }
+                moved = __any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar);
+                if (moved) {
+                  // Some row's reference moves: its sums so far are rescaled, and with them the weights of
+                  // this block that are already written.
+                  if (mx > m + kSlack) {
+                    l *= ex2(m - mx);
+                    m = mx;
+                  }
+                  float rn = mw > r + kSlack ? mw : r;
+                  rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
+                  const float down = ex2(r - rn);
+                  r = rn;
+                  hs = ex2(m - rn);
+                  far = __any_sync(0xffffffffu, hs * fmaxf(vs[0], vs[1]) > kFar);
+                  if (i > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
+                  if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
+                }
+              } while (moved);
               float l0, l1;
               unpair(sum, l0, l1);
               l += l0 + l1;
