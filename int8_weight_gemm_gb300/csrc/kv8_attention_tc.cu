@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           }
           // A warp takes 32 tokens: eight rows by four 16-byte pieces at a time, so that neither the
           // reads (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.
-#pragma unroll 1
+#pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t turn = turns[n % kScales][2 * cw + (i >> 1)];
             const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
