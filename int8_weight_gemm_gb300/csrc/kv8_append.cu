@@ -42,11 +42,20 @@ struct QkParams {
   float eps;
   int rot, max_pos, interleaved;
   int q_heads, kv_heads, tokens;
+  int batches;   // kQkHeads heads a lane group takes one after the other
   uint32_t* status;
 };
 
 constexpr int kQkThreads = 256;
-constexpr int kQkHeads = 4;   // heads of one row that a lane group takes: their loads are in flight together
+constexpr int kQkHeads = 4;   // heads of one row whose loads a lane group has in flight together
+
+// Batches of kQkHeads heads a lane group takes: one where there are few groups (a second one would only add its
+// latency), two where there are many, so that a position's rotation is read half as often (16383 rows of 40
+// heads: 67.2 us with two, 70.0 with one, 75.5 with four; 16 rows: 3.1 with one, 4.7 with two).
+static int batches_of(int heads, int rows) {
+  const int chunks = (heads + kQkHeads - 1) / kQkHeads;
+  return (long long)chunks * rows > 16384 && chunks > 1 ? 2 : 1;
+}
 
 // The position's row of the table; a position outside it is recorded and taken as 0.
 __device__ __forceinline__ const float* turn_row(const float* cos_sin, int pos, int rot, int max_pos, uint32_t* status) {
@@ -57,7 +66,37 @@ __device__ __forceinline__ const float* turn_row(const float* cos_sin, int pos, 
   return cos_sin + (size_t)pos * rot;
 }
 
-template <bool kF16, int kLanes>
+// Heads h0 ... of one row (of q_heads queries, then kv_heads keys) through norm and rotation.
+template <bool kF16, int kLanes, bool kPaired>
+__device__ __forceinline__ void turn_heads(const QkParams& p, int row, bool live, int h0, int l, const Turn<kPaired>& t) {
+  constexpr int D = 8 * kLanes;
+  const int heads = p.q_heads + p.kv_heads;
+  for (int b = 0; b < p.batches; ++b, h0 += kQkHeads) {
+    uint4 raw[kQkHeads];
+#pragma unroll
+    for (int i = 0; i < kQkHeads; ++i) {
+      const int h = h0 + i;
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (live && h < heads)
+        raw[i] = load_head<kLanes, kPaired>(h < p.q_heads ? p.q + row * p.q_stride + h * D : p.k + row * p.k_stride + (h - p.q_heads) * D, l);
+    }
+#pragma unroll
+    for (int i = 0; i < kQkHeads; ++i) {
+      const int h = h0 + i;
+      const bool is_q = h < p.q_heads;
+      const uint16_t* gamma = is_q ? p.gamma_q : p.gamma_k;
+      float x[8], g[8];
+      unpack8<kF16>(raw[i], x);
+      if (gamma) unpack8<kF16>(load_head<kLanes, kPaired>(gamma, l), g);
+      norm_turn<kLanes, kPaired>(x, gamma ? g : nullptr, p.eps, t, l, p.rot, p.interleaved != 0);
+      if (live && h < heads)
+        store_head<kLanes, kPaired>(is_q ? p.q_out + row * p.q_out_stride + h * D : p.k_out + row * p.k_out_stride + (h - p.q_heads) * D,
+                                    l, pack8<kF16>(x));
+    }
+  }
+}
+
+template <bool kF16, int kLanes, bool kPaired>
 __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const __grid_constant__ QkParams p) {
   pdl_trigger();
   pdl_wait();
@@ -65,38 +104,11 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const __grid_c
   const int l = threadIdx.x % kLanes;
   const int row = blockIdx.x * kGroups + threadIdx.x / kLanes;
   const bool live = row < p.tokens;
-  const int heads = p.q_heads + p.kv_heads;
-  const int h0 = blockIdx.y * kQkHeads;
-  constexpr int D = 8 * kLanes;
-  uint4 raw[kQkHeads];
-#pragma unroll
-  for (int i = 0; i < kQkHeads; ++i) {
-    const int h = h0 + i;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (live && h < heads) {
-      const uint16_t* src = h < p.q_heads ? p.q + row * p.q_stride + h * D : p.k + row * p.k_stride + (h - p.q_heads) * D;
-      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * l);
-    }
-  }
-  Turn t;
-  if (p.rot > 0) {
-    load_turn(turn_row(p.cos_sin, live ? __ldg(p.positions + row) : 0, p.rot, p.max_pos, p.status), l, p.rot,
-              p.interleaved != 0, t);
-  }
-#pragma unroll
-  for (int i = 0; i < kQkHeads; ++i) {
-    const int h = h0 + i;
-    const bool is_q = h < p.q_heads;
-    const uint16_t* gamma = is_q ? p.gamma_q : p.gamma_k;
-    float x[8], g[8];
-    unpack8<kF16>(raw[i], x);
-    if (gamma) unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(gamma) + l), g);
-    norm_turn<kLanes>(x, gamma ? g : nullptr, p.eps, t, l, p.rot, p.interleaved != 0);
-    if (live && h < heads) {
-      uint16_t* dst = is_q ? p.q_out + row * p.q_out_stride + h * D : p.k_out + row * p.k_out_stride + (h - p.q_heads) * D;
-      *reinterpret_cast<uint4*>(dst + 8 * l) = pack8<kF16>(x);
-    }
-  }
+  Turn<kPaired> t;
+  if (p.rot > 0)
+    load_turn<kPaired>(turn_row(p.cos_sin, live ? __ldg(p.positions + row) : 0, p.rot, p.max_pos, p.status), l, p.rot,
+                       p.interleaved != 0, t);
+  turn_heads<kF16, kLanes, kPaired>(p, row, live, blockIdx.y * kQkHeads * p.batches, l, t);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -124,11 +136,37 @@ __device__ __forceinline__ uint32_t hold(float x, float s) {
   return (uint32_t)((int)(x != x ? 0.f : q) + 128);
 }
 
-// CTAs of page_tokens * D / 32 threads (at most 32 kLanes).  A page's CTA: the new tokens of one page, one kv head, keys
-// or values; thread (group g, lane l) takes elements 8 l ... of the page's slots g + i * groups.  A
-// query CTA: one row a lane group, kQkHeads heads.
-template <bool kF16, int kLanes>
-__global__ void __launch_bounds__(32 * kLanes) kv8_append_kernel(const __grid_constant__ AppendParams p) {
+// hold() of eight values.  A division takes a dozen instructions, and its last bit matters only next to a half:
+// x * (1 / s) is within 127 (2^-23 + 2^-24) < 3e-5 of the rounded quotient, so where it is further than 1e-4 from
+// every half, the nearest whole number is hold()'s (adding 1.5 * 2^23 leaves it in the low bits).  The others
+// (about 2 in 10^4), infinities, NaN, and scales whose reciprocal leaves fp32 go the long way.  inv = 1 / s.
+__device__ __forceinline__ uint2 hold8(const float (&x)[8], float s, float inv) {
+  uint32_t b[8];
+  bool sure = s > 1e-37f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = __fmul_rn(x[i], inv);
+    const float n = __fadd_rn(q, 12582912.f);
+    sure = sure && fabsf(__fsub_rn(q, __fsub_rn(n, 12582912.f))) < 0.4999f;
+    b[i] = __float_as_uint(n);
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    w[y] = __byte_perm(__byte_perm(b[4 * y], b[4 * y + 1], 0x0040), __byte_perm(b[4 * y + 2], b[4 * y + 3], 0x0040), 0x5410) ^ 0x80808080u;
+  if (!sure) {
+    w[0] = w[1] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i >> 2] |= hold(x[i], s) << (8 * (i & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// CTAs of page_tokens * D / 32 threads (at most 32 kLanes).  A page's CTA: the new tokens of one page, one
+// kv head, keys or values; thread (group g, lane l) takes a lane's values of the page's slots g + i * groups.  A
+// query CTA: one row a lane group.  (Two CTAs of the widest page on an SM, four of half of it: 64 registers.)
+template <bool kF16, int kLanes, bool kPaired>
+__global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_kernel(const __grid_constant__ AppendParams p) {
   pdl_trigger();
   pdl_wait();
   constexpr int D = 8 * kLanes;
@@ -141,15 +179,8 @@ __global__ void __launch_bounds__(32 * kLanes) kv8_append_kernel(const __grid_co
     // Queries: norm and rotation at the slots' positions.
     const int qb = blockIdx.x - p.page_blocks;
     const int row = (qb / p.q_chunks) * groups + g;
-    const int h0 = (qb % p.q_chunks) * kQkHeads;
     const bool live = row < p.step.tokens;
-    uint4 raw[kQkHeads];
-#pragma unroll
-    for (int i = 0; i < kQkHeads; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (live && h0 + i < c.q_heads) raw[i] = *reinterpret_cast<const uint4*>(c.q + row * c.q_stride + (h0 + i) * D + 8 * l);
-    }
-    Turn t;
+    Turn<kPaired> t;
     if (c.rot > 0) {
       int pos = 0;
       if (live) {
@@ -166,18 +197,11 @@ __global__ void __launch_bounds__(32 * kLanes) kv8_append_kernel(const __grid_co
           pos = __ldg(p.step.kv_len + lo) - (__ldg(p.step.row0 + lo + 1) - row);
         }
       }
-      load_turn(turn_row(c.cos_sin, pos, c.rot, c.max_pos, c.status), l, c.rot, c.interleaved != 0, t);
+      load_turn<kPaired>(turn_row(c.cos_sin, pos, c.rot, c.max_pos, c.status), l, c.rot, c.interleaved != 0, t);
     }
-    float gq[8];
-    if (c.gamma_q) unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(c.gamma_q) + l), gq);
-#pragma unroll
-    for (int i = 0; i < kQkHeads; ++i) {
-      float x[8];
-      unpack8<kF16>(raw[i], x);
-      norm_turn<kLanes>(x, c.gamma_q ? gq : nullptr, c.eps, t, l, c.rot, c.interleaved != 0);
-      if (live && h0 + i < c.q_heads)
-        *reinterpret_cast<uint4*>(c.q_out + row * c.q_out_stride + (h0 + i) * D + 8 * l) = pack8<kF16>(x);
-    }
+    QkParams q = c;
+    q.kv_heads = 0;   // the keys go into the cache
+    turn_heads<kF16, kLanes, kPaired>(q, row, live, (qb % p.q_chunks) * kQkHeads * c.batches, l, t);
     return;
   }
 
@@ -209,23 +233,27 @@ __global__ void __launch_bounds__(32 * kLanes) kv8_append_kernel(const __grid_co
   const bool norm = !is_v && c.gamma_k != nullptr;
   const int rot = is_v ? 0 : c.rot;
   float gk[8];
-  if (norm) unpack8<kF16>(__ldg(reinterpret_cast<const uint4*>(c.gamma_k) + l), gk);
+  if (norm) unpack8<kF16>(load_head<kLanes, kPaired>(c.gamma_k, l), gk);
+  uint4 raw[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int t = g + i * groups;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (t >= lo && t < hi) raw[i] = load_head<kLanes, kPaired>(src + (s.row0 + pg * P + t - first_slot) * stride + h * D, l);
+  }
   float x[kHeld][8];
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int t = g + i * groups;
     const bool mine = t >= lo && t < hi;
-    const int row = s.row0 + pg * P + t - first_slot;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (mine) raw = *reinterpret_cast<const uint4*>(src + row * stride + h * D + 8 * l);
-    unpack8<kF16>(raw, x[i]);
-    Turn turn;
+    unpack8<kF16>(raw[i], x[i]);
+    Turn<kPaired> turn;
     if (rot > 0) {
-      const int pos = !mine ? 0 : c.positions ? __ldg(c.positions + row) : pg * P + t;
-      load_turn(turn_row(c.cos_sin, pos, rot, c.max_pos, c.status), l, rot, c.interleaved != 0, turn);
+      const int pos = !mine ? 0 : c.positions ? __ldg(c.positions + s.row0 + pg * P + t - first_slot) : pg * P + t;
+      load_turn<kPaired>(turn_row(c.cos_sin, pos, rot, c.max_pos, c.status), l, rot, c.interleaved != 0, turn);
     }
-    norm_turn<kLanes>(x[i], norm ? gk : nullptr, c.eps, turn, l, rot, c.interleaved != 0);
+    norm_turn<kLanes, kPaired>(x[i], norm ? gk : nullptr, c.eps, turn, l, rot, c.interleaved != 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[i][j]));
   }
@@ -238,25 +266,20 @@ __global__ void __launch_bounds__(32 * kLanes) kv8_append_kernel(const __grid_co
   const float now = fmaxf(old, fresh);
   const bool again = lo > 0 && now > old;   // the earlier tokens are held at a new scale
   if (threadIdx.x == 0) *scale = now;
+  const float inv = __fdiv_rn(1.0f, now);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int t = g + i * groups;
-    uint2* const dst = reinterpret_cast<uint2*>(bytes + (size_t)t * D + 8 * l);
+    uint8_t* const dst = bytes + (size_t)t * D;
     if (t >= lo && t < hi) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j >> 2] |= hold(x[i][j], now) << (8 * (j & 3));
-      *dst = make_uint2(w[0], w[1]);
+      store_bytes<kLanes, kPaired>(dst, l, hold8(x[i], now, inv));
     } else if (again && t < lo) {
-      const uint2 was = *dst;
+      const uint2 was = load_bytes<kLanes, kPaired>(dst, l);
       const uint32_t u[2] = {was.x, was.y};
-      uint32_t w[2] = {0u, 0u};
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float v = (float)((int)((u[j >> 2] >> (8 * (j & 3))) & 0xFFu) - 128);
-        w[j >> 2] |= hold(__fmul_rn(v, old), now) << (8 * (j & 3));
-      }
-      *dst = make_uint2(w[0], w[1]);
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn((float)((int)((u[j >> 2] >> (8 * (j & 3))) & 0xFFu) - 128), old);
+      store_bytes<kLanes, kPaired>(dst, l, hold8(v, now, inv));
     }
   }
 }
@@ -399,11 +422,14 @@ static cudaError_t launch(void (*kernel)(const P), dim3 grid, int threads, const
 template <typename P>
 using Kernel = void (*)(const P);
 
-// The instance for a type and a head size.
-#define KV8_PICK(name, P, f16, dim)                                                                     \
-  ((dim) == 64 ? ((f16) ? (Kernel<P>)name<true, 8> : (Kernel<P>)name<false, 8>)                          \
-   : (dim) == 128 ? ((f16) ? (Kernel<P>)name<true, 16> : (Kernel<P>)name<false, 16>)                     \
-                  : ((f16) ? (Kernel<P>)name<true, 32> : (Kernel<P>)name<false, 32>))
+// The instance for a type and a head size; ...: further template arguments.
+#define KV8_PICK(name, P, f16, dim, ...)                                                                                  \
+  ((dim) == 64 ? ((f16) ? (Kernel<P>)name<true, 8, ##__VA_ARGS__> : (Kernel<P>)name<false, 8, ##__VA_ARGS__>)              \
+   : (dim) == 128 ? ((f16) ? (Kernel<P>)name<true, 16, ##__VA_ARGS__> : (Kernel<P>)name<false, 16, ##__VA_ARGS__>)         \
+                  : ((f16) ? (Kernel<P>)name<true, 32, ##__VA_ARGS__> : (Kernel<P>)name<false, 32, ##__VA_ARGS__>))
+
+// Whether a lane can hold whole pairs (load_head).
+static bool paired(const QkParams& c, int head_dim) { return c.rot == head_dim && !c.interleaved; }
 
 }  // namespace w8a8
 
@@ -437,9 +463,13 @@ extern "C" int qk_norm_rope(const qk_prep_t* prep, const void* q, long long q_st
   c.q_heads = q_heads, c.kv_heads = kv_heads, c.tokens = tokens;
   c.status = static_cast<uint32_t*>(ws);
   const int groups = kQkThreads / (head_dim / 8);
-  const dim3 grid((unsigned)((tokens + groups - 1) / groups), (unsigned)((q_heads + kv_heads + kQkHeads - 1) / kQkHeads));
-  const cudaError_t e = launch<QkParams>(KV8_PICK(qk_norm_rope_kernel, QkParams, dtype == KV8_F16, head_dim), grid, kQkThreads,
-                                         c, static_cast<cudaStream_t>(stream));
+  c.batches = batches_of(q_heads + kv_heads, tokens);
+  const int chunk = kQkHeads * c.batches;
+  const dim3 grid((unsigned)((tokens + groups - 1) / groups), (unsigned)((q_heads + kv_heads + chunk - 1) / chunk));
+  const bool f16 = dtype == KV8_F16;
+  const cudaError_t e = launch<QkParams>(paired(c, head_dim) ? KV8_PICK(qk_norm_rope_kernel, QkParams, f16, head_dim, true)
+                                                             : KV8_PICK(qk_norm_rope_kernel, QkParams, f16, head_dim, false),
+                                         grid, kQkThreads, c, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "qk_norm_rope");
 }
 
@@ -482,11 +512,14 @@ extern "C" int kv8_append(const kv8_cache_t* cache, const kv8_step_t* step, cons
   p.seq_pages = kv8_pages_of(step->max_tokens, cache->page_tokens);
   const long long page_blocks = 2ll * step->seqs * p.seq_pages * cache->kv_heads;
   const int threads = cache->page_tokens * D / 32, groups = threads / (D / 8);
-  p.q_chunks = (q_heads + kQkHeads - 1) / kQkHeads;
+  p.qk.batches = batches_of(q_heads, step->tokens);
+  p.q_chunks = (q_heads + kQkHeads * p.qk.batches - 1) / (kQkHeads * p.qk.batches);
   const long long blocks = page_blocks + (long long)p.q_chunks * ((step->tokens + groups - 1) / groups);
   if (blocks > 0x7fffffffll) return W8A8_ERR_INVALID_ARG;
   p.page_blocks = (int)page_blocks;
-  const cudaError_t e = launch<AppendParams>(KV8_PICK(kv8_append_kernel, AppendParams, dtype == KV8_F16, D),
+  const bool f16 = dtype == KV8_F16;
+  const cudaError_t e = launch<AppendParams>(paired(p.qk, D) ? KV8_PICK(kv8_append_kernel, AppendParams, f16, D, true)
+                                                             : KV8_PICK(kv8_append_kernel, AppendParams, f16, D, false),
                                              dim3((unsigned)blocks), threads, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_append");
 }
