@@ -181,7 +181,11 @@ def _stream(stream):
     if stream is None:
         import torch
 
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        # The handle of torch.cuda.current_stream() (making that object costs 3 us, a third of a small call).
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -488,7 +492,7 @@ class KV8Cache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, page_tokens, dim
         self.c = KV8CacheT(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads, page_tokens, dim)
-        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+        self.addr = ctypes.addressof(self.c)
 
 
 def kv8_cache(pages: int, kv_heads: int, page_tokens: int, head_dim: int, device="cuda") -> KV8Cache:
@@ -518,7 +522,7 @@ class KV8Step:
         self.row0, self.kv_len, self.page_table = row0, kv_len, page_table
         self.tokens = tokens
         self.c = KV8StepT(row0.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), seqs, tokens, max_tokens, width)
-        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+        self.addr = ctypes.addressof(self.c)
 
 
 class QKPrep:
@@ -543,7 +547,7 @@ class QKPrep:
             raise ValueError(f"gamma_k: expected {self.dtype}, got {gamma_k.dtype}")
         self.c = QKPrepT(gamma_q.data_ptr() if gamma_q is not None else None, gamma_k.data_ptr() if gamma_k is not None else None,
                          cos_sin.data_ptr() if rot_dim > 0 else None, float(eps), rot_dim, max_pos, int(interleaved))
-        self._as_parameter_ = ctypes.c_void_p(ctypes.addressof(self.c))
+        self.addr = ctypes.addressof(self.c)
 
     def check(self, dtype, head_dim):
         if self.dtype is not None and (self.dtype != dtype or self.gamma_len < head_dim):
@@ -600,22 +604,20 @@ def kv8_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
 def qk_norm_rope(prep, q, k, positions, ws, q_out=None, k_out=None, stream=None):
     """(q, k) [tokens, heads, head_dim] through `prep` at `positions` [tokens] int32; q_out = q and k_out = k work in
     place."""
-    import torch
-
     rows, q_heads, dim = q.shape
     kv_heads = k.shape[1]
-    dt = _kv8_dtype(q, "q")
+    dt, dtype = _kv8_dtype(q, "q"), q.dtype
     if q_out is None:
-        q_out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
+        q_out = q.new_empty((rows, q_heads, dim))
     if k_out is None:
-        k_out = torch.empty((rows, kv_heads, dim), dtype=q.dtype, device=q.device)
-    prep.check(q.dtype, dim)
-    qs, ks = _heads(q, "q", rows, q_heads, dim, q.dtype), _heads(k, "k", rows, kv_heads, dim, q.dtype)
-    qo, ko = _heads(q_out, "q_out", rows, q_heads, dim, q.dtype), _heads(k_out, "k_out", rows, kv_heads, dim, q.dtype)
+        k_out = q.new_empty((rows, kv_heads, dim))
+    prep.check(dtype, dim)
+    qs, ks = _heads(q, "q", rows, q_heads, dim, dtype), _heads(k, "k", rows, kv_heads, dim, dtype)
+    qo, ko = _heads(q_out, "q_out", rows, q_heads, dim, dtype), _heads(k_out, "k_out", rows, kv_heads, dim, dtype)
     pos = _positions(positions, rows)
     wp, wn = _ws(ws)
     _on_cuda(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out, ws=ws)
-    rc = lib().qk_norm_rope(prep, q.data_ptr(), qs, q_heads, k.data_ptr(), ks, kv_heads, dim, pos, rows, q_out.data_ptr(), qo,
+    rc = lib().qk_norm_rope(prep.addr, q.data_ptr(), qs, q_heads, k.data_ptr(), ks, kv_heads, dim, pos, rows, q_out.data_ptr(), qo,
                             k_out.data_ptr(), ko, dt, wp, wn, _stream(stream))
     _check("qk_norm_rope", rc)
     return q_out, k_out
@@ -624,27 +626,25 @@ def qk_norm_rope(prep, q, k, positions, ws, q_out=None, k_out=None, stream=None)
 def kv8_append(cache, step, prep, k, v, ws, q=None, q_out=None, positions=None, stream=None):
     """Append k, v [tokens, kv_heads, head_dim] of the step to the cache, k through `prep` (None: as it is); q
     [tokens, q_heads, head_dim] goes through `prep` into q_out, which is returned (None without q)."""
-    import torch
-
     rows, heads, dim = step.tokens, cache.kv_heads, cache.head_dim
-    dt = _kv8_dtype(k, "k")
-    ks, vs = _heads(k, "k", rows, heads, dim, k.dtype), _heads(v, "v", rows, heads, dim, k.dtype)
+    dt, dtype = _kv8_dtype(k, "k"), k.dtype
+    ks, vs = _heads(k, "k", rows, heads, dim, dtype), _heads(v, "v", rows, heads, dim, dtype)
     if prep is not None:
-        prep.check(k.dtype, dim)
+        prep.check(dtype, dim)
     q_heads = qs = qo = 0
     qp = qop = None
     if q is not None:
         q_heads = q.shape[1]
         if q_out is None:
-            q_out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
-        qs, qo = _heads(q, "q", rows, q_heads, dim, k.dtype), _heads(q_out, "q_out", rows, q_heads, dim, k.dtype)
+            q_out = q.new_empty((rows, q_heads, dim))
+        qs, qo = _heads(q, "q", rows, q_heads, dim, dtype), _heads(q_out, "q_out", rows, q_heads, dim, dtype)
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out: given without q")
     pos = _positions(positions, rows)
     wp, wn = _ws(ws)
     _on_cuda(k=k, v=v, q=q, q_out=q_out, positions=positions, ws=ws)
-    rc = lib().kv8_append(cache, step, prep, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, q_heads, qop, qo, pos, dt, wp, wn,
+    rc = lib().kv8_append(cache.addr, step.addr, prep.addr if prep is not None else None, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, q_heads, qop, qo, pos, dt, wp, wn,
                           _stream(stream))
     _check("kv8_append", rc)
     return q_out
@@ -653,21 +653,19 @@ def kv8_append(cache, step, prep, k, v, ws, q=None, q_out=None, positions=None, 
 def kv8_attention(cache, step, q, ws, out=None, lse=None, scale=None, window: int = 0, flags: int = 0, stream=None):
     """softmax(scale q k^T) v of q [tokens, q_heads, head_dim] over the cache -> out (the same shape); lse fp32
     [tokens, q_heads] is filled if given.  scale defaults to 1 / sqrt(head_dim)."""
-    import torch
-
     rows, dim = step.tokens, cache.head_dim
-    dt = _kv8_dtype(q, "q")
+    dt, dtype = _kv8_dtype(q, "q"), q.dtype
     q_heads = q.shape[1]
     if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
-    qs, os_ = _heads(q, "q", rows, q_heads, dim, q.dtype), _heads(out, "out", rows, q_heads, dim, q.dtype)
+        out = q.new_empty((rows, q_heads, dim))
+    qs, os_ = _heads(q, "q", rows, q_heads, dim, dtype), _heads(out, "out", rows, q_heads, dim, dtype)
     lp = None
     if lse is not None:
         _dev(lse, "lse", 4 * rows * q_heads, esize=4)
         lp = lse.data_ptr()
     wp, wn = _ws(ws)
     _on_cuda(q=q, out=out, lse=lse, ws=ws)
-    rc = lib().kv8_attention(cache, step, q.data_ptr(), qs, q_heads, out.data_ptr(), os_, lp,
+    rc = lib().kv8_attention(cache.addr, step.addr, q.data_ptr(), qs, q_heads, out.data_ptr(), os_, lp,
                              dim ** -0.5 if scale is None else scale, window, flags, dt, wp, wn, _stream(stream))
     _check("kv8_attention", rc)
     return out
@@ -686,5 +684,5 @@ def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
     ks, vs = _heads(k_out, "k_out", rows, heads, dim, k_out.dtype), _heads(v_out, "v_out", rows, heads, dim, k_out.dtype)
     wp, wn = _ws(ws)
     _on_cuda(k_out=k_out, v_out=v_out, ws=ws)
-    _check("kv8_read", lib().kv8_read(cache, step, k_out.data_ptr(), ks, v_out.data_ptr(), vs, dt, wp, wn, _stream(stream)))
+    _check("kv8_read", lib().kv8_read(cache.addr, step.addr, k_out.data_ptr(), ks, v_out.data_ptr(), vs, dt, wp, wn, _stream(stream)))
     return k_out, v_out
