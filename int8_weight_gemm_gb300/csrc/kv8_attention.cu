@@ -62,6 +62,10 @@ struct Layout {
   static constexpr bool kQShared = D * NT > 256;
   static constexpr int kQBytes = kQShared ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int kSmem = 1024 + kRing + kQBytes;
+  // Whether the next granule's scores are worked out beside this one's weights and sums, two independent streams
+  // of instructions: where there are registers for both.  (D = 128, one tile: 64 long contexts 150.4 -> 145.7 us;
+  // 24 rows 43.7 -> 46.6, D = 64 28.4 -> 30.0.)
+  static constexpr bool kAhead = D == 128 && NT == 1;
   static constexpr int kRow = D + 4;                    // floats of a row in the join buffer
   // What an item costs beside its tokens (queries, first copies, join), in units: each item's place in
   // the split is that much longer, so a run that crosses into another item gets fewer tokens.
@@ -107,7 +111,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     long long u;
   } start_sm;
   __shared__ float4 mlr_sm[kWarps][L::kRows];   // (m, l, r, -) of each warp's rows
-  __shared__ float2 qstat_sm[L::kQShared ? L::kRows : 1];   // (multiplier, offset) of each row
+  __shared__ float4 row_st[L::kRows];   // of each row: score multiplier, offset, first and one past the last token it sees
+  __shared__ int2 range_sm[NT];
   __shared__ int last_sm, abort_flag;
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint2* const qsm = reinterpret_cast<uint2*>(ring + L::kRing);   // [NT][kSteps][32] fragments
@@ -242,8 +247,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     // d0 + 1, d0 + 3, d0 = the first of the lane's word s: the order in which a key's four bytes come
     // apart.  A lane's words: D / 4 contiguous values (D = 256: 32 of each half).
     uint32_t qb[L::kQShared ? 1 : NT][kSteps][2];
-    float rowmul[NT][2], offs[NT][2], m[NT][2], l[NT][2], r[NT][2], hs[NT][2];
-    int beg[NT][2], end[NT][2];
+    float m[NT][2], l[NT][2], r[NT][2], hs[NT][2];
     int full_lo = 0, full_hi = 0x7fffffff;   // tokens that every row sees
     // The loads of the queries go out before the first copies of the cache, which would delay them by
     // everything that the rings hold.
@@ -269,7 +273,6 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       for (int j = 0; j < NS; ++j)
         if (j < mine_n) issue(j);
     }
-    float mul_r[kMine], of_r[kMine];
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       if (L::kQShared && warp >= NT) break;
@@ -312,38 +315,42 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       // score (in powers of two) = (acc - offs) * rowmul * k_scale
-      of_r[i] = sum * (128.f / 16777216.f);
-      mul_r[i] = p.scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 + ex) << 23);
-      if (L::kQShared && c == 0) qstat_sm[(L::kQShared ? warp * 8 : 0) + g] = make_float2(mul_r[i], of_r[i]);
+      // The row's own: by one lane of one warp (every warp works out the same where it holds all tiles).
+      const int row = (L::kQShared ? warp : i) * 8 + g;
+      const bool live = row < rows_left;
+      const int pos = x.s.len - x.s.n + (tile * L::kRows + row) / p.group;
+      const int end = !live ? 0x7fffffff : p.causal ? min(pos + 1, x.s.len) : x.s.len;
+      const int beg = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      if (c == 0 && (L::kQShared || warp == 0))
+        row_st[row] = make_float4(p.scale_log2 * 16777216.f * __uint_as_float((uint32_t)(127 + ex) << 23), sum * (128.f / 16777216.f),
+                                  __int_as_float(beg), __int_as_float(end));
+      full_hi = min(full_hi, end);
+      full_lo = max(full_lo, beg);
     }
-    if (L::kQShared) __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {   // this lane's scores are of rows 2c and 2c + 1
-        if (L::kQShared) {
-          const float2 t = qstat_sm[L::kQShared ? i * 8 + 2 * c + e : 0];
-          rowmul[i][e] = t.x;
-          offs[i][e] = t.y;
-        } else {
-          rowmul[i][e] = __shfl_sync(0xffffffffu, mul_r[L::kQShared ? 0 : i], 4 * (2 * c + e));
-          offs[i][e] = __shfl_sync(0xffffffffu, of_r[L::kQShared ? 0 : i], 4 * (2 * c + e));
-        }
+      for (int e = 0; e < 2; ++e) {
         m[i][e] = kFloor;
         r[i][e] = kFloor;
         l[i][e] = 0.f;
         hs[i][e] = 0.f;
-        const int row = i * 8 + 2 * c + e;
-        const bool live = row < rows_left;
-        const int pos = x.s.len - x.s.n + (tile * L::kRows + row) / p.group;
-        end[i][e] = !live ? 0x7fffffff : p.causal ? min(pos + 1, x.s.len) : x.s.len;
-        beg[i][e] = live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
-        full_hi = min(full_hi, end[i][e]);
-        full_lo = max(full_lo, beg[i][e]);
       }
     }
     full_hi = __reduce_min_sync(0xffffffffu, full_hi);
     full_lo = __reduce_max_sync(0xffffffffu, full_lo);
+    if (L::kQShared) {
+      // A warp has seen its own tile's rows alone.
+      if (lane == 0 && warp < NT) range_sm[warp] = make_int2(full_lo, full_hi);
+    }
+    __syncthreads();
+    if (L::kQShared) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        full_lo = max(full_lo, range_sm[i].x);
+        full_hi = min(full_hi, range_sm[i].y);
+      }
+    }
     float o[NT][kSteps][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -353,29 +360,14 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
         for (int k = 0; k < 4; ++k) o[i][n][k] = 0.f;
 
     // ---------------------------------------------------------------- the granules
-    for (int j = 0; j < mine_n && !dead; ++j) {
+    // Scores (before their scales) of granule j: tokens T + g and T + g + 8, rows 2c and 2c + 1 of each tile; two
+    // chains of products where one tile alone would wait for each of its own.  False when the wait ran out.
+    constexpr int kChains = NT == 1 ? 2 : 1;
+    auto scores = [&](int j, float (&s)[NT][kChains][4]) {
       const uint32_t slot = (count + (uint32_t)j) % NS, phase = ((count + (uint32_t)j) / NS) & 1u;
       const uint8_t* const kst = stage0 + slot * L::kStage;
-      const uint8_t* const vst = kst + L::kSide;
       const bool got = mbar_wait(&bar[slot], phase, &abort_flag, p.status);
-      if (!__all_sync(0xffffffffu, got)) {
-        // A wait ran out (recorded in the status word).  The copies in flight land before this CTA's
-        // shared memory is given back; no more are issued.
-        dead = true;
-        for (int i = j; i < min(j + NS, mine_n); ++i)
-          mbar_wait_drain(&bar[(count + (uint32_t)i) % NS], ((count + (uint32_t)i) / NS) & 1u, p.status);
-        break;
-      }
-      const int T = T0 + (warp + j * kWarps) * kGranule;
-      const int par = (j >> 5) & 1;
-      const float ks = __shfl_sync(0xffffffffu, par ? ks_r[1] : ks_r[0], j & 31);
-      const float vs = __shfl_sync(0xffffffffu, par ? vs_r[1] : vs_r[0], j & 31);
-      const bool bad = ((par ? bad_r[1] : bad_r[0]) >> (j & 31)) & 1u;
-
-      // Scores of tokens T + g and T + g + 8, rows 2c and 2c + 1 of each tile: two chains of products
-      // where one tile alone would wait for each of its own.
-      constexpr int kChains = NT == 1 ? 2 : 1;
-      float s[NT][kChains][4];
+      if (!__all_sync(0xffffffffu, got)) return false;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -406,6 +398,37 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
           }
         }
       }
+      return true;
+    };
+    // A wait that runs out is recorded in the status word.  The copies in flight land before this CTA's shared
+    // memory is given back; no more are issued.
+    auto give_up = [&](int j) {
+      dead = true;
+      for (int i = j; i < min(j + NS, mine_n); ++i)
+        mbar_wait_drain(&bar[(count + (uint32_t)i) % NS], ((count + (uint32_t)i) / NS) & 1u, p.status);
+    };
+    float sn[NT][kChains][4];
+    if (L::kAhead && mine_n > 0 && !dead && !scores(0, sn)) give_up(0);
+    for (int j = 0; j < mine_n && !dead; ++j) {
+      if (!L::kAhead && !scores(j, sn)) {
+        give_up(j);
+        break;
+      }
+      const uint8_t* const vst = stage0 + ((count + (uint32_t)j) % NS) * L::kStage + L::kSide;
+      const int T = T0 + (warp + j * kWarps) * kGranule;
+      const int par = (j >> 5) & 1;
+      const float ks = __shfl_sync(0xffffffffu, par ? ks_r[1] : ks_r[0], j & 31);
+      const float vs = __shfl_sync(0xffffffffu, par ? vs_r[1] : vs_r[0], j & 31);
+      const bool bad = ((par ? bad_r[1] : bad_r[0]) >> (j & 31)) & 1u;
+      float s[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[i][k] = kChains == 2 ? sn[i][0][k] + sn[i][kChains - 1][k] : sn[i][0][k];
+      if (L::kAhead && j + 1 < mine_n && !scores(j + 1, sn)) {
+        give_up(j + 1);
+        break;
+      }
       const bool edge = T < full_lo || T + kGranule > full_hi || bad;
       const float lvs = lg2(vs);
       uint32_t pb[NT][2];
@@ -415,19 +438,16 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
         bool move = false, far = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float c1 = ks * rowmul[i][e];
-          const float c0 = -offs[i][e] * c1;
+          const float4 st = row_st[8 * i + 2 * c + e];
+          const float c1 = ks * st.x;
+          const float c0 = -st.y * c1;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            float a = s[i][0][2 * t + e];
-            if (kChains == 2) a += s[i][kChains - 1][2 * t + e];
-            z[2 * t + e] = fmaf(a, c1, c0);
-          }
+          for (int t = 0; t < 2; ++t) z[2 * t + e] = fmaf(s[i][2 * t + e], c1, c0);
           if (edge) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int tok = T + 8 * t + g;
-              if (bad || tok < beg[i][e] || tok >= end[i][e]) z[2 * t + e] = -INFINITY;
+              if (bad || tok < __float_as_int(st.z) || tok >= __float_as_int(st.w)) z[2 * t + e] = -INFINITY;
             }
           }
           mx[e] = fmaxf(z[e], z[2 + e]);
