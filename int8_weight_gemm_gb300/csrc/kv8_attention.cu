@@ -44,19 +44,19 @@ namespace w8a8 {
 namespace attn {
 
 // NT: 8-row tiles a warp holds.  A lane holds D NT / 4 sums, so the warps that an SM can hold follow
-// from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in two CTAs.
+// from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in CTAs of four.
 template <int D, int NT>
 struct Layout {
-  static constexpr int kWarps = D * NT <= 128 ? 8 : D * NT <= 256 ? 6 : 4;
+  static constexpr int kWarps = D * NT == 128 && NT == 1 ? 8 : 4;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtas = 2;                       // CTAs on an SM
+  static constexpr int kCtas = (D * NT <= 128 ? 16 : D * NT <= 256 ? 12 : 8) / kWarps;   // CTAs on an SM
   static constexpr int kUnit = kGranule * kWarps;       // tokens of the split's unit
   static constexpr int kRows = 8 * NT;
   static constexpr int kBoxes = D > 128 ? D / 128 : 1;
   static constexpr int kBoxBytes = kGranule * (D > 128 ? 128 : D);
   static constexpr int kSide = kBoxes * kBoxBytes;      // keys (or values) of a granule
   static constexpr int kStage = 2 * kSide;
-  static constexpr int kStages = 98304 / (kWarps * kStage);   // a warp's ring
+  static constexpr int kStages = 196608 / (kCtas * kWarps * kStage);   // a warp's ring
   static constexpr int kRing = kWarps * kStages * kStage;
   // The queries' fragments are the same for every warp: in shared memory where registers are short.
   static constexpr bool kQShared = D * NT > 256;
@@ -74,7 +74,7 @@ struct Layout {
   static constexpr int kPart = kRows * (D + 4);
   static_assert(kWarps * kRows * kRow * 4 <= kRing, "the join buffer lies over the rings");
   static_assert(kStages >= 2 && kStages <= 16, "ring depth");
-  static_assert(kCtas * (kSmem + 4096) <= 232448, "shared memory of an SM");
+  static_assert(kCtas * (kSmem + 5120) <= 232448, "shared memory of an SM");
 };
 
 // Transpose of an 8 x 8 matrix of 16-bit values held as two of row lane / 4 by each lane.
@@ -597,121 +597,101 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       }
     }
     if (!whole) {
-      // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.
+      // The part is written.  The item's parts (one of each of n consecutive CTAs) join in the CTAs' order: up to
+      // kGroup of them by the last CTA to arrive; more of them first in groups of about sqrt(n), each by the last
+      // of its CTAs, so that no CTA reads more than a few (131071 tokens, 57 parts of 16 rows: 81.5 us without
+      // groups, 63.4 with them).
+      constexpr int kGroup = 8;
       const int first = runs.owner(item_u0 + L::kLead), n = runs.owner(item_u0 + x.span - 1) - first + 1;
-      // (The barrier orders the CTA's stores before thread 0's release, and its acquire before the reads.)
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const uint32_t old = atom_add_acq_rel_u32(p.counters + first, 1u);
-        if (old >= (uint32_t)n) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
-        if (old == (uint32_t)n - 1) p.counters[first] = 0u;   // ready for the next call
-        last_sm = old == (uint32_t)n - 1;
+      const int first_slot = item_u0 <= runs.begin(first) ? 0 : 1;
+      int group = n;
+      if (n > kGroup) {
+        group = kGroup;
+        while (group * group < n) ++group;
       }
-      __syncthreads();
-      if (last_sm) {
-        const int first_slot = item_u0 <= runs.begin(first) ? 0 : 1;
-        const float* const parts = p.parts + ((size_t)first * 2 + first_slot) * L::kPart;   // part i > 0: CTA first + i, slot 0
-        auto part_of = [&](int i) { return i == 0 ? parts : p.parts + (size_t)(first + i) * 2 * L::kPart; };
-        // As many rows at a time as have their statistics in shared memory: (m, l, r) of each part, then
-        // in their place the factor of its sums.
-        float4* const st = reinterpret_cast<float4*>(ring);
-        constexpr int kRoom = (L::kRing - kThreads * 16) / 16;
-        float4* const half = st + kRoom;   // [kThreads] sums to be added
-        __shared__ float4 row_sm[L::kRows];
-        const int chunk = min(rows, kRoom / n);
-        for (int r0 = 0; r0 < rows; r0 += chunk) {
-          const int nr = min(chunk, rows - r0);
-          for (int i = threadIdx.x; i < n * nr; i += kThreads) {
-            const int pi = i / nr, row = i - pi * nr;
-            st[row * n + pi] = __ldcg(reinterpret_cast<const float4*>(part_of(pi) + L::kRows * D) + r0 + row);
-          }
-          __syncthreads();
-          // Few parts: a thread for a row; many: a warp for a row.
-          const bool few = n <= 16;
-          for (int row = few ? threadIdx.x : warp; row < nr; row += few ? kThreads : kWarps) {
-            float M = kFloor, Rf = kFloor, lt = 0.f;
-            const int i0 = few ? 0 : lane, di = few ? 1 : 32;
-            for (int i = i0; i < n; i += di) {
-              M = fmaxf(M, st[row * n + i].x);
-              Rf = fmaxf(Rf, st[row * n + i].z);
-            }
-            if (!few) {
+      const int groups = (n + group - 1) / group;
+      // Part i: of CTA first + i, in its first place (the first CTA's: in the place of its last segment unless the
+      // item begins its run).
+      auto part_of = [&](int i) { return p.parts + ((size_t)(first + i) * 2 + (i == 0 ? first_slot : 0)) * L::kPart; };
+      const int mine = (int)blockIdx.x - first, lead = mine / group * group;
+      int base = lead, step = 1, count_n = min(group, n - lead);
+      uint32_t* counter = groups > 1 ? p.group_counters + 2 * (first + lead) + (lead == 0 ? first_slot : 0) : p.counters + first;
+      for (bool top = groups == 1;; top = true) {
+        // (The barrier orders the CTA's stores before thread 0's release, and its acquire before the reads.)
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          const uint32_t old = atom_add_acq_rel_u32(counter, 1u);
+          if (old >= (uint32_t)count_n) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
+          if (old == (uint32_t)count_n - 1) *counter = 0u;   // ready for the next call
+          last_sm = old == (uint32_t)count_n - 1;
+        }
+        __syncthreads();
+        if (!last_sm) break;
+        // Threads take four values of a row at kB places at once, kP parts of each in flight.
+        constexpr int kVec = D / 4, kPlaces = (L::kRows * kVec + kThreads - 1) / kThreads;
+        constexpr int kB = kPlaces < 2 ? 1 : 2, kP = kB == 1 && D * NT == 128 ? 8 : 4;
+        for (int at0 = threadIdx.x; at0 < rows * kVec; at0 += kB * kThreads) {
+          float M[kB], Rf[kB], lt[kB];
+          float4 acc[kB];
 #pragma unroll
-              for (int w = 16; w > 0; w >>= 1) {
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-                Rf = fmaxf(Rf, __shfl_xor_sync(0xffffffffu, Rf, w));
-              }
-            }
-            for (int i = i0; i < n; i += di) {
-              const float4 t = st[row * n + i];
-              lt += t.y * ex2(t.x - M);
-              st[row * n + i].x = ex2(t.z - Rf);
-            }
-            if (!few) {
+          for (int y = 0; y < kB; ++y) M[y] = kFloor, Rf[y] = kFloor, lt[y] = 0.f, acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = 0; i < count_n; i += kP) {
+            float4 t[kP][kB], v[kP][kB];
 #pragma unroll
-              for (int w = 16; w > 0; w >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, w);
-            }
-            if (few || lane == 0) row_sm[row] = make_float4(M, lt, Rf, 0.f);
-          }
-          __syncthreads();
-          // Threads take four values at each of kPlaces places; where the rows leave threads over, they
-          // share the parts.  Eight loads or more of a thread are in flight.
-          constexpr int kPlaces = (L::kRows * (D / 4) + kThreads - 1) / kThreads;
-          constexpr int kAhead = kPlaces >= 8 ? 1 : 8 / kPlaces;
-          const int places = nr * (D / 4);
-          const int share = places < kThreads ? kThreads / places : 1;
-          const int k = share > 1 ? (int)threadIdx.x / places : 0;
-          const int at0 = share > 1 ? (int)threadIdx.x - k * places : (int)threadIdx.x;
-          const int i1 = k < share ? n * (k + 1) / share : 0;
-          float4 acc[kPlaces];
+            for (int z = 0; z < kP; ++z) {
+              const float* const src = part_of(base + step * min(i + z, count_n - 1));
 #pragma unroll
-          for (int y = 0; y < kPlaces; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int i = n * k / share; i < i1; i += kAhead) {
-            float4 v[kAhead][kPlaces];
-#pragma unroll
-            for (int z = 0; z < kAhead; ++z)
-#pragma unroll
-              for (int y = 0; y < kPlaces; ++y) {
+              for (int y = 0; y < kB; ++y) {
                 const int at = at0 + y * kThreads;
+                t[z][y] = make_float4(kFloor, 0.f, kFloor, 0.f);
                 v[z][y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i + z < i1 && at < places) v[z][y] = __ldcg(reinterpret_cast<const float4*>(part_of(i + z) + r0 * D) + at);
-              }
-#pragma unroll
-            for (int z = 0; z < kAhead; ++z)
-#pragma unroll
-              for (int y = 0; y < kPlaces; ++y) {
-                const int at = at0 + y * kThreads;
-                if (i + z < i1 && at < places) {
-                  const float a = st[(at / (D / 4)) * n + i + z].x;
-                  acc[y].x = fmaf(v[z][y].x, a, acc[y].x), acc[y].y = fmaf(v[z][y].y, a, acc[y].y);
-                  acc[y].z = fmaf(v[z][y].z, a, acc[y].z), acc[y].w = fmaf(v[z][y].w, a, acc[y].w);
+                if (i + z < count_n && at < rows * kVec) {
+                  t[z][y] = __ldcg(reinterpret_cast<const float4*>(src + L::kRows * D) + at / kVec);
+                  v[z][y] = __ldcg(reinterpret_cast<const float4*>(src) + at);
                 }
               }
-          }
-          if (share > 1) {
-            half[threadIdx.x] = acc[0];
-            __syncthreads();
-            if (k == 0) {
-              for (int y = 1; y < share; ++y) {
-                const float4 v = half[y * places + at0];
-                acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
-              }
             }
-          }
-          if (k == 0) {
 #pragma unroll
-            for (int y = 0; y < kPlaces; ++y) {
-              const int at = at0 + y * kThreads;
-              if (at < places) {
-                const int row = at / (D / 4);
-                const float4 t = row_sm[row];
-                store_row<kF16>(p, x.s.row0, tile * L::kRows + r0 + row, h, 4 * (at % (D / 4)), D, acc[y], t.x, t.y, t.z);
+            for (int y = 0; y < kB; ++y) {
+              float mn = M[y], rn = Rf[y];
+#pragma unroll
+              for (int z = 0; z < kP; ++z) mn = fmaxf(mn, t[z][y].x), rn = fmaxf(rn, t[z][y].z);
+              const float a0 = ex2(Rf[y] - rn);
+              lt[y] *= ex2(M[y] - mn);
+              acc[y].x *= a0, acc[y].y *= a0, acc[y].z *= a0, acc[y].w *= a0;
+              M[y] = mn;
+              Rf[y] = rn;
+#pragma unroll
+              for (int z = 0; z < kP; ++z) {
+                lt[y] = fmaf(t[z][y].y, ex2(t[z][y].x - mn), lt[y]);
+                const float a = ex2(t[z][y].z - rn);
+                acc[y].x = fmaf(v[z][y].x, a, acc[y].x), acc[y].y = fmaf(v[z][y].y, a, acc[y].y);
+                acc[y].z = fmaf(v[z][y].z, a, acc[y].z), acc[y].w = fmaf(v[z][y].w, a, acc[y].w);
               }
             }
           }
-          __syncthreads();
+#pragma unroll
+          for (int y = 0; y < kB; ++y) {
+            const int at = at0 + y * kThreads;
+            if (at >= rows * kVec) continue;
+            const int row = at / kVec, d = 4 * (at % kVec);
+            if (top) {
+              store_row<kF16>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc[y], M[y], lt[y], Rf[y]);
+            } else {
+              // The group's sums take the place of its first part's; its statistics once every thread has read them.
+              *(reinterpret_cast<float4*>(part_of(base)) + at) = acc[y];
+              if (d == 0) mlr_sm[0][row] = make_float4(M[y], lt[y], Rf[y], 0.f);
+            }
+          }
         }
+        if (top) break;
+        __syncthreads();
+        for (int row = threadIdx.x; row < rows; row += kThreads)
+          *(reinterpret_cast<float4*>(part_of(base) + L::kRows * D) + row) = mlr_sm[0][row];
+        base = 0, step = group, count_n = groups;
+        counter = p.counters + first;
       }
+      __syncthreads();
     }
     if (u < u1) {
       // The join buffer lies over the rings: plain accesses to it come before the next copies.
@@ -763,14 +743,17 @@ static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStrea
   return rows <= 8 ? launch_few<kF16, 256, 1>(p, sms, s) : launch_few<kF16, 256, 2>(p, sms, s);
 }
 
-// Two parts of the widest variant's rows for each CTA.
+// Two parts for each CTA of the variant that needs most.
+template <int D, int NT>
+static size_t parts_of(int sms) {
+  return (size_t)sms * Layout<D, NT>::kCtas * 2 * Layout<D, NT>::kPart * sizeof(float);
+}
 static size_t parts_bytes(int head_dim, int sms) {
-  const int part = head_dim == 64 ? Layout<64, 4>::kPart : head_dim == 128 ? Layout<128, 4>::kPart : Layout<256, 2>::kPart;
-  const size_t few = (size_t)sms * 2 * 2 * part * sizeof(float), many = many_parts_bytes(head_dim, sms);
+  const size_t few = head_dim == 64 ? parts_of<64, 4>(sms) : head_dim == 128 ? parts_of<128, 4>(sms) : parts_of<256, 2>(sms), many = many_parts_bytes(head_dim, sms);
   return few > many ? few : many;
 }
 
-constexpr size_t counters_bytes(int sms) { return ((size_t)sms * 2 * sizeof(uint32_t) + 255) / 256 * 256; }
+constexpr size_t counters_bytes(int sms) { return ((size_t)sms * 12 * sizeof(uint32_t) + 255) / 256 * 256; }
 
 }  // namespace attn
 }  // namespace w8a8
@@ -828,6 +811,7 @@ extern "C" int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, c
   uint8_t* const w = static_cast<uint8_t*>(ws);
   p.status = reinterpret_cast<uint32_t*>(w);
   p.counters = reinterpret_cast<uint32_t*>(w + kWsHeaderBytes);
+  p.group_counters = p.counters + (size_t)sms * 4;
   p.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + attn::counters_bytes(sms));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   e = dtype == KV8_F16 ? attn::launch_rows<true>(p, D, sms, s) : attn::launch_rows<false>(p, D, sms, s);

@@ -33,6 +33,7 @@ struct Params {
   float scale_log2;        // scale * log2 e
   uint32_t* status;
   uint32_t* counters;      // [CTA] arrivals at the item that crosses the end of its run, zero between calls
+  uint32_t* group_counters;   // [CTA][2] arrivals at a group of parts, by its first part's place, zero between calls
   float* parts;            // [CTA][2] parts of split items
 };
 
