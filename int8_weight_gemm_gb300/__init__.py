@@ -182,10 +182,10 @@ def _stream(stream):
         import torch
 
         # The handle of torch.cuda.current_stream() (making that object costs 3 us, a third of a small call).
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(torch.cuda.current_device())
-        return torch.cuda.current_stream().cuda_stream
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
     return ctypes.c_void_p(stream.cuda_stream)
@@ -550,7 +550,7 @@ class QKPrep:
         self.addr = ctypes.addressof(self.c)
 
     def check(self, dtype, head_dim):
-        if self.dtype is not None and (self.dtype != dtype or self.gamma_len < head_dim):
+        if self.dtype is not None and (self.dtype is not dtype or self.gamma_len < head_dim):
             raise ValueError(f"gamma_q, gamma_k: expected {head_dim} of {dtype}, got {self.gamma_len} of {self.dtype}")
 
 
@@ -576,7 +576,7 @@ def _heads(t, name, rows, heads, dim, dtype):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (s1 != dim and heads > 1):
         raise ValueError(f"{name}: expected contiguous heads (strides {tuple(t.stride())})")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     return s0 if rows > 1 else heads * dim
 
@@ -584,8 +584,8 @@ def _heads(t, name, rows, heads, dim, dtype):
 def _positions(t, rows):
     if t is None:
         return None
-    _dev(t, "positions", 4 * rows, esize=4)
-    if t.is_floating_point():
+    if t.element_size() != 4 or t.is_floating_point() or not t.is_contiguous() or t.numel() < rows:
+        _dev(t, "positions", 4 * rows, esize=4)
         raise ValueError(f"positions: expected int32, got {t.dtype}")
     return t.data_ptr()
 
@@ -616,7 +616,8 @@ def qk_norm_rope(prep, q, k, positions, ws, q_out=None, k_out=None, stream=None)
     qo, ko = _heads(q_out, "q_out", rows, q_heads, dim, dtype), _heads(k_out, "k_out", rows, kv_heads, dim, dtype)
     pos = _positions(positions, rows)
     wp, wn = _ws(ws)
-    _on_cuda(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out, ws=ws)
+    if not (q.is_cuda and k.is_cuda and q_out.is_cuda and k_out.is_cuda and ws.is_cuda and (pos is None or positions.is_cuda)):
+        _on_cuda(q=q, k=k, positions=positions, q_out=q_out, k_out=k_out, ws=ws)
     rc = lib().qk_norm_rope(prep.addr, q.data_ptr(), qs, q_heads, k.data_ptr(), ks, kv_heads, dim, pos, rows, q_out.data_ptr(), qo,
                             k_out.data_ptr(), ko, dt, wp, wn, _stream(stream))
     _check("qk_norm_rope", rc)
@@ -643,7 +644,8 @@ def kv8_append(cache, step, prep, k, v, ws, q=None, q_out=None, positions=None, 
         raise ValueError("q_out: given without q")
     pos = _positions(positions, rows)
     wp, wn = _ws(ws)
-    _on_cuda(k=k, v=v, q=q, q_out=q_out, positions=positions, ws=ws)
+    if not (k.is_cuda and v.is_cuda and ws.is_cuda and (q is None or (q.is_cuda and q_out.is_cuda)) and (pos is None or positions.is_cuda)):
+        _on_cuda(k=k, v=v, q=q, q_out=q_out, positions=positions, ws=ws)
     rc = lib().kv8_append(cache.addr, step.addr, prep.addr if prep is not None else None, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, q_heads, qop, qo, pos, dt, wp, wn,
                           _stream(stream))
     _check("kv8_append", rc)
@@ -664,7 +666,8 @@ def kv8_attention(cache, step, q, ws, out=None, lse=None, scale=None, window: in
         _dev(lse, "lse", 4 * rows * q_heads, esize=4)
         lp = lse.data_ptr()
     wp, wn = _ws(ws)
-    _on_cuda(q=q, out=out, lse=lse, ws=ws)
+    if not (q.is_cuda and out.is_cuda and ws.is_cuda and (lse is None or lse.is_cuda)):
+        _on_cuda(q=q, out=out, lse=lse, ws=ws)
     rc = lib().kv8_attention(cache.addr, step.addr, q.data_ptr(), qs, q_heads, out.data_ptr(), os_, lp,
                              dim ** -0.5 if scale is None else scale, window, flags, dt, wp, wn, _stream(stream))
     _check("kv8_attention", rc)
@@ -683,6 +686,7 @@ def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
     dt = _kv8_dtype(k_out, "k_out")
     ks, vs = _heads(k_out, "k_out", rows, heads, dim, k_out.dtype), _heads(v_out, "v_out", rows, heads, dim, k_out.dtype)
     wp, wn = _ws(ws)
-    _on_cuda(k_out=k_out, v_out=v_out, ws=ws)
+    if not (k_out.is_cuda and v_out.is_cuda and ws.is_cuda):
+        _on_cuda(k_out=k_out, v_out=v_out, ws=ws)
     _check("kv8_read", lib().kv8_read(cache.addr, step.addr, k_out.data_ptr(), ks, v_out.data_ptr(), vs, dt, wp, wn, _stream(stream)))
     return k_out, v_out
