@@ -45,6 +45,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2<kF16>(f[0], f[1]), pack2<kF16>(f[2], f[3]), pack2<kF16>(f[4], f[5]), pack2<kF16>(f[6], f[7]));
 }
 
+// Two fp32 operations in one instruction (each rounded as the scalar one).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // A head is held by a group of kLanes = head_dim / 8 lanes, eight values a lane.  kPaired (the whole head
 // rotates, pairs half a head apart): lane l holds values 4 l ... 4 l + 3 of either half, so that both values
 // of a pair are its own and no lane needs another's, and a position's cosines and sines are read once.
@@ -121,29 +144,56 @@ __device__ __forceinline__ void load_turn(const float* row, int l, int rot, bool
   }
 }
 
-// Norm and rotation of one head.  Every lane of the warp takes part (the shuffles are warp-wide, xor or within
-// a group).  The products and sums of the rotation are rounded one by one, in the order of its formula
+// rs[i] = 1 / sqrt(mean of the i-th of four heads' squares + eps).  Each lane brings its share of all four; the first
+// two exchanges leave a lane with one head's sum, so the four cost little more than one, root included.  Every lane
+// of the warp takes part.
+template <int kLanes>
+__device__ __forceinline__ void norms_of(const float (&x)[4][8], float eps, float (&rs)[4]) {
+  float ss[4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint64_t t = mul2(pair(x[h][0], x[h][1]), pair(x[h][0], x[h][1]));
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) t = fma2(pair(x[h][i], x[h][i + 1]), pair(x[h][i], x[h][i + 1]), t);
+    float lo, hi;
+    unpair(t, lo, hi);
+    ss[h] = lo + hi;
+  }
+  const int lane = threadIdx.x & 31;
+  const bool b0 = lane & (kLanes / 2), b1 = lane & (kLanes / 4);
+  float u = b0 ? ss[2] : ss[0], v = b0 ? ss[3] : ss[1];
+  u += __shfl_xor_sync(0xffffffffu, b0 ? ss[0] : ss[2], kLanes / 2);
+  v += __shfl_xor_sync(0xffffffffu, b0 ? ss[1] : ss[3], kLanes / 2);
+  float s = b1 ? v : u;
+  s += __shfl_xor_sync(0xffffffffu, b1 ? u : v, kLanes / 4);
+#pragma unroll
+  for (int o = kLanes / 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const float r = __frsqrt_rn(s * (1.0f / (8 * kLanes)) + eps);   // of head 2 b0 + b1
+  const int base = lane & ~(kLanes - 1);
+#pragma unroll
+  for (int h = 0; h < 4; ++h) rs[h] = __shfl_sync(0xffffffffu, r, base + (h >> 1) * (kLanes / 2) + (h & 1) * (kLanes / 4));
+}
+
+// The norm's factors, then the rotation, of one head.  Every lane of the warp takes part (the shuffles are
+// warp-wide).  The products and sums of the rotation are rounded one by one, in the order of its formula
 // (a c - b s, b c + a s), so a value does not depend on how the compiler contracts them.
-template <int kLanes, bool kPaired>
-__device__ __forceinline__ void norm_turn(float (&x)[8], const float* gamma8, float eps, const Turn<kPaired>& t, int l, int rot,
-                                          bool interleaved) {
-  if (gamma8) {
-    float ss = 0.f;
+template <bool kPaired>
+__device__ __forceinline__ void norm_turn(float (&x)[8], bool norm, float rs, const float (&gamma8)[8], const Turn<kPaired>& t, int l,
+                                          int rot, bool interleaved) {
+  if (norm) {
+    const uint64_t r2 = pair(rs, rs);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / (8 * kLanes)) + eps));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * rs * gamma8[i];
+    for (int i = 0; i < 8; i += 2)
+      unpair(mul2(mul2(pair(x[i], x[i + 1]), r2), pair(gamma8[i], gamma8[i + 1])), x[i], x[i + 1]);
   }
   if (rot == 0) return;
   if (kPaired) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a = x[i], b = x[i + 4];
-      x[i] = __fsub_rn(__fmul_rn(a, t.c[i]), __fmul_rn(b, t.s[i]));
-      x[i + 4] = __fadd_rn(__fmul_rn(b, t.c[i]), __fmul_rn(a, t.s[i]));
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t a = pair(x[i], x[i + 1]), b = pair(x[i + 4], x[i + 5]);
+      const uint64_t c = pair(t.c[i], t.c[i + 1]), s = pair(t.s[i], t.s[i + 1]), n = pair(-t.s[i], -t.s[i + 1]);
+      unpair(add2(mul2(a, c), mul2(b, n)), x[i], x[i + 1]);
+      unpair(add2(mul2(b, c), mul2(a, s)), x[i + 4], x[i + 5]);
     }
     return;
   }

@@ -51,7 +51,7 @@ constexpr int kQkHeads = 4;   // heads of one row whose loads a lane group has i
 
 // Batches of kQkHeads heads a lane group takes: one where there are few groups (a second one would only add its
 // latency), two where there are many, so that a position's rotation is read half as often (16383 rows of 40
-// heads: 67.2 us with two, 70.0 with one, 75.5 with four; 16 rows: 3.1 with one, 4.7 with two).
+// heads: 57.2 us with two, 59.3 with one, 60.3 with four; 16 rows: 2.7 with one, 3.8 with two).
 static int batches_of(int heads, int rows) {
   const int chunks = (heads + kQkHeads - 1) / kQkHeads;
   return (long long)chunks * rows > 16384 && chunks > 1 ? 2 : 1;
@@ -80,18 +80,21 @@ __device__ __forceinline__ void turn_heads(const QkParams& p, int row, bool live
       if (live && h < heads)
         raw[i] = load_head<kLanes, kPaired>(h < p.q_heads ? p.q + row * p.q_stride + h * D : p.k + row * p.k_stride + (h - p.q_heads) * D, l);
     }
+    float x[kQkHeads][8], rs[kQkHeads];
+#pragma unroll
+    for (int i = 0; i < kQkHeads; ++i) unpack8<kF16>(raw[i], x[i]);
+    if (p.gamma_q || p.gamma_k) norms_of<kLanes>(x, p.eps, rs);
 #pragma unroll
     for (int i = 0; i < kQkHeads; ++i) {
       const int h = h0 + i;
       const bool is_q = h < p.q_heads;
       const uint16_t* gamma = is_q ? p.gamma_q : p.gamma_k;
-      float x[8], g[8];
-      unpack8<kF16>(raw[i], x);
+      float g[8];
       if (gamma) unpack8<kF16>(load_head<kLanes, kPaired>(gamma, l), g);
-      norm_turn<kLanes, kPaired>(x, gamma ? g : nullptr, p.eps, t, l, p.rot, p.interleaved != 0);
+      norm_turn<kPaired>(x[i], gamma != nullptr, rs[i], g, t, l, p.rot, p.interleaved != 0);
       if (live && h < heads)
         store_head<kLanes, kPaired>(is_q ? p.q_out + row * p.q_out_stride + h * D : p.k_out + row * p.k_out_stride + (h - p.q_heads) * D,
-                                    l, pack8<kF16>(x));
+                                    l, pack8<kF16>(x[i]));
     }
   }
 }
@@ -128,6 +131,7 @@ struct AppendParams {
 };
 
 constexpr int kHeld = 4;   // tokens a thread holds
+static_assert(kHeld == 4 && kQkHeads == 4, "norms_of takes four at a time");
 
 // The byte that holds x at scale s.
 __device__ __forceinline__ uint32_t hold(float x, float s) {
@@ -241,19 +245,21 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
     raw[i] = make_uint4(0u, 0u, 0u, 0u);
     if (t >= lo && t < hi) raw[i] = load_head<kLanes, kPaired>(src + (s.row0 + pg * P + t - first_slot) * stride + h * D, l);
   }
-  float x[kHeld][8];
+  float x[kHeld][8], rs[kHeld];
   float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) unpack8<kF16>(raw[i], x[i]);
+  if (norm) norms_of<kLanes>(x, c.eps, rs);
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
     const int t = g + i * groups;
     const bool mine = t >= lo && t < hi;
-    unpack8<kF16>(raw[i], x[i]);
     Turn<kPaired> turn;
     if (rot > 0) {
       const int pos = !mine ? 0 : c.positions ? __ldg(c.positions + s.row0 + pg * P + t - first_slot) : pg * P + t;
       load_turn<kPaired>(turn_row(c.cos_sin, pos, rot, c.max_pos, c.status), l, rot, c.interleaved != 0, turn);
     }
-    norm_turn<kLanes, kPaired>(x[i], norm ? gk : nullptr, c.eps, turn, l, rot, c.interleaved != 0);
+    norm_turn<kPaired>(x[i], norm, rs[i], gk, turn, l, rot, c.interleaved != 0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[i][j]));
   }
