@@ -407,6 +407,18 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       for (int i = j; i < min(j + NS, mine_n); ++i)
         mbar_wait_drain(&bar[(count + (uint32_t)i) % NS], ((count + (uint32_t)i) / NS) & 1u, p.status);
     };
+    // Granule j takes the slot that this warp has read.  The copy's writes are of the asynchronous proxy: without
+    // the fence they can overtake the lanes' reads, which a barrier of the warp alone does not hold up (seen as a
+    // granule's values replaced by those of the one after it in the slot, in one of 10^5).  After the products the
+    // reads have long returned and the fence costs nothing; where the next granule's scores are in hand already the
+    // copy is better early (24 rows 43.8 -> 40.0 us, 64-wide heads 24.6 -> 24.1, one tile of 128 147.2 -> 146.2).
+    auto refill = [&](int j) {
+      fence_async_shared();
+      __syncwarp();
+      if (j >= mine_n) return;
+      if ((j & 31) == 0) fetch(j);
+      issue(j);
+    };
     float sn[NT][kChains][4];
     if (L::kAhead && mine_n > 0 && !dead && !scores(0, sn)) give_up(0);
     for (int j = 0; j < mine_n && !dead; ++j) {
@@ -513,15 +525,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             vw[t][0] = v.x, vw[t][1] = v.y, vw[t][kWords - 2] = v.z, vw[t][kWords - 1] = v.w;
           }
         }
-        if (bx == L::kBoxes - 1) {
-          // Every byte of the granule is in registers: its slot takes a later one.
-          __syncwarp();
-          const int jn = j + NS;
-          if (jn < mine_n) {
-            if ((jn & 31) == 0) fetch(jn);
-            issue(jn);
-          }
-        }
+        if (L::kAhead && bx == L::kBoxes - 1) refill(j + NS);   // every byte of the granule is in registers
 #pragma unroll
         for (int wd = 0; wd < kWords; ++wd) {
           uint32_t bf[2][4];   // [tokens 2c.. / 2c + 8..][d]
@@ -540,6 +544,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
                             pb[i][1]);
         }
       }
+      if (!L::kAhead) refill(j + NS);
     }
     count += (uint32_t)mine_n;
 

@@ -230,6 +230,45 @@ def test_cache_offsets_past_32_bits():
     assert c.status() == 0
 
 
+@pytest.mark.parametrize("dim,n,kv_heads,page", [(64, 1, 8, 64), (128, 1, 8, 64), (128, 3, 8, 32), (128, 6, 4, 128), (256, 1, 4, 16)])
+def test_long_contexts_under_load(dim, n, kv_heads, page):
+    # Every SM streams for long: runs of 32 granules of a warp and more, slots refilled while others still read
+    # theirs.  Every row of the first pass against 64 bits, and every bit of the others against the first.
+    gen = torch.Generator(device="cuda").manual_seed(dim + n)
+    B, G, width = 64, 4, 7936 // page
+    lens = torch.randint(5000, width * page + 1, (B,), device="cuda", generator=gen, dtype=torch.int32)
+    shape = (B * width, kv_heads, page, dim)
+    k, v = (torch.randint(1, 256, shape, device="cuda", generator=gen, dtype=torch.uint8) for _ in range(2))
+    ks, vs = (0.01 * torch.exp(0.2 * torch.randn(shape[:2], device="cuda", generator=gen)) for _ in range(2))
+    table = torch.randperm(B * width, device="cuda", generator=gen).to(torch.int32).view(B, width)
+    row0 = torch.arange(B + 1, device="cuda", dtype=torch.int32) * n
+    q = torch.randn(B * n, kv_heads * G, dim, device="cuda", generator=gen).bfloat16()
+    cache, step = lib8.KV8Cache(k, v, ks, vs), lib8.KV8Step(row0, lens, table, B * n, n)
+    ws = lib8.alloc_workspace(lib8.kv8_workspace_bytes(kv_heads * G, kv_heads, dim))
+    first = lib8.kv8_attention(cache, step, q, ws).clone()
+    for _ in range(20):
+        assert torch.equal(lib8.kv8_attention(cache, step, q, ws), first)
+    assert lib8.w8a8_workspace_status(ws) == 0
+    scale = dim ** -0.5
+    for b in range(B):
+        L = int(lens[b])
+        pages = table[b].long()
+        per_token = [s[pages].double().repeat_interleave(page, 0)[:L].T for s in (ks, vs)]              # [heads, L]
+        kk, vv = ((x[pages].double().sub_(128).transpose(0, 1).reshape(kv_heads, -1, dim)[:, :L] * s[:, :, None])
+                  for x, s in zip((k, v), per_token))
+        qq = q[b * n:(b + 1) * n].double().unflatten(1, (kv_heads, G)).permute(1, 2, 0, 3)              # [heads, G, n, dim]
+        s = torch.einsum("hgnd,hld->hgnl", qq, kk) * scale
+        seen = torch.arange(L, device="cuda")[None] <= (L - n + torch.arange(n, device="cuda"))[:, None]
+        w = torch.softmax(s.masked_fill(~seen, float("-inf")), -1)
+        ref = torch.einsum("hgnl,hld->hgnd", w, vv)
+        d = (scale * qq.abs().sum(-1) * 256 * (dim + 32) * 2.0 ** -24 * per_token[0].amax(1)[:, None, None]
+             + s.abs().amax(-1) * 2.0 ** -21 + 2.0 ** -20)
+        e = (2 * d + 2.0 ** -11 + (L / 16 + 64) * 2.0 ** -23)[..., None] * torch.einsum("hgnl,hld->hgnd", w, vv.abs())
+        e = e + (L * 2.0 ** -25 * (w * per_token[1][:, None, None]).amax(-1) * 127)[..., None]
+        got = first[b * n:(b + 1) * n].double().unflatten(1, (kv_heads, G)).permute(1, 2, 0, 3)
+        assert ((got - ref).abs() <= e + UNIT["bf16"] * (ref.abs() + e)).all(), b
+
+
 def test_no_rows_is_a_no_op():
     c = Case([1], [5], 4, 2, 64, 16).tensors()
     step = lib8.KV8Step(torch.zeros_like(c.step.row0), c.step.kv_len, c.step.page_table, 0, 1)
