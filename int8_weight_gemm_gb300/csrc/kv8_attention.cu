@@ -730,14 +730,16 @@ static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a sequence and kv head up to which this file's kernel runs.
-constexpr long long kFewRows = 32;
+// Rows of a sequence and kv head up to which this file's kernel runs.  Heads of 256 score twice in the other one and
+// stay here longer (16 rows a tile): 8 contexts of 3000, 128 rows 77 us here, 69 there; 4 of 1000, 80 rows 21 and 30;
+// 16 of 4000, 48 rows 79 and 108.
+constexpr long long few_rows(int head_dim) { return head_dim == 256 ? 112 : 32; }
 
 // The narrowest variant that holds a sequence's rows in one tile, else the widest.
 template <bool kF16>
 static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
   const long long rows = (long long)p.step.max_tokens * p.group;
-  if (head_dim <= 128 && rows > kFewRows) return launch_many(p, head_dim, kF16, sms, s);
+  if (rows > few_rows(head_dim)) return launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
     return rows <= 8 ? launch_few<kF16, 64, 1>(p, sms, s) : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s) : launch_few<kF16, 64, 4>(p, sms, s);
   if (head_dim == 128)

@@ -24,6 +24,11 @@
 //  - four converter warps: 8 bits -> fp16 operands, two blocks of each ahead of the products;
 //  - one thread issues the products: W V of a block, then, when those have completed (the other stream's
 //    are in the pipe meanwhile), the next scores into the same tensor memory.
+// Heads of 256: a stream's sums of 256 columns and its scores do not fit half the tensor memory, nor the operands of
+// 128 tokens shared memory.  An item is then 128 of the values' columns, a block 64 tokens, and the streams are one
+// tile's blocks: half as many products again and twice the exponentials, and still 2.2 times as fast as 16 rows a warp
+// (two prompts of 2048 on contexts of 6000, 32 query heads: 886 us, 1923 so).  The converters bound it, with the
+// issuing warp's own time.
 // The work is cut like that of the other kernel: items (row tile, kv head) laid end to end in units of a
 // block and cut into equal runs; an item cut across CTAs is finished by the last to arrive, parts joined
 // in the CTAs' order, so replays give the same bits.
@@ -32,7 +37,6 @@
 namespace w8a8 {
 namespace attn {
 
-constexpr int kBlock = 128;       // tokens of a block
 constexpr int kTileRows = 128;    // rows of a tile
 constexpr int kSoftWarps = 8;     // four for each stream
 constexpr int kSoftThreads = 32 * kSoftWarps;
@@ -40,22 +44,28 @@ constexpr int kConvWarps = 4;
 constexpr int kProducerWarp = kSoftWarps + kConvWarps;
 constexpr int kMmaWarp = kProducerWarp + 1;
 constexpr int kTcThreads = 32 * (kMmaWarp + 1);
-constexpr int kGrans = kBlock / kGranule;   // granules of a block
 constexpr int kScales = 8;        // blocks whose scales are held
 
 template <int D, int kTiles>
 struct TcLayout {
   static constexpr int kRows = kTiles * kTileRows;
+  // Heads of 256: an item is 128 of the values' columns (two items score alike), a block 64 tokens: its sums and
+  // scores fit a stream's tensor memory, its operands shared memory.
+  static constexpr int kCols = D < 128 ? D : 128;     // columns of values
+  static constexpr int kSplits = D / kCols;           // items of a head and row tile
+  static constexpr int kBlock = D > 128 ? 64 : 128;   // tokens of a block
+  static constexpr int kGrans = kBlock / kGranule;    // granules of a block
   static constexpr int kUnit = kBlock;
   static constexpr int kLead = 3;
   static constexpr int kQBytes = kTileRows * D * 2;
-  static constexpr int kBlk16 = kBlock * D * 2;       // an fp16 block
+  static constexpr int kHalf = kBlock * 128;          // 64 fp16 of each of a block's tokens
+  static constexpr int kK16 = kBlock * D * 2, kV16 = kBlock * kCols * 2;   // fp16 blocks
   static constexpr int kSlot = kBlock * D;            // an 8-bit block
   // 8-bit blocks in flight: with one tile the cache comes from HBM at the pace of the products.
   static constexpr int kSlots = kTiles == 2 ? 2 : 4;
-  static constexpr int kBytes = 1024 + kTiles * kQBytes + 4 * kBlk16 + kSlots * kSlot;
+  static constexpr int kBytes = 1024 + kTiles * kQBytes + 2 * (kK16 + kV16) + kSlots * kSlot;
   static constexpr int kSCol = 0, kOCol = kBlock, kStreamCols = 256;   // tensor-memory columns of a stream
-  static constexpr int kPart = kRows * (D + 4);       // floats: sums, then (m, l, r, -) of each row
+  static constexpr int kPart = kRows * (kCols + 4);   // floats: sums, then (m, l, r, -) of each row
   static_assert(kBytes + 2048 <= 232448, "shared memory");
 };
 
@@ -71,7 +81,7 @@ __device__ __forceinline__ TileSpan tile_span(const Params& p, const Seq& s, int
   const int last = min(s.n - 1, (int)quotient((long long)tile * L::kRows + L::kRows - 1, p.group));
   t.hi = p.causal ? max(0, s.len - s.n + last + 1) : s.len;
   t.lo = p.window > 0 ? max(0, s.len - s.n + first - p.window + 1) & ~(kGranule - 1) : 0;
-  t.units = max(1, (t.hi - t.lo + kBlock - 1) / kBlock);
+  t.units = max(1, (t.hi - t.lo + L::kBlock - 1) / L::kBlock);
   return t;
 }
 
@@ -85,14 +95,14 @@ struct Segment {
   int nb;                    // blocks
   int T0;                    // first token
   int row0, pos0, len;       // of the sequence: first row, position of its first row, cached tokens
-  int h, tile, rows;         // kv head, row tile, rows of the tile that exist
+  int h, col0, tile, rows;   // kv head, first column of the values, row tile, rows of the tile that exist
   int whole;                 // the item's only part
   int slot;                  // else: its place among this CTA's parts,
   int first, parts, slot0;   //   and the item's first CTA, number of CTAs, and place in the first one
 };
 constexpr int kSegments = 4;   // segments under way
 
-// A run's segments, one item's part each.  Items are ordered by sequence, kv head, row tile.
+// A run's segments, one item's part each.  Items are ordered by sequence, kv head and its columns (h), row tile.
 template <typename L>
 struct Walk {
   long long u, u1, item_u0;
@@ -106,7 +116,7 @@ struct Walk {
         item_u0 += L::kLead + t.units;
         if (++tile == tiles) {
           tile = 0;
-          if (++h == p.kv_heads) {
+          if (++h == p.kv_heads * L::kSplits) {
             h = 0;
             do {
               load_seq(p.step, ++b, 1 << p.page_shift, false, p.status, s);
@@ -238,8 +248,7 @@ struct alignas(16) GranScale {
 template <bool kF16, int D, int kTiles>
 __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const __grid_constant__ Params p) {
   using L = TcLayout<D, kTiles>;
-  constexpr int kSlots = L::kSlots;
-  constexpr int kHalfBytes = kBlock * 128;   // 64 fp16 of each of 128 rows
+  constexpr int kSlots = L::kSlots, kBlock = L::kBlock, kGrans = L::kGrans, kCols = L::kCols;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t slot_full[kSlots], slot_empty[kSlots];   // 8-bit blocks
   __shared__ __align__(8) uint64_t sc_full[kScales];                        // scales of a block
@@ -261,8 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
 
   uint8_t* const qtile = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const k16 = qtile + kTiles * L::kQBytes;   // [2]
-  uint8_t* const v16 = k16 + 2 * L::kBlk16;           // [2]
-  uint8_t* const ring = v16 + 2 * L::kBlk16;          // [kSlots] 8-bit blocks
+  uint8_t* const v16 = k16 + 2 * L::kK16;             // [2]
+  uint8_t* const ring = v16 + 2 * L::kV16;            // [kSlots] 8-bit blocks
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -299,7 +308,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     const int tiles = tiles_of<L>(p, s);
     long long n = 0;
     for (int t = 0; t < tiles; ++t) n += L::kLead + tile_span<L>(p, s, t).units;
-    return n * p.kv_heads;
+    return n * p.kv_heads * L::kSplits;
   };
   for (int b = s0; b < s1; ++b) {
     Seq s;
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           g.nb = nb;
           g.T0 = wk.t.lo + wk.ub * kBlock;
           g.row0 = wk.s.row0, g.pos0 = wk.s.len - wk.s.n, g.len = wk.s.len;
-          g.h = wk.h, g.tile = wk.tile, g.rows = (int)min((long long)L::kRows, (long long)wk.s.n * p.group - (long long)wk.tile * L::kRows);
+          g.h = wk.h / L::kSplits, g.col0 = wk.h % L::kSplits * kCols, g.tile = wk.tile, g.rows = (int)min((long long)L::kRows, (long long)wk.s.n * p.group - (long long)wk.tile * L::kRows);
           g.whole = wk.whole();
           g.slot = wk.item_u0 <= u0 ? 0 : 1;
           g.first = runs.owner(wk.item_u0 + L::kLead);
@@ -395,8 +404,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       if (!more) break;
       const int T0 = wk.t.lo + wk.ub * kBlock, T1 = min(wk.t.hi, wk.t.lo + wk.ue * kBlock);
       const int* const table = p.step.page_table + (size_t)wk.b * p.step.table_width;
-      for (int base = 0; ok && base < nb; base += 4) {
-        // Lane: granule lane % 8 of block base + lane / 8.
+      constexpr int kFetch = 32 / kGrans;   // blocks
+      for (int base = 0; ok && base < nb; base += kFetch) {
+        // Lane: granule lane % kGrans of block base + lane / kGrans.
         const int t = T0 + base * kBlock + lane * kGranule;
         GranScale sc{0.f, 0.f, -INFINITY, -INFINITY};
         uint32_t turn = 0x3C003C00u;
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             atomicOr(p.status, W8A8_DEV_BAD_INDEX);
             live = false;
           } else {
-            const size_t at = (size_t)page * p.kv_heads + wk.h;
+            const size_t at = (size_t)page * p.kv_heads + wk.h / L::kSplits;
             row = (int)(at << p.page_shift) + (t & ((1 << p.page_shift) - 1));
             const float ks = __ldg(p.ks + at), vs = __ldg(p.vs + at);
             sc.ks = fabsf(ks);
@@ -420,13 +430,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         }
         const uint32_t lives = __ballot_sync(0xffffffffu, live);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kFetch; ++i) {
           if (base + i >= nb) break;
           const uint32_t n = blk + base + i;
-          const bool own = (lane >> 3) == i;
-          if (own) scales[n % kScales][lane & 7] = sc, turns[n % kScales][lane & 7] = turn;
+          const bool own = lane / kGrans == i;
+          if (own) scales[n % kScales][lane % kGrans] = sc, turns[n % kScales][lane % kGrans] = turn;
           arrive_warp(&sc_full[n % kScales]);
-          const uint32_t bytes = (uint32_t)__popc((lives >> (8 * i)) & 0xFFu) * kGranule * D;
+          const uint32_t tokens = (uint32_t)__popc((lives >> (kGrans * i)) & ((1u << kGrans) - 1u)) * kGranule;
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
@@ -434,11 +444,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], bytes);
+            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], tokens * (side ? kCols : D));
             ++copies;
             __syncwarp();
-            if (own && live)
-              tma_load_2d(ring + slot * L::kSlot + (lane & 7) * kGranule * D, side ? &p.vmap : &p.kmap, 0, row, &slot_full[slot]);
+            if (own && live) {
+              // (A box is 128 columns at most; those of a block's granules lie together.)
+              uint8_t* const dst = ring + slot * L::kSlot + lane % kGrans * kGranule * kCols;
+              if (side) {
+                tma_load_2d(dst, &p.vmap, wk.h % L::kSplits * kCols, row, &slot_full[slot]);
+              } else {
+#pragma unroll
+                for (int x = 0; x < L::kSplits; ++x) tma_load_2d(dst + x * kBlock * kCols, &p.kmap, x * kCols, row, &slot_full[slot]);
+              }
+            }
           }
           if (!ok) break;
         }
@@ -466,43 +484,57 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         for (int side = 0; side < 2; ++side) {
           const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
           const uint8_t* const src = ring + slot * L::kSlot;
-          uint8_t* const dst = (side ? v16 : k16) + (n & 1) * L::kBlk16;
+          uint8_t* const dst = side ? v16 + (n & 1) * L::kV16 : k16 + (n & 1) * L::kK16;
           if (!wait_all(&slot_full[slot], use & 1u, &abort_flag, p.status) ||
               (n >= 2 && !wait_all(side ? &v_empty[n & 1] : &k_empty[n & 1], ((n >> 1) - 1) & 1u, &abort_flag, p.status))) {
             ok = false;
             break;
           }
-          // A warp takes 32 tokens: eight rows by four 16-byte pieces at a time, so that neither the
-          // reads (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.
+          // A warp takes a quarter of the tokens: eight rows by four 16-byte pieces at a time, so that neither the reads
+          // (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.  All reads go out first.
+          auto convert = [&](auto cols) {
+            constexpr int kEights = kBlock / 8 / kConvWarps, kY = decltype(cols)::value / 64;
+            uint4 w[kEights][kY];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t turn = turns[n % kScales][2 * cw + (i >> 1)];
-            const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
-            const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
-            const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
-            const int t = (4 * cw + i) * 8 + (lane & 7);
+            for (int i = 0; i < kEights; ++i) {
+              const int t = (kEights * cw + i) * 8 + (lane & 7);
 #pragma unroll
-            for (int y = 0; y < D / 64; ++y) {
-              const int piece = (lane >> 3) + 4 * y;
-              const uint4 w = D == 64 ? *reinterpret_cast<const uint4*>(src + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4))
-                                      : *reinterpret_cast<const uint4*>(src + t * 128 + ((piece ^ (t & 7)) << 4));
-              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-              uint32_t out[8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                // fp16 0x6400 | b = 1024 + b, so (1024 + b) sg - 1152 sg = sg (b - 128), exactly.
-                const uint32_t a = __byte_perm(in[k], 0x64646464u, 0x4140), c = __byte_perm(in[k], 0x64646464u, 0x4342);
-                const __half2 ha = __hfma2(*reinterpret_cast<const __half2*>(&a), sg, of);
-                const __half2 hc = __hfma2(*reinterpret_cast<const __half2*>(&c), sg, of);
-                out[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-                out[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hc);
+              for (int y = 0; y < kY; ++y) {
+                const int piece = (lane >> 3) + 4 * y;
+                w[i][y] = D == 64 ? *reinterpret_cast<const uint4*>(src + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4))
+                                  : *reinterpret_cast<const uint4*>(src + (piece >> 3) * kBlock * kCols + t * 128 + (((piece & 7) ^ (t & 7)) << 4));
               }
-              uint8_t* const row = dst + (piece >> 2) * kHalfBytes + t * 128;
-              const int ch = 2 * (piece & 3);
-              *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
             }
-          }
+#pragma unroll
+            for (int i = 0; i < kEights; ++i) {
+              const uint32_t turn = turns[n % kScales][(kEights * cw + i) >> 1];
+              const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
+              const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
+              const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
+              const int t = (kEights * cw + i) * 8 + (lane & 7);
+#pragma unroll
+              for (int y = 0; y < kY; ++y) {
+                const int piece = (lane >> 3) + 4 * y;
+                const uint32_t in[4] = {w[i][y].x, w[i][y].y, w[i][y].z, w[i][y].w};
+                uint32_t out[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  // fp16 0x6400 | b = 1024 + b, so (1024 + b) sg - 1152 sg = sg (b - 128), exactly.
+                  const uint32_t a = __byte_perm(in[k], 0x64646464u, 0x4140), c = __byte_perm(in[k], 0x64646464u, 0x4342);
+                  const __half2 ha = __hfma2(*reinterpret_cast<const __half2*>(&a), sg, of);
+                  const __half2 hc = __hfma2(*reinterpret_cast<const __half2*>(&c), sg, of);
+                  out[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                  out[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hc);
+                }
+                uint8_t* const row = dst + (piece >> 2) * L::kHalf + t * 128;
+                const int ch = 2 * (piece & 3);
+                *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+                *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+              }
+            }
+          };
+          if (D == kCols || side) convert(Const<kCols>());
+          else convert(Const<D>());
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -518,8 +550,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     // address in 16 bytes and moves by constants.  (One warp for both streams: with one each, the products of
     // two accumulators mix in the pipe and each takes longer; prompt chunk 441 -> 521 us.)
     constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
-    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
-    const uint64_t dq = desc_kmajor(smem_addr(qtile)), dk = desc_kmajor(smem_addr(k16)), dv = desc_mnmajor(smem_addr(v16), kHalfBytes);
+    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, kCols) | (1u << 16);   // B is MN-major
+    const uint64_t dq = desc_kmajor(smem_addr(qtile)), dk = desc_kmajor(smem_addr(k16)), dv = desc_mnmajor(smem_addr(v16), L::kHalf);
     const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
     auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); };
     uint32_t blk = 0, cnt = 0;   // blocks of the CTA before this segment; steps of the first stream
@@ -547,7 +579,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t lo = v_lo + u * (uint32_t)(L::kBlk16 >> 4);
+            const uint32_t lo = v_lo + u * (uint32_t)(L::kV16 >> 4);
 #pragma unroll
             for (int k = 0; k < kBlock / 16; ++k)
               umma_f16_tmem_a(t + L::kOCol, t + (uint32_t)(L::kSCol + 8 * k), desc(lo + (uint32_t)(k * 16 * 128 >> 4), v_hi), idesc_o, i > 0 || k > 0);
@@ -565,11 +597,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         if (!ok || !more) continue;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t ql = q_lo + (kTiles == 2 ? s : 0) * (uint32_t)(L::kQBytes >> 4), kl = k_lo + ub * (uint32_t)(L::kBlk16 >> 4);
+          const uint32_t ql = q_lo + (kTiles == 2 ? s : 0) * (uint32_t)(L::kQBytes >> 4), kl = k_lo + ub * (uint32_t)(L::kK16 >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (uint32_t)(((k >> 2) * kHalfBytes + (k & 3) * 32) >> 4);
-            umma_f16_ss(t + L::kSCol, desc(ql + off, k_hi), desc(kl + off, k_hi), idesc_s, k > 0);
+            const uint32_t qo = (uint32_t)(((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), ko = (uint32_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
+            umma_f16_ss(t + L::kSCol, desc(ql + qo, k_hi), desc(kl + ko, k_hi), idesc_s, k > 0);
           }
           umma_commit(&s_full[s]);
           if (kTiles == 1 || s == 1) umma_commit(&k_empty[ub]);
@@ -631,7 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             unpack8<kF16>(live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u), f);
 #pragma unroll
             for (int k = 0; k < 8; ++k) f[k] *= down;
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * kHalfBytes + (((i & 7) ^ (row & 7)) << 4)) = pack8<true>(f);
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * kTileRows * 128 + (((i & 7) ^ (row & 7)) << 4)) = pack8<true>(f);
           }
           fence_async_shared();
           arrive_warp(&q_full[kTiles == 2 ? st : 0]);
@@ -744,7 +776,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                   hs = ex2(m - rn);
                   far = __any_sync(0xffffffffu, hs * fmaxf(vs[0], vs[1]) > kFar);
                   if (i > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
-                  if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
+                  if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? kCols : 0, t_s, ch, down);
                 }
               } while (moved);
               float l0, l1;
@@ -770,7 +802,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       float scale_own = 1.f, scale_other = 0.f;   // of the two streams' sums (one tile: they join here)
       // The second stream's (m, l, r), then kX columns of its sums at a time ([kX][128]), go over through the
       // queries' shared memory (every score has been computed).
-      constexpr int kX = L::kQBytes / (kTileRows * 4);
+      constexpr int kX = L::kQBytes / (kTileRows * 4) < kCols ? L::kQBytes / (kTileRows * 4) : kCols;
       float* const xch = reinterpret_cast<float*>(qtile);
       if (kTiles == 1) {
         bool met = meet();   // the other stream's scores too
@@ -794,7 +826,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       float* const part = p.parts + ((size_t)blockIdx.x * 2 + g->slot) * L::kPart;
       const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(r - m);
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
+      for (int c0 = 0; c0 < kCols; c0 += 32) {
         if (kTiles == 1 && c0 % kX == 0) {
           if (!meet()) ok = false;
           if (st == 1) {
@@ -821,7 +853,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (kTiles == 1) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
         }
         if (live && whole) {
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + c0);
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + g->col0 + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             float y[8];
@@ -834,15 +866,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             dst[k / 8] = pack8<kF16>(y);
           }
         } else if (live) {
-          float4* const dst = reinterpret_cast<float4*>(part + irow * D + c0);
+          float4* const dst = reinterpret_cast<float4*>(part + irow * kCols + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
       }
       if (!ok) break;
       if (live && (kTiles == 2 || st == 0)) {
-        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
-        else if (p.lse) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
+        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * kCols + irow * 4) = make_float4(m, l, r, 0.f);
+        else if (p.lse && g->col0 == 0) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
       }
       tc_fence_before();
       if (!whole) {
@@ -874,7 +906,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             float mm = kFloor, rm = kFloor, lt = 0.f;
 #pragma unroll 4
             for (int i = 0; i < np; ++i) {
-              const float4 t = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * D) + irow);
+              const float4 t = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * kCols) + irow);
               const float mn = fmaxf(mm, t.x);
               lt = lt * ex2(mm - mn) + t.y * ex2(t.x - mn);
               mm = mn;
@@ -883,7 +915,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             row_sm[irow] = make_float4(mm, lt, rm, 0.f);
           }
           if (!meet()) ok = false;
-          constexpr int kVec = D / 4, kAt = 4;   // threads of a row, four values each
+          constexpr int kVec = kCols / 4, kAt = 4;   // threads of a row, four values each
           for (int at0 = threadIdx.x; at0 < rows * kVec; at0 += kAt * kSoftThreads) {
             float4 acc[kAt];
 #pragma unroll
@@ -900,7 +932,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                 rr[y] = 0.f;
                 if (at < rows * kVec) {
                   v[y] = __ldcg(reinterpret_cast<const float4*>(src) + at);
-                  rr[y] = __ldcg(src + L::kRows * D + (at / kVec) * 4 + 2);
+                  rr[y] = __ldcg(src + L::kRows * kCols + (at / kVec) * 4 + 2);
                 }
               }
 #pragma unroll
@@ -922,9 +954,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                 const int oi = g->tile * L::kRows + rw;
                 const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
                 const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
-                *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
+                *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + g->col0 + d) =
                     make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
-                if (p.lse && d == 0)
+                if (p.lse && g->col0 + d == 0)
                   p.lse[(size_t)orow * p.q_heads + oh] = t.y == 0.f ? -INFINITY : (t.x + lg2(t.y)) * 0.69314718056f;
               }
             }
@@ -966,6 +998,7 @@ static cudaError_t launch_tc(const Params& p, int sms, cudaStream_t stream) {
 
 cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s) {
   const bool one = (long long)p.step.max_tokens * p.group <= kTileRows;
+  if (head_dim == 256) return f16 ? launch_tc<true, 256, 1>(p, sms, s) : launch_tc<false, 256, 1>(p, sms, s);
   if (head_dim == 64)
     return f16 ? (one ? launch_tc<true, 64, 1>(p, sms, s) : launch_tc<true, 64, 2>(p, sms, s))
                : (one ? launch_tc<false, 64, 1>(p, sms, s) : launch_tc<false, 64, 2>(p, sms, s));
@@ -974,8 +1007,7 @@ cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaSt
 }
 
 size_t many_parts_bytes(int head_dim, int sms) {
-  if (head_dim > 128) return 0;
-  const int part = head_dim == 64 ? TcLayout<64, 2>::kPart : TcLayout<128, 2>::kPart;
+  const int part = head_dim == 64 ? TcLayout<64, 2>::kPart : head_dim == 128 ? TcLayout<128, 2>::kPart : TcLayout<256, 1>::kPart;
   return (size_t)sms * 2 * part * sizeof(float);
 }
 

@@ -60,6 +60,21 @@ def test_windows_and_prompts(ns, lens, dim):
     c.check_attention(out, lse, scale)
 
 
+@pytest.mark.parametrize("ns,lens,heads,window,causal", [
+    ([29, 1, 0, 28], [29, 64, 9, 200], (8, 2), 0, True),     # 116 rows: the fewest that count as many for this width
+    ([130, 33], [130, 65], (1, 1), 0, True),                 # more than a tile of 128
+    ([60, 2], [1000, 1], (4, 2), 100, True),
+    ([60, 200], [63, 200], (3, 1), 17, True),
+    ([40, 64], [0, 161], (4, 1), 0, False),
+    ([150], [4001], (2, 1), 0, True),                        # one sequence over many CTAs
+])
+@pytest.mark.parametrize("page", [16, 128])
+def test_prompts_of_wide_heads(ns, lens, heads, window, causal, page):
+    c = Case(ns, lens, *heads, 256, page, "bf16" if page == 16 else "f16", seed=sum(ns) + page, pad=8)
+    out, lse, scale = _run(c, window=window, flags=0 if causal else lib8.KV8_FLAG_NOT_CAUSAL, pad_out=16)
+    c.check_attention(out, lse, scale, window, causal)
+
+
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 10**6])
 @pytest.mark.parametrize("ns,lens", [([1, 1, 1, 1], [1, 16, 130, 400]), ([5, 3, 40], [5, 90, 333]), ([150], [420])])
 def test_sliding_windows(ns, lens, window):
