@@ -37,14 +37,19 @@
 // The work is cut over all (sequence, row tile, kv head) items laid end to end, in units of one
 // granule for each warp, into equal runs, one for each CTA: lengths live on the device, so each CTA
 // finds its run from a scan of kv_len.  An item cut across CTAs is finished by the last of them to
-// arrive.  Two CTAs share an SM, so that one's start, join and drain hide behind the other's stream.
+// arrive.  Two to four CTAs share an SM, so that one's start, join and drain hide behind the others' streams.
+//
+// Measured (32 query heads, 8 kv heads of 128): 64 contexts of 6001-8191 146 us (6.4 TB/s, 94 % of a copy); one of
+// 131071 49.7 (5.4 TB/s with its join); 16 of 257-4099 22.2, where starts and joins take half; windows of 6 tokens on
+// 16 of 1001-5003 40.4, bound by issue slots and latency at 8 warps an SM.
 #include "kv8_attention.cuh"
 
 namespace w8a8 {
 namespace attn {
 
 // NT: 8-row tiles a warp holds.  A lane holds D NT / 4 sums, so the warps that an SM can hold follow
-// from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in CTAs of four.
+// from D NT: 16 of 128 registers, 12 of 168 or 8 of 255, in CTAs of four (eight for one tile of 128-wide heads: half
+// the parts to join).
 template <int D, int NT>
 struct Layout {
   static constexpr int kWarps = D * NT == 128 && NT == 1 ? 8 : 4;
@@ -63,8 +68,8 @@ struct Layout {
   static constexpr int kQBytes = kQShared ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int kSmem = 1024 + kRing + kQBytes;
   // Whether the next granule's scores are worked out beside this one's weights and sums, two independent streams
-  // of instructions: where there are registers for both.  (D = 128, one tile: 64 long contexts 150.4 -> 145.7 us;
-  // 24 rows 43.7 -> 46.6, D = 64 28.4 -> 30.0.)
+  // of instructions: where there are registers for both.  (D = 128, one tile: 64 long contexts 148.4 -> 146.2 us, one
+  // of 131071 tokens 51.3 -> 49.6; 24 rows 40.3 -> 46.8, D = 64 24.3 -> 25.8.)
   static constexpr bool kAhead = D == 128 && NT == 1;
   static constexpr int kRow = D + 4;                    // floats of a row in the join buffer
   // What an item costs beside its tokens (queries, first copies, join), in units: each item's place in
@@ -410,8 +415,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     // Granule j takes the slot that this warp has read.  The copy's writes are of the asynchronous proxy: without
     // the fence they can overtake the lanes' reads, which a barrier of the warp alone does not hold up (seen as a
     // granule's values replaced by those of the one after it in the slot, in one of 10^5).  After the products the
-    // reads have long returned and the fence costs nothing; where the next granule's scores are in hand already the
-    // copy is better early (24 rows 43.8 -> 40.0 us, 64-wide heads 24.6 -> 24.1, one tile of 128 147.2 -> 146.2).
+    // reads have long returned and the fence costs nothing (before them 24 rows 40.2 -> 43.8 us, heads of 64 24.3 ->
+    // 24.6).
     auto refill = [&](int j) {
       fence_async_shared();
       __syncwarp();
@@ -525,7 +530,6 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             vw[t][0] = v.x, vw[t][1] = v.y, vw[t][kWords - 2] = v.z, vw[t][kWords - 1] = v.w;
           }
         }
-        if (L::kAhead && bx == L::kBoxes - 1) refill(j + NS);   // every byte of the granule is in registers
 #pragma unroll
         for (int wd = 0; wd < kWords; ++wd) {
           uint32_t bf[2][4];   // [tokens 2c.. / 2c + 8..][d]
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
                             pb[i][1]);
         }
       }
-      if (!L::kAhead) refill(j + NS);
+      refill(j + NS);
     }
     count += (uint32_t)mine_n;
 

@@ -32,6 +32,11 @@
 // The work is cut like that of the other kernel: items (row tile, kv head) laid end to end in units of a
 // block and cut into equal runs; an item cut across CTAs is finished by the last to arrive, parts joined
 // in the CTAs' order, so replays give the same bits.
+//
+// Measured (32 query heads, 8 kv heads of 128): two prompts of 1900-2048 tokens on contexts of 5800-6144 421 us, 794
+// TFLOP/s, 41 % of a large matrix product's rate.  What bounds it is a stream's chain (scores, weights, sums: four waits
+// that wake a role, 250 cycles each, beside 2600 cycles of exponentials a block); the tensor pipe is busy 34 % of the
+// time.
 #include "kv8_attention.cuh"
 
 namespace w8a8 {
