@@ -63,8 +63,10 @@ struct Layout {
   static constexpr int kStage = 2 * kSide;
   static constexpr int kStages = 196608 / (kCtas * kWarps * kStage);   // a warp's ring
   static constexpr int kRing = kWarps * kStages * kStage;
-  // The queries' fragments are the same for every warp: in shared memory where registers are short.
-  static constexpr bool kQShared = D * NT > 256;
+  // The queries' fragments are the same for every warp: in shared memory where registers are short (D NT = 256, 32
+  // contexts of 8000, 8 kv heads: 32 rows of 64 150 -> 122 us, 4 of 256 170.7 -> 168.6; 16 contexts of 3000, 16 rows of
+  // 128 32.6 -> 31.6).
+  static constexpr bool kQShared = D * NT >= 256;
   static constexpr int kQBytes = kQShared ? NT * (D / 16) * 32 * 8 : 0;
   static constexpr int kSmem = 1024 + kRing + kQBytes;
   // Whether the next granule's scores are worked out beside this one's weights and sums, two independent streams
@@ -75,6 +77,10 @@ struct Layout {
   // What an item costs beside its tokens (queries, first copies, join), in units: each item's place in
   // the split is that much longer, so a run that crosses into another item gets fewer tokens.
   static constexpr int kLead = 3;
+  // Items of up to this many units are not cut where there is a CTA for each: a unit takes 0.9 us of a CTA alone, a
+  // join 2.9 (200 tokens, 8 rows of 2 kv heads: 7.0 -> 5.8 us, 32 such sequences 8.9 -> 7.4, heads of 64 6.4 -> 5.7, 24
+  // rows 11.0 -> 9.8; at five units 128-wide heads lose, 7.7 -> 8.2, at four those of 256, 7.9 -> 8.1).
+  static constexpr int kWhole = D == 256 ? 3 : 4;
   // A part of a split item in the workspace: kRows x D sums, then (m, l, r, -) of each row.
   static constexpr int kPart = kRows * (D + 4);
   static_assert(kWarps * kRows * kRow * 4 <= kRing, "the join buffer lies over the rings");
@@ -110,6 +116,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][NS];
   __shared__ long long scan_sm[kWarps];
+  __shared__ int2 items_sm[kWarps];   // items, and the units of the longest
   __shared__ struct {
     Span x;
     int b;
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   __shared__ float4 mlr_sm[kWarps][L::kRows];   // (m, l, r, -) of each warp's rows
   __shared__ float4 row_st[L::kRows];   // of each row: score multiplier, offset, first and one past the last token it sees
   __shared__ int2 range_sm[NT];
-  __shared__ int last_sm, abort_flag;
+  __shared__ int last_sm, abort_flag, even_sm;
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint2* const qsm = reinterpret_cast<uint2*>(ring + L::kRing);   // [NT][kSteps][32] fragments
 
@@ -143,28 +150,45 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   const int per = (p.step.seqs + kThreads - 1) / kThreads;   // sequences a thread scans
   const int s0 = min(p.step.seqs, (int)threadIdx.x * per), s1 = min(p.step.seqs, s0 + per);
   long long mine = 0;
+  int items = 0, longest = 0;
   Span x;   // the last sequence that this thread looked at
   for (int b = s0; b < s1; ++b) {
     x = load_span<L>(p, b);
     mine += (long long)x.tiles * x.span;
+    items = (int)min((long long)items + (long long)x.tiles * p.kv_heads, 1LL << 20);   // (more than any grid: all alike)
+    if (x.tiles > 0) longest = max(longest, x.units);
   }
   mine *= p.kv_heads;
   long long incl = mine;
+  int incl_items = items;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += t;
+    const int ti = __shfl_up_sync(0xffffffffu, incl_items, o);
+    if (lane >= o) incl += t, incl_items += ti;
   }
-  if (lane == 31) scan_sm[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) scan_sm[warp] = incl, items_sm[warp] = make_int2(incl_items, longest);
   __syncthreads();
   long long before = incl - mine, U = 0;
+  int before_items = incl_items - items, all_items = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += scan_sm[w];
+    if (w < warp) before += scan_sm[w], before_items += items_sm[w].x;
     U += scan_sm[w];
+    all_items += items_sm[w].x;
+    longest = max(longest, items_sm[w].y);
   }
-  const int ctas = (int)min((long long)gridDim.x, U);
+  // Few short items: one to a CTA, at the length of the longest, and no parts to join.
+  int even = 0;
+  if (longest <= L::kWhole && all_items <= (int)gridDim.x) {
+    even = L::kLead + longest;
+    before = (long long)before_items * even, mine = (long long)items * even, U = (long long)all_items * even;
+    x.span = even;
+  }
+  const int ctas = even ? all_items : (int)min((long long)gridDim.x, U);
   if ((int)blockIdx.x >= ctas) return;
+  if (threadIdx.x == 0) even_sm = even;
   const Runs runs(U, ctas);
   const long long u0 = runs.begin(blockIdx.x), u1 = runs.begin(blockIdx.x + 1);
   if (u0 >= before && u0 < before + mine) {
@@ -173,6 +197,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     int b = s0;
     for (; per > 1; ++b) {
       x = load_span<L>(p, b);
+      if (even) x.span = even;
       const long long n = (long long)x.tiles * x.span * p.kv_heads;
       if (u0 < at + n) break;
       at += n;
@@ -193,6 +218,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     while (u >= seq_u0 + (long long)x.tiles * x.span * p.kv_heads) {
       seq_u0 += (long long)x.tiles * x.span * p.kv_heads;
       x = load_span<L>(p, ++b);
+      if (even_sm) x.span = even_sm;
     }
     const int item = (int)quotient(u - seq_u0, x.span);
     const long long item_u0 = seq_u0 + (long long)item * x.span;   // its lead, then its units
@@ -553,7 +579,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     count += (uint32_t)mine_n;
 
     // ---------------------------------------------------------------- join the warps, then the CTAs
-    const bool whole = ub == 0 && ue == x.units;
+    const bool whole = ub == 0 && ue >= x.units;
     const int slot = item_u0 <= u0 ? 0 : 1;   // the run's first segment, or its last
     float* const part = p.parts + ((size_t)blockIdx.x * 2 + slot) * L::kPart;
     float* const buf = reinterpret_cast<float*>(ring);
@@ -745,7 +771,10 @@ static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStrea
   const long long rows = (long long)p.step.max_tokens * p.group;
   if (rows > few_rows(head_dim)) return launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
-    return rows <= 8 ? launch_few<kF16, 64, 1>(p, sms, s) : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s) : launch_few<kF16, 64, 4>(p, sms, s);
+    return rows <= 8    ? launch_few<kF16, 64, 1>(p, sms, s)
+           : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s)
+           : rows <= 24 ? launch_few<kF16, 64, 3>(p, sms, s)
+                        : launch_few<kF16, 64, 4>(p, sms, s);
   if (head_dim == 128)
     return rows <= 8    ? launch_few<kF16, 128, 1>(p, sms, s)
            : rows <= 16 ? launch_few<kF16, 128, 2>(p, sms, s)
