@@ -1,4 +1,4 @@
-// Attention over the 8-bit paged key-value cache: few query rows (single tokens, verify windows).
+// Attention over the 8-bit paged key-value cache: few query rows (single tokens, verify windows, small chunks).
 //
 // Row i of sequence b stands at position p = kv_len - n + i and sees the cached tokens
 // j in [max(0, p - window + 1), p] (causal) or [0, kv_len):
@@ -760,16 +760,22 @@ static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Rows of a sequence and kv head up to which this file's kernel runs.  Heads of 256 score twice in the other one and
-// stay here longer (16 rows a tile): 8 contexts of 3000, 128 rows 77 us here, 69 there; 4 of 1000, 80 rows 21 and 30;
-// 16 of 4000, 48 rows 79 and 108.
-constexpr long long few_rows(int head_dim) { return head_dim == 256 ? 112 : 32; }
+// Whether the other kernel takes a step of `rows` rows of a sequence and kv head: enough rows for its tiles of 128, and
+// enough tiles, as the parts of a tile cut over many CTAs cost it more to join than its products save.  Measured (us,
+// here / there): heads of 128, 16 contexts of 2000, 8 kv heads (128 tiles) 40 rows 62 / 51, 128 rows 111 / 62; 8 of 500 (64
+// tiles) 40 rows 21.6 / 22.2, 128 rows 30.1 / 29.6; 2 of 6000, 2 kv heads (4) 40 rows 25 / 29, 192 rows (8) 32 / 54; one of
+// 16000, 4 kv heads, 192 rows 52 / 59.  Heads of 256 (16 rows a tile here): 8 of 3000, 4 kv heads 128 rows (32) 78 / 88, 192
+// (64) 110 / 92; 2 of 6000, 2 kv heads 512 rows 74 / 96, 768 rows 103 / 101.
+static bool takes_many(const Params& p, int head_dim, long long rows) {
+  const long long fewest = head_dim == 256 ? 112 : 32, sure = head_dim == 256 ? 768 : 256;
+  return rows > sure || (rows > fewest && (rows + 127) / 128 * p.step.seqs * p.kv_heads >= 64);
+}
 
 // The narrowest variant that holds a sequence's rows in one tile, else the widest.
 template <bool kF16>
 static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
   const long long rows = (long long)p.step.max_tokens * p.group;
-  if (rows > few_rows(head_dim)) return launch_many(p, head_dim, kF16, sms, s);
+  if (takes_many(p, head_dim, rows)) return launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
     return rows <= 8    ? launch_few<kF16, 64, 1>(p, sms, s)
            : rows <= 16 ? launch_few<kF16, 64, 2>(p, sms, s)

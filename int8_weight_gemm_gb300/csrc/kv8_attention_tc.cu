@@ -24,11 +24,10 @@
 //  - four converter warps: 8 bits -> fp16 operands, two blocks of each ahead of the products;
 //  - one thread issues the products: W V of a block, then, when those have completed (the other stream's
 //    are in the pipe meanwhile), the next scores into the same tensor memory.
-// Heads of 256: a stream's sums of 256 columns and its scores do not fit half the tensor memory, nor the operands of
-// 128 tokens shared memory.  An item is then 128 of the values' columns, a block 64 tokens, and the streams are one
-// tile's blocks: half as many products again and twice the exponentials, and still 2.2 times as fast as 16 rows a warp
-// (two prompts of 2048 on contexts of 6000, 32 query heads: 886 us, 1923 so).  The converters bound it, with the
-// issuing warp's own time.
+// Heads of 256: the sums take half of tensor memory, so there is one stream, of one tile, with two places for the
+// scores of a block of 64 tokens: the next block's scores are there when a block's weights are done.  Four warps do the
+// exponentials and eight convert.  (Two prompts of 2048 on contexts of 6000, 32 query heads, 4 kv heads: 503 us, 664
+// TFLOP/s; two streams of half the columns each, scoring twice, 886; 16 rows a warp 1923.)
 // The work is cut like that of the other kernel: items (row tile, kv head) laid end to end in units of a
 // block and cut into equal runs; an item cut across CTAs is finished by the last to arrive, parts joined
 // in the CTAs' order, so replays give the same bits.
@@ -43,10 +42,7 @@ namespace w8a8 {
 namespace attn {
 
 constexpr int kTileRows = 128;    // rows of a tile
-constexpr int kSoftWarps = 8;     // four for each stream
-constexpr int kSoftThreads = 32 * kSoftWarps;
-constexpr int kConvWarps = 4;
-constexpr int kProducerWarp = kSoftWarps + kConvWarps;
+constexpr int kProducerWarp = 12;   // after the softmax warps and the converters
 constexpr int kMmaWarp = kProducerWarp + 1;
 constexpr int kTcThreads = 32 * (kMmaWarp + 1);
 constexpr int kScales = 8;        // blocks whose scales are held
@@ -54,23 +50,25 @@ constexpr int kScales = 8;        // blocks whose scales are held
 template <int D, int kTiles>
 struct TcLayout {
   static constexpr int kRows = kTiles * kTileRows;
-  // Heads of 256: an item is 128 of the values' columns (two items score alike), a block 64 tokens: its sums and
-  // scores fit a stream's tensor memory, its operands shared memory.
-  static constexpr int kCols = D < 128 ? D : 128;     // columns of values
-  static constexpr int kSplits = D / kCols;           // items of a head and row tile
-  static constexpr int kBlock = D > 128 ? 64 : 128;   // tokens of a block
+  // Heads of 256: one stream with two places for scores, blocks of 64 tokens.
+  static constexpr bool kWide = D > 128;
+  static constexpr int kSoftWarps = kWide ? 4 : 8;    // four for each stream
+  static constexpr int kConvWarps = 12 - kSoftWarps;
+  static constexpr int kBox = D < 128 ? D : 128;      // columns of a copy
+  static constexpr int kBoxes = D / kBox;
+  static constexpr int kBlock = kWide ? 64 : 128;     // tokens of a block
   static constexpr int kGrans = kBlock / kGranule;    // granules of a block
   static constexpr int kUnit = kBlock;
   static constexpr int kLead = 3;
   static constexpr int kQBytes = kTileRows * D * 2;
   static constexpr int kHalf = kBlock * 128;          // 64 fp16 of each of a block's tokens
-  static constexpr int kK16 = kBlock * D * 2, kV16 = kBlock * kCols * 2;   // fp16 blocks
+  static constexpr int kBlk16 = kBlock * D * 2;   // an fp16 block
   static constexpr int kSlot = kBlock * D;            // an 8-bit block
   // 8-bit blocks in flight: with one tile the cache comes from HBM at the pace of the products.
-  static constexpr int kSlots = kTiles == 2 ? 2 : 4;
-  static constexpr int kBytes = 1024 + kTiles * kQBytes + 2 * (kK16 + kV16) + kSlots * kSlot;
-  static constexpr int kSCol = 0, kOCol = kBlock, kStreamCols = 256;   // tensor-memory columns of a stream
-  static constexpr int kPart = kRows * (kCols + 4);   // floats: sums, then (m, l, r, -) of each row
+  static constexpr int kSlots = kTiles == 2 || kWide ? 2 : 4;
+  static constexpr int kBytes = 1024 + kTiles * kQBytes + 4 * kBlk16 + kSlots * kSlot;
+  static constexpr int kSCol = 0, kOCol = kWide ? 256 : kBlock, kStreamCols = 256;   // tensor-memory columns of a stream
+  static constexpr int kPart = kRows * (D + 4);       // floats: sums, then (m, l, r, -) of each row
   static_assert(kBytes + 2048 <= 232448, "shared memory");
 };
 
@@ -100,14 +98,14 @@ struct Segment {
   int nb;                    // blocks
   int T0;                    // first token
   int row0, pos0, len;       // of the sequence: first row, position of its first row, cached tokens
-  int h, col0, tile, rows;   // kv head, first column of the values, row tile, rows of the tile that exist
+  int h, tile, rows;         // kv head, row tile, rows of the tile that exist
   int whole;                 // the item's only part
   int slot;                  // else: its place among this CTA's parts,
   int first, parts, slot0;   //   and the item's first CTA, number of CTAs, and place in the first one
 };
 constexpr int kSegments = 4;   // segments under way
 
-// A run's segments, one item's part each.  Items are ordered by sequence, kv head and its columns (h), row tile.
+// A run's segments, one item's part each.  Items are ordered by sequence, kv head, row tile.
 template <typename L>
 struct Walk {
   long long u, u1, item_u0;
@@ -121,7 +119,7 @@ struct Walk {
         item_u0 += L::kLead + t.units;
         if (++tile == tiles) {
           tile = 0;
-          if (++h == p.kv_heads * L::kSplits) {
+          if (++h == p.kv_heads) {
             h = 0;
             do {
               load_seq(p.step, ++b, 1 << p.page_shift, false, p.status, s);
@@ -179,11 +177,6 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(on));
   return on != 0;
 }
-
-template <int N>
-struct Const {
-  static constexpr int value = N;
-};
 
 // Shared-memory descriptors with the 128-byte swizzle (rows of 128 bytes, atoms of 8 rows, 1024-byte
 // aligned; version 1 in bits 46..47, layout 2 in bits 61..63).  K-major: the rows are the operand's rows,
@@ -253,7 +246,8 @@ struct alignas(16) GranScale {
 template <bool kF16, int D, int kTiles>
 __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const __grid_constant__ Params p) {
   using L = TcLayout<D, kTiles>;
-  constexpr int kSlots = L::kSlots, kBlock = L::kBlock, kGrans = L::kGrans, kCols = L::kCols;
+  constexpr int kSlots = L::kSlots, kBlock = L::kBlock, kGrans = L::kGrans, kSoftWarps = L::kSoftWarps, kConvWarps = L::kConvWarps;
+  constexpr bool kWide = L::kWide, kAlternate = kTiles == 1 && !kWide;   // (the streams are one tile's even and odd blocks)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t slot_full[kSlots], slot_empty[kSlots];   // 8-bit blocks
   __shared__ __align__(8) uint64_t sc_full[kScales];                        // scales of a block
@@ -275,8 +269,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
 
   uint8_t* const qtile = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const k16 = qtile + kTiles * L::kQBytes;   // [2]
-  uint8_t* const v16 = k16 + 2 * L::kK16;             // [2]
-  uint8_t* const ring = v16 + 2 * L::kV16;            // [kSlots] 8-bit blocks
+  uint8_t* const v16 = k16 + 2 * L::kBlk16;           // [2]
+  uint8_t* const ring = v16 + 2 * L::kBlk16;          // [kSlots] 8-bit blocks
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -313,7 +307,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     const int tiles = tiles_of<L>(p, s);
     long long n = 0;
     for (int t = 0; t < tiles; ++t) n += L::kLead + tile_span<L>(p, s, t).units;
-    return n * p.kv_heads * L::kSplits;
+    return n * p.kv_heads;
   };
   for (int b = s0; b < s1; ++b) {
     Seq s;
@@ -396,7 +390,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           g.nb = nb;
           g.T0 = wk.t.lo + wk.ub * kBlock;
           g.row0 = wk.s.row0, g.pos0 = wk.s.len - wk.s.n, g.len = wk.s.len;
-          g.h = wk.h / L::kSplits, g.col0 = wk.h % L::kSplits * kCols, g.tile = wk.tile, g.rows = (int)min((long long)L::kRows, (long long)wk.s.n * p.group - (long long)wk.tile * L::kRows);
+          g.h = wk.h, g.tile = wk.tile, g.rows = (int)min((long long)L::kRows, (long long)wk.s.n * p.group - (long long)wk.tile * L::kRows);
           g.whole = wk.whole();
           g.slot = wk.item_u0 <= u0 ? 0 : 1;
           g.first = runs.owner(wk.item_u0 + L::kLead);
@@ -423,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             atomicOr(p.status, W8A8_DEV_BAD_INDEX);
             live = false;
           } else {
-            const size_t at = (size_t)page * p.kv_heads + wk.h / L::kSplits;
+            const size_t at = (size_t)page * p.kv_heads + wk.h;
             row = (int)(at << p.page_shift) + (t & ((1 << p.page_shift) - 1));
             const float ks = __ldg(p.ks + at), vs = __ldg(p.vs + at);
             sc.ks = fabsf(ks);
@@ -441,7 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           const bool own = lane / kGrans == i;
           if (own) scales[n % kScales][lane % kGrans] = sc, turns[n % kScales][lane % kGrans] = turn;
           arrive_warp(&sc_full[n % kScales]);
-          const uint32_t tokens = (uint32_t)__popc((lives >> (kGrans * i)) & ((1u << kGrans) - 1u)) * kGranule;
+          const uint32_t bytes = (uint32_t)__popc((lives >> (kGrans * i)) & ((1u << kGrans) - 1u)) * kGranule * D;
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
@@ -449,18 +443,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
               ok = false;
               break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], tokens * (side ? kCols : D));
+            if (lane == 0) mbar_arrive_expect_tx(&slot_full[slot], bytes);
             ++copies;
             __syncwarp();
             if (own && live) {
               // (A box is 128 columns at most; those of a block's granules lie together.)
-              uint8_t* const dst = ring + slot * L::kSlot + lane % kGrans * kGranule * kCols;
-              if (side) {
-                tma_load_2d(dst, &p.vmap, wk.h % L::kSplits * kCols, row, &slot_full[slot]);
-              } else {
+              uint8_t* const dst = ring + slot * L::kSlot + lane % kGrans * kGranule * L::kBox;
 #pragma unroll
-                for (int x = 0; x < L::kSplits; ++x) tma_load_2d(dst + x * kBlock * kCols, &p.kmap, x * kCols, row, &slot_full[slot]);
-              }
+              for (int x = 0; x < L::kBoxes; ++x)
+                tma_load_2d(dst + x * kBlock * L::kBox, side ? &p.vmap : &p.kmap, x * L::kBox, row, &slot_full[slot]);
             }
           }
           if (!ok) break;
@@ -489,57 +480,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         for (int side = 0; side < 2; ++side) {
           const uint32_t slot = (2 * n + side) % kSlots, use = (2 * n + side) / kSlots;
           const uint8_t* const src = ring + slot * L::kSlot;
-          uint8_t* const dst = side ? v16 + (n & 1) * L::kV16 : k16 + (n & 1) * L::kK16;
+          uint8_t* const dst = (side ? v16 : k16) + (n & 1) * L::kBlk16;
           if (!wait_all(&slot_full[slot], use & 1u, &abort_flag, p.status) ||
               (n >= 2 && !wait_all(side ? &v_empty[n & 1] : &k_empty[n & 1], ((n >> 1) - 1) & 1u, &abort_flag, p.status))) {
             ok = false;
             break;
           }
-          // A warp takes a quarter of the tokens: eight rows by four 16-byte pieces at a time, so that neither the reads
+          // A warp takes its share of the tokens eight rows by four 16-byte pieces at a time, so that neither the reads
           // (swizzled by the copy) nor the writes (swizzled for the products) meet in a bank.  All reads go out first.
-          auto convert = [&](auto cols) {
-            constexpr int kEights = kBlock / 8 / kConvWarps, kY = decltype(cols)::value / 64;
-            uint4 w[kEights][kY];
+          constexpr int kEights = kBlock / 8 / kConvWarps, kY = D / 64;
+          uint4 w[kEights][kY];
 #pragma unroll
-            for (int i = 0; i < kEights; ++i) {
-              const int t = (kEights * cw + i) * 8 + (lane & 7);
+          for (int i = 0; i < kEights; ++i) {
+            const int t = (kEights * cw + i) * 8 + (lane & 7);
 #pragma unroll
-              for (int y = 0; y < kY; ++y) {
-                const int piece = (lane >> 3) + 4 * y;
-                w[i][y] = D == 64 ? *reinterpret_cast<const uint4*>(src + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4))
-                                  : *reinterpret_cast<const uint4*>(src + (piece >> 3) * kBlock * kCols + t * 128 + (((piece & 7) ^ (t & 7)) << 4));
-              }
+            for (int y = 0; y < kY; ++y) {
+              const int piece = (lane >> 3) + 4 * y;
+              w[i][y] = D == 64 ? *reinterpret_cast<const uint4*>(src + t * 64 + ((piece ^ ((t >> 1) & 3)) << 4))
+                                : *reinterpret_cast<const uint4*>(src + (piece >> 3) * kBlock * L::kBox + t * 128 + (((piece & 7) ^ (t & 7)) << 4));
             }
+          }
 #pragma unroll
-            for (int i = 0; i < kEights; ++i) {
-              const uint32_t turn = turns[n % kScales][(kEights * cw + i) >> 1];
-              const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
-              const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
-              const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
-              const int t = (kEights * cw + i) * 8 + (lane & 7);
+          for (int i = 0; i < kEights; ++i) {
+            const uint32_t turn = turns[n % kScales][(kEights * cw + i) >> 1];
+            const uint32_t f = side ? turn >> 16 : turn & 0xFFFFu;
+            const __half2 sg = __half2half2(__ushort_as_half((uint16_t)f));
+            const __half2 of = __hmul2(sg, __half2half2(__ushort_as_half(0xE480)));   // -1152
+            const int t = (kEights * cw + i) * 8 + (lane & 7);
 #pragma unroll
-              for (int y = 0; y < kY; ++y) {
-                const int piece = (lane >> 3) + 4 * y;
-                const uint32_t in[4] = {w[i][y].x, w[i][y].y, w[i][y].z, w[i][y].w};
-                uint32_t out[8];
+            for (int y = 0; y < kY; ++y) {
+              const int piece = (lane >> 3) + 4 * y;
+              const uint32_t in[4] = {w[i][y].x, w[i][y].y, w[i][y].z, w[i][y].w};
+              uint32_t out[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  // fp16 0x6400 | b = 1024 + b, so (1024 + b) sg - 1152 sg = sg (b - 128), exactly.
-                  const uint32_t a = __byte_perm(in[k], 0x64646464u, 0x4140), c = __byte_perm(in[k], 0x64646464u, 0x4342);
-                  const __half2 ha = __hfma2(*reinterpret_cast<const __half2*>(&a), sg, of);
-                  const __half2 hc = __hfma2(*reinterpret_cast<const __half2*>(&c), sg, of);
-                  out[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
-                  out[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hc);
-                }
-                uint8_t* const row = dst + (piece >> 2) * L::kHalf + t * 128;
-                const int ch = 2 * (piece & 3);
-                *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-                *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+              for (int k = 0; k < 4; ++k) {
+                // fp16 0x6400 | b = 1024 + b, so (1024 + b) sg - 1152 sg = sg (b - 128), exactly.
+                const uint32_t a = __byte_perm(in[k], 0x64646464u, 0x4140), c = __byte_perm(in[k], 0x64646464u, 0x4342);
+                const __half2 ha = __hfma2(*reinterpret_cast<const __half2*>(&a), sg, of);
+                const __half2 hc = __hfma2(*reinterpret_cast<const __half2*>(&c), sg, of);
+                out[2 * k] = *reinterpret_cast<const uint32_t*>(&ha);
+                out[2 * k + 1] = *reinterpret_cast<const uint32_t*>(&hc);
               }
+              uint8_t* const row = dst + (piece >> 2) * L::kHalf + t * 128;
+              const int ch = 2 * (piece & 3);
+              *reinterpret_cast<uint4*>(row + ((ch ^ (t & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (t & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
             }
-          };
-          if (D == kCols || side) convert(Const<kCols>());
-          else convert(Const<D>());
+          }
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
@@ -555,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     // address in 16 bytes and moves by constants.  (One warp for both streams: with one each, the products of
     // two accumulators mix in the pipe and each takes longer; prompt chunk 441 -> 521 us.)
     constexpr uint32_t idesc_s = idesc_f16_f32(kTileRows, kBlock);
-    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, kCols) | (1u << 16);   // B is MN-major
+    constexpr uint32_t idesc_o = idesc_f16_f32(kTileRows, D) | (1u << 16);   // B is MN-major
     const uint64_t dq = desc_kmajor(smem_addr(qtile)), dk = desc_kmajor(smem_addr(k16)), dv = desc_mnmajor(smem_addr(v16), L::kHalf);
     const uint32_t q_lo = (uint32_t)dq, k_lo = (uint32_t)dk, k_hi = (uint32_t)(dk >> 32), v_lo = (uint32_t)dv, v_hi = (uint32_t)(dv >> 32);
     auto desc = [](uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); };
@@ -567,6 +554,46 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       const int nb = g->nb;
       const uint32_t q_use = seg & 1u;
       end_segment();
+      if constexpr (kWide) {
+        // Scores of a block go out before the products of the weights of the one before it, into the place of the
+        // weights before those.
+        ok = wait(&q_full[0], q_use);
+#pragma unroll 1
+        for (int i = -1; ok && i < nb; ++i) {
+          const uint32_t n = blk + (uint32_t)i, nn = n + 1, u = n & 1u, uu = nn & 1u;
+          if (i + 1 < nb) {
+            ok = wait(&k_full[uu], (nn >> 1) & 1u) && (i < 1 || wait(&pv_done[uu], ((n - 1) >> 1) & 1u));
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t kl = k_lo + uu * (uint32_t)(L::kBlk16 >> 4);
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t qo = (uint32_t)(((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), ko = (uint32_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
+                umma_f16_ss(uu * kBlock, desc(q_lo + qo, k_hi), desc(kl + ko, k_hi), idesc_s, k > 0);
+              }
+              umma_commit(&s_full[uu]);
+              umma_commit(&k_empty[uu]);
+            }
+            __syncwarp();
+          }
+          if (i < 0) continue;
+          ok = wait(&v_full[u], (n >> 1) & 1u) && wait(&p_ready[u], (n >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t lo = v_lo + u * (uint32_t)(L::kBlk16 >> 4);
+#pragma unroll
+            for (int k = 0; k < kBlock / 16; ++k)
+              umma_f16_tmem_a(L::kOCol, u * kBlock + 8 * k, desc(lo + (uint32_t)(k * 16 * 128 >> 4), v_hi), idesc_o, i > 0 || k > 0);
+            umma_commit(&pv_done[u]);
+            umma_commit(&v_empty[u]);
+          }
+          __syncwarp();
+        }
+        blk += nb;
+        continue;
+      }
       const int n0 = kTiles == 2 ? nb : (nb + 1) / 2, n1 = kTiles == 2 ? nb : nb / 2;
       // Steps in order: (stream, turn) = (0, -1), (1, -1), (0, 0), (1, 0), ...: the products of a turn's weights
       // with its values, then, where there is one, the next turn's scores.
@@ -584,7 +611,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t lo = v_lo + u * (uint32_t)(L::kV16 >> 4);
+            const uint32_t lo = v_lo + u * (uint32_t)(L::kBlk16 >> 4);
 #pragma unroll
             for (int k = 0; k < kBlock / 16; ++k)
               umma_f16_tmem_a(t + L::kOCol, t + (uint32_t)(L::kSCol + 8 * k), desc(lo + (uint32_t)(k * 16 * 128 >> 4), v_hi), idesc_o, i > 0 || k > 0);
@@ -602,7 +629,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         if (!ok || !more) continue;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t ql = q_lo + (kTiles == 2 ? s : 0) * (uint32_t)(L::kQBytes >> 4), kl = k_lo + ub * (uint32_t)(L::kK16 >> 4);
+          const uint32_t ql = q_lo + (kTiles == 2 ? s : 0) * (uint32_t)(L::kQBytes >> 4), kl = k_lo + ub * (uint32_t)(L::kBlk16 >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t qo = (uint32_t)(((k >> 2) * kTileRows * 128 + (k & 3) * 32) >> 4), ko = (uint32_t)(((k >> 2) * L::kHalf + (k & 3) * 32) >> 4);
@@ -627,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
     const int row = 32 * quad + lane;                              // of the tile
     const int irow = kTiles == 2 ? st * kTileRows + row : row;     // of the item
     const uint32_t t_lane = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(st * L::kStreamCols);
-    const uint32_t t_s = t_lane + L::kSCol, t_o = t_lane + L::kOCol;
+    const uint32_t t_o = t_lane + L::kOCol;
     uint32_t blk = 0, cnt = 0, join_phase = 0;
     auto meet = [&]() {   // bounded meeting of the softmax warps
       arrive_warp(&join_bar);
@@ -635,10 +662,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       join_phase ^= 1u;
       return ok;
     };
+    // The products of a stream's block c with its values are done.  (A wide head's scores run a block ahead of them: one
+    // barrier could be two phases behind, which its parity does not tell from done.)
+    auto wait_sums = [&](uint32_t c) {
+      return wait_all(&pv_done[kWide ? c & 1u : (uint32_t)st], (kWide ? c >> 1 : c) & 1u, &abort_flag, p.status);
+    };
     bool ok = true;
     while (const Segment* g = ok ? next_segment() : nullptr) {
       const int nb = g->nb;
-      const int ns = kTiles == 2 ? nb : st == 0 ? (nb + 1) / 2 : nb / 2;
+      const int ns = !kAlternate ? nb : st == 0 ? (nb + 1) / 2 : nb / 2;
       const int T0 = g->T0;
       const bool live = irow < g->rows;
       const int ri = g->tile * L::kRows + (live ? irow : 0);
@@ -682,11 +714,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       // ------------------------------------------------ blocks
       float m = kFloor, r = kFloor, hs = 0.f, l = 0.f;
       for (int i = 0; ok && i < ns; ++i, ++cnt) {
-        const int j = kTiles == 2 ? i : 2 * i + st;
+        const int j = kAlternate ? 2 * i + st : i;
         const uint32_t n = blk + (uint32_t)j;
+        // The place of the scores: a stream's own; the block's of a wide head.
+        const uint32_t at = kWide ? n & 1u : (uint32_t)st, t_s = t_lane + L::kSCol + (kWide ? at * kBlock : 0u);
         const int T = T0 + j * kBlock;
         if (!wait_all(&sc_full[n % kScales], (n / kScales) & 1u, &abort_flag, p.status) ||
-            !wait_all(&s_full[st], cnt & 1u, &abort_flag, p.status)) {
+            !wait_all(&s_full[at], (kWide ? n >> 1 : cnt) & 1u, &abort_flag, p.status)) {
           ok = false;
           break;
         }
@@ -780,8 +814,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                   r = rn;
                   hs = ex2(m - rn);
                   far = __any_sync(0xffffffffu, hs * fmaxf(vs[0], vs[1]) > kFar);
-                  if (i > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) ok = false;
-                  if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? kCols : 0, t_s, ch, down);
+                  if (i > 0 && !wait_sums(cnt - 1)) ok = false;
+                  if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
                 }
               } while (moved);
               float l0, l1;
@@ -793,13 +827,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           tmem_wait_st();
           tc_fence_before();
         }
-        arrive_warp(&p_ready[st]);
+        arrive_warp(&p_ready[at]);
       }
       blk += nb;
       if (!ok) break;
 
       // ------------------------------------------------ the segment's end
-      if (ns > 0 && !wait_all(&pv_done[st], (cnt - 1) & 1u, &abort_flag, p.status)) {
+      if (ns > 0 && !wait_sums(cnt - 1)) {
         ok = false;
         break;
       }
@@ -807,9 +841,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       float scale_own = 1.f, scale_other = 0.f;   // of the two streams' sums (one tile: they join here)
       // The second stream's (m, l, r), then kX columns of its sums at a time ([kX][128]), go over through the
       // queries' shared memory (every score has been computed).
-      constexpr int kX = L::kQBytes / (kTileRows * 4) < kCols ? L::kQBytes / (kTileRows * 4) : kCols;
+      constexpr int kX = L::kQBytes / (kTileRows * 4);
       float* const xch = reinterpret_cast<float*>(qtile);
-      if (kTiles == 1) {
+      if (kAlternate) {
         bool met = meet();   // the other stream's scores too
         if (st == 1) xch[row] = m, xch[kTileRows + row] = l, xch[2 * kTileRows + row] = r;
         met = met && meet();
@@ -831,8 +865,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       float* const part = p.parts + ((size_t)blockIdx.x * 2 + g->slot) * L::kPart;
       const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(r - m);
 #pragma unroll 1
-      for (int c0 = 0; c0 < kCols; c0 += 32) {
-        if (kTiles == 1 && c0 % kX == 0) {
+      for (int c0 = 0; c0 < D; c0 += 32) {
+        if (kAlternate && c0 % kX == 0) {
           if (!meet()) ok = false;
           if (st == 1) {
 #pragma unroll 1
@@ -847,7 +881,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           if (!meet()) ok = false;
           if (!ok) break;
         }
-        if (kTiles == 1 && st == 1) continue;
+        if (kAlternate && st == 1) continue;
         uint32_t o[32];
         tmem_ld32(t_o + c0, o);
         tmem_wait_ld32(o);
@@ -855,10 +889,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           v[k] = __uint_as_float(o[k]);
-          if (kTiles == 1) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
+          if (kAlternate) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
         }
         if (live && whole) {
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + g->col0 + c0);
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             float y[8];
@@ -871,47 +905,59 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             dst[k / 8] = pack8<kF16>(y);
           }
         } else if (live) {
-          float4* const dst = reinterpret_cast<float4*>(part + irow * kCols + c0);
+          float4* const dst = reinterpret_cast<float4*>(part + irow * D + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
       }
       if (!ok) break;
       if (live && (kTiles == 2 || st == 0)) {
-        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * kCols + irow * 4) = make_float4(m, l, r, 0.f);
-        else if (p.lse && g->col0 == 0) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
+        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
+        else if (p.lse) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
       }
       tc_fence_before();
       if (!whole) {
         // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.  (The
         // meeting orders the warps' stores before thread 0's release, and its acquire before their reads.)
-        const int np = g->parts;
-        if (!meet()) {
-          ok = false;
-          break;
+        // Many parts join first in groups of about sqrt(n), each by the last of its CTAs, so that no CTA reads more than
+        // a few: one SM reads some 50 KB/us (256 rows on 16000 tokens, 4 kv heads,
+        // 38 parts: 131 us without groups, 71 with them).
+        constexpr int kGroup = 8;
+        const int first = g->first, slot0 = g->slot0, np = g->parts, rows = g->rows;
+        const float* const part0 = p.parts + ((size_t)first * 2 + slot0) * L::kPart;
+        const float* const part1 = p.parts + (size_t)first * 2 * L::kPart;   // part i > 0: 2 i places on
+        auto part_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * L::kPart; };
+        int group = np;
+        if (np > kGroup) {
+          group = 3;
+          while (group * group < np) ++group;
         }
-        if (threadIdx.x == 0) {
-          const uint32_t old = atom_add_acq_rel_u32(p.counters + g->first, 1u);
-          if (old >= (uint32_t)np) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
-          if (old == (uint32_t)np - 1) p.counters[g->first] = 0u;   // ready for the next call
-          last_sm = old == (uint32_t)np - 1;
-        }
-        if (!meet()) {
-          ok = false;
-          break;
-        }
-        if (last_sm) {
-          const float* const part0 = p.parts + ((size_t)g->first * 2 + g->slot0) * L::kPart;
-          const float* const part1 = p.parts + (size_t)g->first * 2 * L::kPart;   // part i > 0: 2 i places on
-          auto part_of = [&](int i) { return i == 0 ? part0 : part1 + (size_t)i * 2 * L::kPart; };
-          const int rows = g->rows;
+        const int groups = (np + group - 1) / group, lead = ((int)blockIdx.x - first) / group * group;
+        int base = lead, step = 1, count = min(group, np - lead);
+        uint32_t* counter = groups > 1 ? p.group_counters + 2 * (first + lead) + (lead == 0 ? slot0 : 0) : p.counters + first;
+        for (bool top = groups == 1;; top = true) {
+          if (!meet()) {
+            ok = false;
+            break;
+          }
+          if (threadIdx.x == 0) {
+            const uint32_t old = atom_add_acq_rel_u32(counter, 1u);
+            if (old >= (uint32_t)count) atomicOr(p.status, W8A8_DEV_COUNTER_CORRUPT);
+            if (old == (uint32_t)count - 1) *counter = 0u;   // ready for the next call
+            last_sm = old == (uint32_t)count - 1;
+          }
+          if (!meet()) {
+            ok = false;
+            break;
+          }
+          if (!last_sm) break;
           // A thread for each row's statistics, then a warp for a row's sums, kAt rows at a time.
           float4* const row_sm = reinterpret_cast<float4*>(qtile);   // (m, l, r, -)
           if (irow < rows && (kTiles == 2 || st == 0)) {
             float mm = kFloor, rm = kFloor, lt = 0.f;
 #pragma unroll 4
-            for (int i = 0; i < np; ++i) {
-              const float4 t = __ldcg(reinterpret_cast<const float4*>(part_of(i) + L::kRows * kCols) + irow);
+            for (int i = 0; i < count; ++i) {
+              const float4 t = __ldcg(reinterpret_cast<const float4*>(part_of(base + step * i) + L::kRows * D) + irow);
               const float mn = fmaxf(mm, t.x);
               lt = lt * ex2(mm - mn) + t.y * ex2(t.x - mn);
               mm = mn;
@@ -920,14 +966,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             row_sm[irow] = make_float4(mm, lt, rm, 0.f);
           }
           if (!meet()) ok = false;
-          constexpr int kVec = kCols / 4, kAt = 4;   // threads of a row, four values each
+          constexpr int kVec = D / 4, kAt = 4, kSoftThreads = 32 * kSoftWarps;   // kVec: threads of a row, four values each
           for (int at0 = threadIdx.x; at0 < rows * kVec; at0 += kAt * kSoftThreads) {
             float4 acc[kAt];
 #pragma unroll
             for (int y = 0; y < kAt; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-            for (int i = 0; i < np; ++i) {
-              const float* const src = part_of(i);
+            for (int i = 0; i < count; ++i) {
+              const float* const src = part_of(base + step * i);
               float4 v[kAt];
               float rr[kAt];
 #pragma unroll
@@ -937,7 +983,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                 rr[y] = 0.f;
                 if (at < rows * kVec) {
                   v[y] = __ldcg(reinterpret_cast<const float4*>(src) + at);
-                  rr[y] = __ldcg(src + L::kRows * kCols + (at / kVec) * 4 + 2);
+                  rr[y] = __ldcg(src + L::kRows * D + (at / kVec) * 4 + 2);
                 }
               }
 #pragma unroll
@@ -953,23 +999,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
 #pragma unroll
             for (int y = 0; y < kAt; ++y) {
               const int at = at0 + y * kSoftThreads;
-              if (at < rows * kVec) {
-                const int rw = at / kVec, d = 4 * (at % kVec);
-                const float4 t = row_sm[rw];
-                const int oi = g->tile * L::kRows + rw;
-                const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
-                const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
-                *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + g->col0 + d) =
-                    make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
-                if (p.lse && g->col0 + d == 0)
-                  p.lse[(size_t)orow * p.q_heads + oh] = t.y == 0.f ? -INFINITY : (t.x + lg2(t.y)) * 0.69314718056f;
+              if (at >= rows * kVec) continue;
+              if (!top) {
+                // The group's sums take the place of its first part's; its statistics once every thread has read them.
+                *(reinterpret_cast<float4*>(const_cast<float*>(part_of(base))) + at) = acc[y];
+                continue;
               }
+              const int rw = at / kVec, d = 4 * (at % kVec);
+              const float4 t = row_sm[rw];
+              const int oi = g->tile * L::kRows + rw;
+              const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
+              const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
+              *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
+                  make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
+              if (p.lse && d == 0)
+                p.lse[(size_t)orow * p.q_heads + oh] = t.y == 0.f ? -INFINITY : (t.x + lg2(t.y)) * 0.69314718056f;
             }
           }
-          if (!meet()) ok = false;   // the statistics' place is the next queries'
+          if (!meet()) ok = false;   // the statistics' place is the next queries', or the next join's
+          if (top || !ok) break;
+          if (irow < rows && (kTiles == 2 || st == 0))
+            *(reinterpret_cast<float4*>(const_cast<float*>(part_of(base)) + L::kRows * D) + irow) = row_sm[irow];
+          base = 0, step = group, count = groups;
+          counter = p.counters + first;
         }
+        if (!ok) break;
       }
-      if (kTiles == 1 && !meet()) ok = false;   // the exchange is over: the next queries may take its place
+      if (kAlternate && !meet()) ok = false;   // the exchange is over: the next queries may take its place
       end_segment();
     }
   }

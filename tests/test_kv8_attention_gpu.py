@@ -61,8 +61,11 @@ def test_windows_and_prompts(ns, lens, dim):
 
 
 @pytest.mark.parametrize("ns,lens,heads,window,causal", [
-    ([29, 1, 0, 28], [29, 64, 9, 200], (8, 2), 0, True),     # 116 rows: the fewest that count as many for this width
+    ([29, 1, 0, 28], [29, 64, 9, 200], (8, 2), 0, True),
     ([130, 33], [130, 65], (1, 1), 0, True),                 # more than a tile of 128
+    ([129, 2], [300, 77], (8, 1), 0, True),                  # 1032 rows of a kv head
+    ([97, 300], [97, 1003], (16, 2), 130, True),
+    ([100], [1503], (8, 1), 0, False),
     ([60, 2], [1000, 1], (4, 2), 100, True),
     ([60, 200], [63, 200], (3, 1), 17, True),
     ([40, 64], [0, 161], (4, 1), 0, False),
@@ -71,6 +74,20 @@ def test_windows_and_prompts(ns, lens, dim):
 @pytest.mark.parametrize("page", [16, 128])
 def test_prompts_of_wide_heads(ns, lens, heads, window, causal, page):
     c = Case(ns, lens, *heads, 256, page, "bf16" if page == 16 else "f16", seed=sum(ns) + page, pad=8)
+    out, lse, scale = _run(c, window=window, flags=0 if causal else lib8.KV8_FLAG_NOT_CAUSAL, pad_out=16)
+    c.check_attention(out, lse, scale, window, causal)
+
+
+@pytest.mark.parametrize("dim,longest", [(64, 9), (64, 32), (128, 9), (128, 32), (128, 60), (256, 32), (256, 60)])
+@pytest.mark.parametrize("window,causal,dtype", [(0, True, "bf16"), (37, True, "f16"), (0, False, "bf16")])
+def test_many_sequences_of_many_rows(dim, longest, window, causal, dtype):
+    # Tiles enough for the kernel of many rows with 36 to 240 rows of a kv head; sequences without rows or tokens,
+    # single rows, fewer tokens than rows, and a few long ones whose tiles are cut.
+    rng = np.random.default_rng(dim + longest)
+    ns = [0, 1, longest, longest] + rng.integers(1, longest + 1, 31).tolist()
+    lens = [9, 1, 0, longest // 2] + [int(n + rng.integers(0, 300)) for n in ns[4:]]
+    lens[7], lens[20] = 3001, 1100
+    c = Case(ns, lens, 8, 2, dim, 16, dtype, seed=longest, pad=8)
     out, lse, scale = _run(c, window=window, flags=0 if causal else lib8.KV8_FLAG_NOT_CAUSAL, pad_out=16)
     c.check_attention(out, lse, scale, window, causal)
 
