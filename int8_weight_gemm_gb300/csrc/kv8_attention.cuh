@@ -83,7 +83,7 @@ struct Runs {
   }
 };
 
-// The kernel of many query rows (kv8_attention_tc.cu): head_dim 64 and 128; its share of the workspace.
+// The kernel of many query rows (kv8_attention_tc.cu); its share of the workspace.
 cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
 size_t many_parts_bytes(int head_dim, int sms);
 
