@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             }
             const float want = mx[e] + lvs;
             float rn = want > r[i][e] + kSlack ? want : r[i][e];
-            rn = fminf(fmaxf(rn, m[i][e] - kSpan), m[i][e] + kSpan);
+            rn = fminf(fmaxf(rn, m[i][e] - kBelow), m[i][e] + kAbove);
             const float a = ex2(r[i][e] - rn);
             r[i][e] = rn;
             hs[i][e] = ex2(m[i][e] - rn);

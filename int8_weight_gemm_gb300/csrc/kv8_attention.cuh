@@ -15,7 +15,9 @@ namespace attn {
 constexpr int kGranule = 16;         // tokens of a warp's step
 constexpr float kFloor = -3.0e38f;   // reference of a row that has seen nothing
 constexpr float kSlack = 8.f;        // a reference moves when it is passed by this much (powers of two)
-constexpr float kSpan = 120.f;       // largest distance of the two references
+// How far r may lie from m: 2^(m - r) and its inverse stay normal numbers.  A weight passes 2^8 only where the upper
+// limit holds r, by a score of 2^8 above m's and a value scale of nearly 2^128: at most 2^(8 + 128 - 125), inside fp16.
+constexpr float kBelow = 120.f, kAbove = 125.f;
 // A weight is p * (v_scale * 2^(m - r)).  Where that factor is above this, p may have left fp32's range
 // while the weight has not, and the weight is taken from its own exponent.
 constexpr float kFar = 1.2676506e30f;   // 2^100

@@ -809,11 +809,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                     m = mx;
                   }
                   float rn = mw > r + kSlack ? mw : r;
-                  rn = fminf(fmaxf(rn, m - kSpan), m + kSpan);
+                  rn = fminf(fmaxf(rn, m - kBelow), m + kAbove);
                   const float down = ex2(r - rn);
                   r = rn;
                   hs = ex2(m - rn);
-                  far = __any_sync(0xffffffffu, hs * fmaxf(vs[0], vs[1]) > kFar);
+                  // What is worked out with the moved references stands, whether or not a limit keeps r below the
+                  // largest weight: with no maxima left to compare, and `far` the third condition itself, the second
+                  // turn is the last.
+                  far = __any_sync(0xffffffffu, fmaxf(hs * vs[0], hs * vs[1]) > kFar);
+                  mx = mw = -INFINITY;
                   if (i > 0 && !wait_sums(cnt - 1)) ok = false;
                   if (__any_sync(0xffffffffu, down != 1.f) && (i > 0 || ch > 0)) rescale(t_o, i > 0 ? D : 0, t_s, ch, down);
                 }

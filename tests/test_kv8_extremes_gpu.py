@@ -1,0 +1,88 @@
+"""kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size.
+The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
+import copy
+
+import numpy as np
+import pytest
+import torch
+
+import int8_weight_gemm_gb300 as lib8
+from kv8_util import DT, Case
+
+pytestmark = pytest.mark.gpu
+LOG2E = 1.4426950408889634
+
+
+def _last(c, n):
+    """The last n rows of a case of one sequence, over the same cache."""
+    d = copy.copy(c)
+    d.ns, d.row0, d.M, d.max_n, d.qkv = [n], np.array([0, n], np.int32), n, n, c.qkv[c.M - n:]
+    return d
+
+
+def _take_cache(c):
+    """The case's host copy of the cache = what the device holds of the pages in use."""
+    used = c.table[c.table >= 0]
+    for host, scales, dev, sdev in ((c.kq, c.ks, c.kc, c.ksd), (c.vq, c.vs, c.vc, c.vsd)):
+        host[used] = dev.cpu().numpy().astype(np.int32)[used] - 128
+        scales[used] = sdev.cpu().numpy()[used]
+
+
+def _check(c, window=0, flags=0):
+    c.tensors()
+    lse = torch.full((c.M, c.Hq), float("nan"), device="cuda")
+    out = lib8.kv8_attention(c.cache, c.step, c.q, c.ws, lse=lse, window=window, flags=flags)
+    assert c.status() == 0
+    c.check_attention(out, lse, c.D ** -0.5, window, not flags & lib8.KV8_FLAG_NOT_CAUSAL)
+    return out, lse
+
+
+def _ladder(c, length):
+    """Queries a e_0 and keys y e_0: a page's logits are 0 (two pages out of three, the first two among them) or, in
+    powers of two, one of 0 ... 16 that differs from row to row."""
+    rows = np.arange(c.M * c.Hq) % 131 * (16 / 131) / LOG2E * c.D ** 0.5
+    x = torch.zeros((c.M, c.Hq + 2 * c.Hkv, c.D))
+    x[:, :c.Hq, 0] = torch.from_numpy(rows.reshape(c.M, c.Hq).astype(np.float32))
+    high = (np.arange(length) // c.P) % 3 == 2
+    return x, high
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 200])
+def test_appended_infinities(dim, rows):
+    # An infinity is held at the largest scale that an append makes (2^121).  Rows whose score on such a page passes
+    # their reference by less than what moves it, beside rows that it moves, in both kernels.
+    L = 200
+    c = Case([L], [L], 8, 1, dim, 16, "bf16", seed=dim)
+    x, high = _ladder(c, L)
+    x[:, 8, 0] = torch.from_numpy(high.astype(np.float32))
+    x[:, 9] = torch.from_numpy(c.rng.standard_normal((L, dim)).astype(np.float32))
+    at = np.flatnonzero(high)[3::16]                 # one token of a page
+    x[at[0::2], 9, 5] = float("inf")
+    x[at[1::2], 9, 7] = float("-inf")
+    c.qkv = x.flatten(1).to(DT["bf16"])
+    c.tensors()
+    lib8.kv8_append(c.cache, c.step, None, c.k, c.v, c.ws)
+    _take_cache(c)
+    assert (c.vs[c.table[c.table >= 0]] > 2.0 ** 121).any()
+    _check(_last(c, rows))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 3, 200])
+def test_the_largest_value_scales(dim, rows):
+    # Scales next to fp32's largest number, which a cache filled by another program may have.
+    L = 200
+    c = Case([L], [L], 8, 1, dim, 16, "bf16", seed=dim)
+    x, high = _ladder(c, L)
+    c.qkv = x.flatten(1).to(DT["bf16"])
+    pages = c.table[0, :-(-L // 16)]
+    c.kq[pages] = 0
+    c.kq[pages[2::3], :, :, 0] = 127
+    c.ks[pages] = np.float32(1 / 127)
+    c.vq[pages] = np.sign(c.vq[pages])
+    c.vs[pages[0::3]] = 1e-30
+    c.vs[pages[1::3]] = 1.0
+    c.vs[pages[2::3]] = 3.4028234e38
+    c.vq[pages[2::3], :, :8] = 0                     # (a page's tokens weigh the same: no weight of a large value is near 1)
+    _check(_last(c, rows))
