@@ -852,7 +852,9 @@ extern "C" int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, c
   p.pages = cache->pages, p.q_heads = q_heads, p.kv_heads = cache->kv_heads;
   p.page_shift = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
   p.group = q_heads / cache->kv_heads;
-  p.window = window, p.causal = (flags & KV8_FLAG_NOT_CAUSAL) ? 0 : 1;
+  // No cache has more than 2^30 tokens: a longer window is none, and the kernels' first token stays inside 32 bits with
+  // any number of rows.
+  p.window = window < (1 << 30) ? window : 1 << 30, p.causal = (flags & KV8_FLAG_NOT_CAUSAL) ? 0 : 1;
   p.scale_log2 = scale * 1.4426950408889634f;
   uint8_t* const w = static_cast<uint8_t*>(ws);
   p.status = reinterpret_cast<uint32_t*>(w);

@@ -1,5 +1,5 @@
-"""kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size.
-The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
+"""kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size, the
+longest windows.  The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
 import copy
 
 import numpy as np
@@ -86,3 +86,14 @@ def test_the_largest_value_scales(dim, rows):
     c.vs[pages[2::3]] = 3.4028234e38
     c.vq[pages[2::3], :, :8] = 0                     # (a page's tokens weigh the same: no weight of a large value is near 1)
     _check(_last(c, rows))
+
+
+@pytest.mark.parametrize("window", [2**30 - 1, 2**30, 2**31 - 2, 2**31 - 1])
+@pytest.mark.parametrize("ns,lens", [([5, 1, 4], [2, 3, 0]), ([70, 3], [5, 90]), ([300], [40])])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_windows_longer_than_any_cache(ns, lens, window, dim):
+    # With more rows than tokens the first row's position is below zero.
+    c = Case(ns, lens, 4, 1, dim, 16, "bf16", seed=dim + len(ns))
+    out, lse = _check(c, window=window)
+    whole = lib8.kv8_attention(c.cache, c.step, c.q, c.ws)
+    assert torch.equal(out, whole)
