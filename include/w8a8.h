@@ -463,7 +463,9 @@ int kv8_append(const kv8_cache_t* cache, const kv8_step_t* step, const qk_prep_t
  * head h / (q_heads / kv_heads).  Row i of a sequence stands at slot p = kv_len - n + i and sees slots
  * max(0, p - window + 1) ... p (window 0: all up to p), or all kv_len with KV8_FLAG_NOT_CAUSAL:
  *   out = sum_j softmax_j(scale * q . k_j) v_j       lse = log sum_j exp(scale * q . k_j)
- * in one pass with fp32 sums and statistics, rounded once.  A row that sees nothing (kv_len 0, or
+ * in one pass with fp32 sums and statistics, rounded once; each token's weight (its probability times
+ * its values' scale) enters the products as fp16, 11 bits of it down to 2^-21 of the row's largest
+ * weight, nothing below 2^-32.  A row that sees nothing (kv_len 0, or
  * n > kv_len) gets out = 0 and lse = -inf.
  *  out  [tokens][q_heads][head_dim] of dtype;  lse  fp32 [tokens][q_heads] contiguous, or NULL
  *  scale  finite and > 0

@@ -24,9 +24,10 @@
 //    o = sum w (b - 128), the bytes converted exactly (the offset is not left to a subtraction at the
 //    end: 128 sum w would be a thousand times the sum of a long cache's values).  r follows the largest
 //    w as m follows the largest s, so neither a page of tiny values under the largest score nor the
-//    reverse loses bits.  Both references move only when a score or weight passes them by 2^8: w stays
-//    inside fp16's range, the sums are rescaled a few times per pass instead of at every granule, and
-//    in between no lane needs another lane's maximum.
+//    reverse loses bits; it lies 2^7 below that w (kHead), so that a long tail of small weights is not
+//    lost either.  Both references move only when a score or weight passes where they were put by 2^8:
+//    w stays inside fp16's range, the sums are rescaled a few times per pass instead of at every
+//    granule, and in between no lane needs another lane's maximum.
 //  * Parts (warps of a CTA, CTAs of a split sequence) join as o 2^(r_i - r), l 2^(m_i - m), in a fixed
 //    order whatever the order of arrival, so replays give the same bits.
 //
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
           }
           mx[e] = fmaxf(z[e], z[2 + e]);
           f[e] = hs[i][e] * vs;
-          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kSlack || f[e] > kFar;
+          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kRoom || f[e] > kFar;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
               m[i][e] = mx[e];
             }
             const float want = mx[e] + lvs;
-            float rn = want > r[i][e] + kSlack ? want : r[i][e];
+            float rn = want > r[i][e] + kRoom ? want - kHead : r[i][e];
             rn = fminf(fmaxf(rn, m[i][e] - kBelow), m[i][e] + kAbove);
             const float a = ex2(r[i][e] - rn);
             r[i][e] = rn;

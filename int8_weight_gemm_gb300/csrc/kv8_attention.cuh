@@ -15,8 +15,14 @@ namespace attn {
 constexpr int kGranule = 16;         // tokens of a warp's step
 constexpr float kFloor = -3.0e38f;   // reference of a row that has seen nothing
 constexpr float kSlack = 8.f;        // a reference moves when it is passed by this much (powers of two)
-// How far r may lie from m: 2^(m - r) and its inverse stay normal numbers.  A weight passes 2^8 only where the upper
-// limit holds r, by a score of 2^8 above m's and a value scale of nearly 2^128: at most 2^(8 + 128 - 125), inside fp16.
+// Where the weights' reference r moves, the largest weight becomes 2^kHead: fp16 has that room above a weight of 1, and
+// below it loses bits from 2^-14 and everything from 2^-25 on, which the sums of the probabilities, held in fp32, count in
+// full.  So a weight keeps its 11 bits down to 2^-21 of the row's largest and is zero below 2^-32 of it.  (A strong token
+// without values over tokens of 2^-21.5 of it: outputs off by 0.01 % instead of 6 %, with r at the largest weight.)
+constexpr float kHead = 7.f;
+constexpr float kRoom = kHead + kSlack;   // no weight passes 2^15
+// How far r may lie from m: 2^(m - r) and its inverse stay normal numbers.  Where the upper limit holds r, by a score of
+// 2^8 above m's and a value scale of nearly 2^128, a weight is at most 2^(8 + 128 - 125).
 constexpr float kBelow = 120.f, kAbove = 125.f;
 // A weight is p * (v_scale * 2^(m - r)).  Where that factor is above this, p may have left fp32's range
 // while the weight has not, and the weight is taken from its own exponent.

@@ -12,7 +12,7 @@
 //  Weights: p = 2^(s - m) sums to l in fp32, w = p * (v_scale * 2^(m - r)), rounded to fp16, goes back into
 //  tensor memory over the scores it came from and is the first operand of O += W V.  The references m and r
 //  of a row are those of the other kernel, for the same reasons: they move when a score or weight passes
-//  them by 2^8, and only then is O (and the weights already written of that block) rescaled, once the
+//  where they were put by 2^8, and only then is O (and the weights already written of that block) rescaled, once the
 //  products that add to O have completed.
 //
 // Layout and split.  One CTA an SM, all of its tensor memory: two streams of scores and outputs, each with
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                   }
                   break;
                 }
-                moved = __any_sync(0xffffffffu, mx > m + kSlack || mw > r + kSlack || fmaxf(f[0], f[1]) > kFar);
+                moved = __any_sync(0xffffffffu, mx > m + kSlack || mw > r + kRoom || fmaxf(f[0], f[1]) > kFar);
                 if (moved) {
                   // Some row's reference moves: its sums so far are rescaled, and with them the weights of
                   // this block that are already written.
@@ -808,7 +808,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
                     l *= ex2(m - mx);
                     m = mx;
                   }
-                  float rn = mw > r + kSlack ? mw : r;
+                  float rn = mw > r + kRoom ? mw - kHead : r;
                   rn = fminf(fmaxf(rn, m - kBelow), m + kAbove);
                   const float down = ex2(r - rn);
                   r = rn;

@@ -1,5 +1,5 @@
 """kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size, the
-longest windows.  The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
+longest windows, the smallest weights.  The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
 import copy
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import int8_weight_gemm_gb300 as lib8
-from kv8_util import DT, Case
+from kv8_util import DT, UNIT, Case, f64
 
 pytestmark = pytest.mark.gpu
 LOG2E = 1.4426950408889634
@@ -97,3 +97,31 @@ def test_windows_longer_than_any_cache(ns, lens, window, dim):
     out, lse = _check(c, window=window)
     whole = lib8.kv8_attention(c.cache, c.step, c.q, c.ws)
     assert torch.equal(out, whole)
+
+
+@pytest.mark.parametrize("far", [17.5, 21.5, 24.5])
+@pytest.mark.parametrize("rows", [1, 3, 200])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_strong_tokens_without_values_over_a_flat_rest(dim, rows, far):
+    # Every sixteenth token holds nearly all of the probability and no value; the output is made of the others, which
+    # weigh 2^-far of it.  As Case.attention's bound, but that a weight is off by at most 2^-32 of the largest (fp16's
+    # half spacing, 2^-25, where the largest is at least 2^7), not by 2^-25.
+    L = 300
+    c = Case([rows], [L], 8, 1, dim, 16, "f16", seed=dim)
+    x = torch.zeros((rows, 10, dim))
+    x[:, :8, 0] = far / LOG2E * dim ** 0.5
+    c.qkv = x.flatten(1).to(DT["f16"])
+    pages = c.table[0, :-(-L // 16)]
+    c.kq[pages] = 0
+    c.kq[pages, :, 0, 0] = 127
+    c.ks[pages] = np.float32(1 / 127)
+    c.vq[pages] = np.abs(c.vq[pages]) // 2 + 60
+    c.vq[pages, :, 0] = 0
+    c.vs[pages] = 1.0
+    out, _ = _check(c)
+    ref, _, e, _ = c.attention(dim ** -0.5)
+    seen = np.arange(L - rows, L) + 1                # of a row
+    w0 = 1 / (-(-seen // 16) + (seen - -(-seen // 16)) * 2.0 ** -far)
+    slack = (seen * 127 * w0)[:, None, None]         # tokens times the largest weighted scale
+    e = e - slack * 2.0 ** -25 * (1 - 2.0 ** -6) + slack * 2.0 ** -32
+    assert (np.abs(f64(out) - ref) <= e + UNIT["f16"] * (np.abs(ref) + e)).all()
