@@ -378,6 +378,7 @@ enum {
  *  k, v               uint8 [pages][kv_heads][page_tokens][head_dim], 16-byte aligned
  *  k_scale, v_scale   fp32 [pages][kv_heads]
  *  page_tokens 16, 32, 64 or 128; kv_heads <= 1024; pages * kv_heads * page_tokens < 2^31.
+ * Scales are finite, of either sign (an append makes none below zero).
  * Bytes and scales of slots that no append has filled are never used, whatever they hold. */
 typedef struct {
     void* k;

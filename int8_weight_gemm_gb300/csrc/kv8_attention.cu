@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
         break;
       }
       const bool edge = T < full_lo || T + kGranule > full_hi || bad;
-      const float lvs = lg2(vs);
+      const float lvs = lg2(fabsf(vs));   // (a weight has the sign of its page's scale)
       uint32_t pb[NT][2];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
           }
           mx[e] = fmaxf(z[e], z[2 + e]);
           f[e] = hs[i][e] * vs;
-          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kRoom || f[e] > kFar;
+          move = move || mx[e] > m[i][e] + kSlack || mx[e] + lvs > r[i][e] + kRoom || fabsf(f[e]) > kFar;
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
               o[i][n][2 + e] *= a;
             }
           }
-          far = __any_sync(0xffffffffu, f[0] > kFar || f[1] > kFar);
+          far = __any_sync(0xffffffffu, fabsf(f[0]) > kFar || fabsf(f[1]) > kFar);
         }
         float w[4];
 #pragma unroll
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             const float pr = ex2(z[2 * t + e] - m[i][e]);
             l[i][e] += pr;
             w[2 * t + e] = pr * f[e];
-            if (far && f[e] > kFar) w[2 * t + e] = ex2(z[2 * t + e] + lvs - r[i][e]);
+            if (far && fabsf(f[e]) > kFar) w[2 * t + e] = copysignf(ex2(z[2 * t + e] + lvs - r[i][e]), vs);
           }
         }
 #pragma unroll

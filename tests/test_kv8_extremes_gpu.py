@@ -1,5 +1,6 @@
 """kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size, the
-longest windows, the smallest weights.  The bounds are those of kv8_util.Case.attention unless a test says otherwise."""
+longest windows, the smallest weights, negative scales.  The bounds are those of kv8_util.Case.attention unless a test
+says otherwise."""
 import copy
 
 import numpy as np
@@ -125,3 +126,32 @@ def test_strong_tokens_without_values_over_a_flat_rest(dim, rows, far):
     slack = (seen * 127 * w0)[:, None, None]         # tokens times the largest weighted scale
     e = e - slack * 2.0 ** -25 * (1 - 2.0 ** -6) + slack * 2.0 ** -32
     assert (np.abs(f64(out) - ref) <= e + UNIT["f16"] * (np.abs(ref) + e)).all()
+
+
+def _turn_signs(c):
+    """Negative scales for two pages out of three: of the keys, of the values, of both in turn."""
+    used = c.table[c.table >= 0]
+    c.ks[used[0::3]] *= -1
+    c.vs[used[0::3]] *= -1
+    c.vs[used[1::3]] *= -1
+    c.ks[used[2::5]] *= -1
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("ns,lens,window,flags", [([1, 1, 3], [150, 17, 333], 0, 0), ([20], [222], 0, 0), ([300], [333], 0, 0),
+                                                  ([2, 40], [200, 100], 70, 0), ([5, 260], [90, 300], 0, lib8.KV8_FLAG_NOT_CAUSAL)])
+def test_negative_scales(ns, lens, window, flags, dim):
+    c = Case(ns, lens, 8, 2, dim, 16, "bf16", seed=dim + len(ns))
+    _turn_signs(c)
+    _check(c, window, flags)
+
+
+@pytest.mark.parametrize("rows", [2, 100])
+def test_negative_scales_far_from_the_largest_score(rows):
+    # The largest scores stand on pages of no value size, so that weights come from their own exponents.
+    c = Case([rows], [222], 8, 2, 128, 16, "bf16", seed=18)
+    used = c.table[c.table >= 0]
+    c.ks[used[::3]] *= 25.0
+    c.vs[used[::3]] = 0.0
+    c.vs[used[1::3]] *= -1e12
+    _check(c)
