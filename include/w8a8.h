@@ -446,13 +446,13 @@ int qk_norm_rope(const qk_prep_t* prep, const void* q, long long q_stride, int q
  * cache, and put its queries (q_heads of them; 0: none) through `prep` into q_out, in one launch.
  *  positions  [tokens] int32 rotation positions, or NULL: each row's cache slot
  * A page's scale is the largest magnitude given to it over 127: with r of its slots filled before
- * the step, s = max(s_old, amax / 127) for r > 0, and amax / 127 for r = 0 (the page starts anew),
+ * the step, s = max(|s_old|, amax / 127) for r > 0, and amax / 127 for r = 0 (the page starts anew),
  * amax over the step's values of the page and head.  A value x is held as
  * 128 + clamp(round(x / s), -127, 127), halves away from zero (128 for s = 0), from fp32: nothing is
- * rounded to 16 bits on the way.  Where s grows, the r earlier tokens are held again as
- * 128 + round((byte - 128) * s_old / s).  So tokens taken back (a smaller kv_len, as after a verify
- * window) are simply written over, at a scale that is large enough.  A NaN is held as 0, an infinity
- * as the largest finite value.
+ * rounded to 16 bits on the way.  Where s changes, the r earlier tokens are held again as
+ * 128 + round((byte - 128) * s_old / s), at most 255.  So tokens taken back (a smaller kv_len, as
+ * after a verify window) are simply written over, at a scale that is large enough.  A NaN is held as
+ * 0, an infinity as the largest finite value.
  * Every sequence needs n <= kv_len.  No page may belong to two sequences that append to it.
  * Errors as above. */
 int kv8_append(const kv8_cache_t* cache, const kv8_step_t* step, const qk_prep_t* prep, const void* k,

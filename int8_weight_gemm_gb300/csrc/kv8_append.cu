@@ -7,8 +7,8 @@
 //    sum rounded to fp32, for the first rot values of a head; pairs (i, i + rot / 2) or (2 i, 2 i + 1).
 //  * Cache: one fp32 scale s for each (page, kv head), a byte standing for (byte - 128) * s.  A
 //    page's scale is the largest magnitude it has been given over 127: with r tokens already in the
-//    page, s = max(s_old, amax / 127) for r > 0 and amax / 127 for r = 0; x is held as
-//    128 + clamp(round(x / s)).  When s grows, the r earlier tokens are held again at the new scale:
+//    page, s = max(|s_old|, amax / 127) for r > 0 and amax / 127 for r = 0; x is held as
+//    128 + clamp(round(x / s)).  When s changes, the r earlier tokens are held again at the new scale:
 //    128 + round((byte - 128) * s_old / s).  Values are quantised from fp32: nothing is rounded to 16
 //    bits on the way.  round = halves away from zero, division IEEE; s = 0 gives bytes 128; a NaN is
 //    held as 0 and an infinity as the largest finite value, so no byte or scale of the cache is ever
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
   __syncthreads();
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) amax = fmaxf(amax, red[w]);
   const float fresh = __fdiv_rn(fminf(amax, kMaxFinite), 127.0f);
-  const float now = fmaxf(old, fresh);
-  const bool again = lo > 0 && now > old;   // the earlier tokens are held at a new scale
+  const float now = fmaxf(fabsf(old), fresh);
+  const bool again = lo > 0 && now != old;   // the earlier tokens are held at a new scale (of the other sign: byte 0 as 255)
   if (threadIdx.x == 0) *scale = now;
   const float inv = __fdiv_rn(1.0f, now);
 #pragma unroll
@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
       const uint32_t u[2] = {was.x, was.y};
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn((float)((int)((u[j >> 2] >> (8 * (j & 3))) & 0xFFu) - 128), old);
+      for (int j = 0; j < 8; ++j)
+        v[j] = fminf(__fmul_rn((float)((int)((u[j >> 2] >> (8 * (j & 3))) & 0xFFu) - 128), old), __fmul_rn(127.f, now));
       store_bytes<kLanes, kPaired>(dst, l, hold8(v, now, inv));
     }
   }

@@ -155,3 +155,34 @@ def test_negative_scales_far_from_the_largest_score(rows):
     c.vs[used[::3]] = 0.0
     c.vs[used[1::3]] *= -1e12
     _check(c)
+
+
+@pytest.mark.parametrize("amp", [0.05, 1.0, 8.0])
+@pytest.mark.parametrize("ns,lens", [([1, 8, 0, 5], [40, 8, 25, 130]), ([33, 3], [66, 30])])
+def test_append_onto_pages_of_negative_scale(ns, lens, amp):
+    # The page's tokens keep their values: its scale is the larger of its magnitude and the new tokens', and positive.
+    c = Case(ns, lens, 4, 2, 64, 32, "bf16", seed=6, amp=amp)
+    used = c.table[c.table >= 0]
+    c.ks[used] *= -1
+    c.vs[used[::2]] *= -1
+    c.kq[used, :, 0, :4], c.vq[used, :, 0, 4:8] = -128, -128        # (byte 0, which no append writes)
+    c.tensors()
+    lib8.kv8_append(c.cache, c.step, None, c.k, c.v, c.ws)
+    assert c.status() == 0
+    for x, q, s, qd, sd in ((c.k, c.kq, c.ks, c.kc, c.ksd), (c.v, c.vq, c.vs, c.vc, c.vsd)):
+        now_q, now_s = qd.cpu().numpy().astype(np.float64) - 128, sd.cpu().numpy().astype(np.float64)
+        x = f64(x)
+        for b, (n, L) in enumerate(zip(ns, lens)):
+            for t in range(L - n - (L - n) % c.P if n else L, L, c.P):
+                page, lo, hi = int(c.table[b, t // c.P]), max(L - n - t, 0), min(L - t, c.P)
+                new = x[c.row0[b] + t + lo - (L - n):c.row0[b] + t + hi - (L - n)]
+                fresh = np.abs(new).max((0, 2)) / 127
+                want = np.maximum(fresh, np.abs(s[page]) if lo else 0)
+                assert np.abs(now_s[page] - want).max() <= 2.0 ** -22 * want.max()
+                step = now_s[page][:, None, None]
+                got = now_q[page] * step
+                # half a step and the fp32 roundings of 127 steps; -128 steps are held as -127 or 127
+                e = step * (0.5 + 2.0 ** -15)
+                assert (np.abs(got[:, lo:hi] - new.transpose(1, 0, 2)) <= e).all()
+                was = q[page] * s[page].astype(np.float64)[:, None, None]
+                assert (np.abs(got[:, :lo] - was[:, :lo]) <= e + step * 0.5 * (np.abs(q[page][:, :lo]) == 128)).all()
