@@ -363,7 +363,9 @@ int q8_0_blocks_from_split(const int8_t* q, const void* d, void* blocks, int K, 
  * kv8_workspace_bytes; it is not to be shared with the GEMM and Q8_0 calls, since attention leaves
  * partial sums in it.  Indices in device memory cannot be checked on the host: the kernels check
  * them before every use, leave out what they would have addressed, and record W8A8_DEV_BAD_INDEX
- * (w8a8_workspace_status).
+ * (w8a8_workspace_status).  A row whose position is not in the rotation table is left out too: q_out
+ * and k_out keep what they held there; its key enters the cache as zeros (its slot will be read) and
+ * does not count in the page's scale; its value is appended.
  * ------------------------------------------------------------------------------------------- */
 
 enum { KV8_BF16 = 0, KV8_F16 = 1 };   /* dtype of the 16-bit tensors of a call */

@@ -61,18 +61,17 @@ static int batches_of(int heads, int rows) {
   return (long long)chunks * rows > 16384 && chunks > 1 ? 2 : 1;
 }
 
-// The position's row of the table; a position outside it is recorded and taken as 0.
-__device__ __forceinline__ const float* turn_row(const float* cos_sin, int pos, int rot, int max_pos, uint32_t* status) {
-  if (pos < 0 || pos >= max_pos) {
-    atomicOr(status, W8A8_DEV_BAD_INDEX);
-    pos = 0;
-  }
-  return cos_sin + (size_t)pos * rot;
+// Whether the table has a row for the position; one that it does not have is recorded.
+__device__ __forceinline__ bool in_table(const QkParams& p, int pos) {
+  if (pos >= 0 && pos < p.max_pos) return true;
+  atomicOr(p.status, W8A8_DEV_BAD_INDEX);
+  return false;
 }
 
-// Heads h0 ... of one row (of q_heads queries, then kv_heads keys) through norm and rotation.
+// Heads h0 ... of one row (of q_heads queries, then kv_heads keys) through norm and rotation; `keep`: the row is written.
+// (Its loads do not wait for what decides that, the position.)
 template <bool kF16, int kLanes, bool kPaired>
-__device__ __forceinline__ void turn_heads(const QkParams& p, int row, bool live, int h0, int l, const Turn<kPaired>& t) {
+__device__ __forceinline__ void turn_heads(const QkParams& p, int row, bool live, bool keep, int h0, int l, const Turn<kPaired>& t) {
   constexpr int D = 8 * kLanes;
   const int heads = p.q_heads + p.kv_heads;
   for (int b = 0; b < p.batches; ++b, h0 += kQkHeads) {
@@ -96,7 +95,7 @@ __device__ __forceinline__ void turn_heads(const QkParams& p, int row, bool live
       float g[8];
       if (gamma) unpack8<kF16>(load_head<kLanes, kPaired>(gamma, l), g);
       norm_turn<kPaired>(x[i], gamma != nullptr, rs[i], g, t, l, p.rot, p.interleaved != 0);
-      if (live && h < heads)
+      if (keep && h < heads)
         store_head<kLanes, kPaired>(is_q ? p.q_out + row * p.q_out_stride + h * D : p.k_out + row * p.k_out_stride + (h - p.q_heads) * D,
                                     l, pack8<kF16>(x[i]));
     }
@@ -111,11 +110,15 @@ __global__ void __launch_bounds__(kQkThreads) qk_norm_rope_kernel(const __grid_c
   const int l = threadIdx.x % kLanes;
   const int row = blockIdx.x * kGroups + threadIdx.x / kLanes;
   const bool live = row < p.tokens;
+  bool keep = live;
   Turn<kPaired> t;
-  if (p.rot > 0)
-    load_turn<kPaired>(turn_row(p.cos_sin, live ? __ldg(p.positions + row) : 0, p.rot, p.max_pos, p.status), l, p.rot,
-                       p.interleaved != 0, t);
-  turn_heads<kF16, kLanes, kPaired>(p, row, live, blockIdx.y * kQkHeads * p.batches, l, t);
+  if (p.rot > 0) {
+    const int pos = live ? __ldg(p.positions + row) : 0;
+    const bool in = in_table(p, pos);
+    keep = live && in;
+    load_turn<kPaired>(p.cos_sin + (size_t)(in ? pos : 0) * p.rot, l, p.rot, p.interleaved != 0, t);
+  }
+  turn_heads<kF16, kLanes, kPaired>(p, row, live, keep, blockIdx.y * kQkHeads * p.batches, l, t);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -188,6 +191,7 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
     const int qb = blockIdx.x - p.page_blocks;
     const int row = (qb / p.q_chunks) * groups + g;
     const bool live = row < p.step.tokens;
+    bool keep = live;
     Turn<kPaired> t;
     if (c.rot > 0) {
       int pos = 0;
@@ -205,11 +209,13 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
           pos = __ldg(p.step.kv_len + lo) - (__ldg(p.step.row0 + lo + 1) - row);
         }
       }
-      load_turn<kPaired>(turn_row(c.cos_sin, pos, c.rot, c.max_pos, c.status), l, c.rot, c.interleaved != 0, t);
+      const bool in = in_table(c, pos);
+      keep = live && in;
+      load_turn<kPaired>(c.cos_sin + (size_t)(in ? pos : 0) * c.rot, l, c.rot, c.interleaved != 0, t);
     }
     QkParams q = c;
     q.kv_heads = 0;   // the keys go into the cache
-    turn_heads<kF16, kLanes, kPaired>(q, row, live, (qb % p.q_chunks) * kQkHeads * c.batches, l, t);
+    turn_heads<kF16, kLanes, kPaired>(q, row, live, keep, (qb % p.q_chunks) * kQkHeads * c.batches, l, t);
     return;
   }
 
@@ -259,11 +265,18 @@ __global__ void __launch_bounds__(32 * kLanes, kLanes == 32 ? 1 : 2) kv8_append_
     const int t = g + i * groups;
     const bool mine = t >= lo && t < hi;
     Turn<kPaired> turn;
+    bool in = true;
     if (rot > 0) {
       const int pos = !mine ? 0 : c.positions ? __ldg(c.positions + s.row0 + pg * P + t - first_slot) : pg * P + t;
-      load_turn<kPaired>(turn_row(c.cos_sin, pos, rot, c.max_pos, c.status), l, rot, c.interleaved != 0, turn);
+      in = in_table(c, pos);
+      load_turn<kPaired>(c.cos_sin + (size_t)(in ? pos : 0) * rot, l, rot, c.interleaved != 0, turn);
     }
     norm_turn<kPaired>(x[i], norm, rs[i], gk, turn, l, rot, c.interleaved != 0);
+    if (__builtin_expect(!in, 0)) {   // a key without a rotation is held as zeros: its slot will be read
+      asm volatile("" ::: "memory");  // (a branch, not a selection of every value)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[i][j]));
   }

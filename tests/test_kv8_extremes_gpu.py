@@ -1,6 +1,6 @@
 """kv8_append and kv8_attention at the ends of their ranges, against plain 64-bit forms: values of the largest size, the
-longest windows, the smallest weights, negative scales.  The bounds are those of kv8_util.Case.attention unless a test
-says otherwise."""
+longest windows, the smallest weights, negative scales, positions out of the table.  The bounds are those of
+kv8_util.Case.attention unless a test says otherwise."""
 import copy
 
 import numpy as np
@@ -9,6 +9,7 @@ import torch
 
 import int8_weight_gemm_gb300 as lib8
 from kv8_util import DT, UNIT, Case, f64
+from test_kv8_append_gpu import REL, _check16, _check_append, _prep, _turned
 
 pytestmark = pytest.mark.gpu
 LOG2E = 1.4426950408889634
@@ -186,3 +187,46 @@ def test_append_onto_pages_of_negative_scale(ns, lens, amp):
                 assert (np.abs(got[:, lo:hi] - new.transpose(1, 0, 2)) <= e).all()
                 was = q[page] * s[page].astype(np.float64)[:, None, None]
                 assert (np.abs(got[:, :lo] - was[:, :lo]) <= e + step * 0.5 * (np.abs(q[page][:, :lo]) == 128)).all()
+
+
+@pytest.mark.parametrize("dim,rot,interleaved", [(64, 64, False), (128, 128, False), (128, 64, True), (256, 256, False), (256, 96, False)])
+@pytest.mark.parametrize("bad", [-1, 60, 2**31 - 1])
+def test_rows_of_positions_out_of_the_table_are_left_out(dim, rot, interleaved, bad):
+    # Rows 1, 4 and 8 stand at positions that the table does not have: their rows of the outputs are not written, their
+    # keys enter the cache as zeros and do not count in a page's scale; their values, which do not rotate, are appended.
+    n, L, P = 10, 40, 16
+    out = np.zeros(n, bool)
+    out[[1, 4, 8]] = True
+    pos = np.where(out, bad, np.arange(n) + 3).astype(np.int32)
+    good = np.where(out, 0, pos)
+    c = Case([n], [L], 4, 2, dim, P, "bf16", seed=dim).tensors()
+    prep = _prep(c, rot, interleaved, True, 60)
+    c.k[torch.from_numpy(out).cuda()] *= 1000.0
+    posd = torch.from_numpy(pos).cuda()
+    qo, ko = torch.full_like(c.q.contiguous(), 7.0), torch.full_like(c.k.contiguous(), 7.0)
+    lib8.qk_norm_rope(prep, c.q, c.k, posd, c.ws, q_out=qo, k_out=ko)
+    assert c.status() == lib8.W8A8_DEV_BAD_INDEX and c.status() == 0
+    for got, x, g in ((qo, c.q, c.gq), (ko, c.k, c.gk)):
+        assert (got[torch.from_numpy(out).cuda()] == 7.0).all()
+        _check16(c, got[torch.from_numpy(~out).cuda()], x[torch.from_numpy(~out).cuda()], g, good[~out])
+    qo.fill_(7.0)
+    lib8.kv8_append(c.cache, c.step, prep, c.k, c.v, c.ws, q=c.q, q_out=qo, positions=posd)
+    assert c.status() == lib8.W8A8_DEV_BAD_INDEX
+    assert (qo[torch.from_numpy(out).cuda()] == 7.0).all()
+    _check16(c, qo[torch.from_numpy(~out).cuda()], c.q[torch.from_numpy(~out).cuda()], c.gq, good[~out])
+    y, mag = _turned(c, c.k, c.gk, good)
+    after_q, after_s = c.kc.cpu().numpy().astype(np.int32) - 128, c.ksd.cpu().numpy()
+    for t in range((L - n) // P * P, L, P):
+        page, lo, hi = int(c.table[0, t // P]), max(L - n - t, 0), min(L - t, P)
+        rows = np.arange(t + lo - (L - n), t + hi - (L - n))
+        for h in range(2):
+            keep = rows[~out[rows]]
+            old = float(c.ks[page, h]) if lo else 0.0
+            s = max(old, np.abs(y[keep, h]).max() / 127)
+            got_s = float(after_s[page, h])
+            assert abs(got_s - s) <= 2 * REL * (mag[keep, h].max() / 127 + s)
+            slack = REL * mag[keep, h] / got_s + 127 * 2.0 ** -20
+            assert (np.abs(after_q[page, h, lo:hi][~out[rows]] - (y[keep, h] / got_s).clip(-127, 127)) <= 0.5 + slack).all()
+            assert (after_q[page, h, lo:hi][out[rows]] == 0).all()
+    v = f64(c.v)
+    _check_append(c, v, np.abs(v), c.vq, c.vs, c.vc.cpu().numpy().astype(np.int32) - 128, c.vsd.cpu().numpy(), True)
