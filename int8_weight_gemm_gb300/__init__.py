@@ -596,8 +596,8 @@ def _ws(ws):
     return ws.data_ptr(), ws.nbytes
 
 
-@functools.lru_cache(maxsize=1024)
 def kv8_workspace_bytes(q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of the workspace of these calls on the current device (its SMs decide)."""
     return int(lib().kv8_workspace_bytes(q_heads, kv_heads, head_dim))
 
 
