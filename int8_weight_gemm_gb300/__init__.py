@@ -473,21 +473,31 @@ def q8_0_blocks_from_split(q, d, blocks=None, stream=None):
 # what does not change between calls (the cache, a step's index buffers, the norm weights and rotation table) is
 # checked once, in a handle that holds its tensors.
 
+def _fp32(t, name, nbytes=0):
+    _dev(t, name, nbytes, esize=4)
+    if not t.is_floating_point():
+        raise ValueError(f"{name}: expected float32, got {t.dtype}")
+
+
 class KV8Cache:
     """One layer's cache: k, v uint8 [pages, kv_heads, page_tokens, head_dim], k_scale, v_scale fp32 [pages, kv_heads]."""
 
     def __init__(self, k, v, k_scale, v_scale):
+        import torch
+
         if k.dim() != 4:
             raise ValueError(f"k: expected [pages, kv_heads, page_tokens, head_dim], got {tuple(k.shape)}")
         if v.shape != k.shape:
             raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
         pages, heads, page_tokens, dim = k.shape
-        _dev(k, "k", esize=1)
-        _dev(v, "v", esize=1)
+        for name, t in (("k", k), ("v", v)):
+            _dev(t, name, esize=1)
+            if t.dtype is not torch.uint8:
+                raise ValueError(f"{name}: expected uint8, got {t.dtype}")
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             if tuple(t.shape) != (pages, heads):
                 raise ValueError(f"{name}: expected shape {(pages, heads)}, got {tuple(t.shape)}")
-            _dev(t, name, esize=4)
+            _fp32(t, name)
         _on_cuda(k=k, v=v, k_scale=k_scale, v_scale=v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.kv_heads, self.page_tokens, self.head_dim = pages, heads, page_tokens, dim
@@ -534,7 +544,7 @@ class QKPrep:
         if rot_dim > 0:
             if cos_sin is None or cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim:
                 raise ValueError(f"cos_sin: expected [max_pos, {rot_dim}], got {None if cos_sin is None else tuple(cos_sin.shape)}")
-            _dev(cos_sin, "cos_sin", esize=4)
+            _fp32(cos_sin, "cos_sin")
             max_pos = cos_sin.shape[0]
         for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
             if g is not None:
@@ -663,7 +673,7 @@ def kv8_attention(cache, step, q, ws, out=None, lse=None, scale=None, window: in
     qs, os_ = _heads(q, "q", rows, q_heads, dim, dtype), _heads(out, "out", rows, q_heads, dim, dtype)
     lp = None
     if lse is not None:
-        _dev(lse, "lse", 4 * rows * q_heads, esize=4)
+        _fp32(lse, "lse", 4 * rows * q_heads)
         lp = lse.data_ptr()
     wp, wn = _ws(ws)
     if not (q.is_cuda and out.is_cuda and ws.is_cuda and (lse is None or lse.is_cuda)):
