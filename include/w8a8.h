@@ -469,7 +469,8 @@ int kv8_append(const kv8_cache_t* cache, const kv8_step_t* step, const qk_prep_t
  * in one pass with fp32 sums and statistics, rounded once; each token's weight (its probability times
  * its values' scale) enters the products as fp16, 11 bits of it down to 2^-21 of the row's largest
  * weight, nothing below 2^-32.  A row that sees nothing (kv_len 0, or
- * n > kv_len) gets out = 0 and lse = -inf.
+ * n > kv_len) gets out = 0 and lse = -inf.  Scores have to stay inside fp32: a row that
+ * sees a page with a key held from an infinity has no defined result; other rows keep theirs.
  *  out  [tokens][q_heads][head_dim] of dtype;  lse  fp32 [tokens][q_heads] contiguous, or NULL
  *  scale  finite and > 0
  * Replays give the same bits.  Errors as above. */

@@ -90,6 +90,28 @@ def test_the_largest_value_scales(dim, rows):
     _check(_last(c, rows))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [3, 193])
+def test_an_appended_infinite_key_stays_with_the_rows_that_see_it(dim, rows):
+    # The last token, alone on its page, has it: every row before it, and the other sequence, keep their results.
+    c = Case([193, 40], [193, 90], 8, 1, dim, 16, "bf16", seed=dim)
+    c.qkv[192, 8 * dim + 3] = float("inf")
+    c.tensors()
+    lib8.kv8_append(c.cache, c.step, None, c.k, c.v, c.ws)
+    assert c.status() == 0
+    _take_cache(c)
+    assert c.ks[c.table[0, 12], 0] > 2.0 ** 121
+    d = copy.copy(c)
+    d.ns = [rows, 40]
+    d.row0, d.M, d.max_n = np.array([0, rows, rows + 40], np.int32), rows + 40, max(rows, 40)
+    d.qkv = c.qkv[193 - rows:]
+    d.tensors()
+    out = lib8.kv8_attention(d.cache, d.step, d.q, d.ws)
+    assert d.status() == 0
+    out[rows - 1] = 0
+    d.check_attention(out, None, dim ** -0.5, rows=[r for r in range(d.M) if r != rows - 1])
+
+
 @pytest.mark.parametrize("window", [2**30 - 1, 2**30, 2**31 - 2, 2**31 - 1])
 @pytest.mark.parametrize("ns,lens", [([5, 1, 4], [2, 3, 0]), ([70, 3], [5, 90]), ([300], [40])])
 @pytest.mark.parametrize("dim", [64, 128, 256])
