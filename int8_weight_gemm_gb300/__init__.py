@@ -269,7 +269,9 @@ def w8a8_workspace_status(ws, stream=None) -> int:
 
 
 def alloc_workspace(nbytes: int, device="cuda", stream=None):
-    """A zeroed workspace tensor (uint8) of at least nbytes (torch allocations are 512-B aligned)."""
+    """A zeroed workspace tensor (uint8) of at least nbytes (torch allocations are 512-B aligned).  One that an
+    attention-side call (qk_norm_rope, kv8_*) has used is not for the GEMM and Q8_0 calls: those expect zeros where
+    attention leaves partial sums."""
     import torch
 
     ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -471,7 +473,7 @@ def q8_0_blocks_from_split(q, d, blocks=None, stream=None):
 # ---------------------------------------------------------------------------------------------
 # Attention side: rotation, the 8-bit paged cache, attention.  A serving loop calls these once a layer and step, so
 # what does not change between calls (the cache, a step's index buffers, the norm weights and rotation table) is
-# checked once, in a handle that holds its tensors.
+# checked once, in a handle that holds its tensors.  Their workspace (kv8_workspace_bytes) is their own.
 
 def _fp32(t, name, nbytes=0):
     _dev(t, name, nbytes, esize=4)

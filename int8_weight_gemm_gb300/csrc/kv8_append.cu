@@ -20,9 +20,10 @@
 // new values of one head in registers between the amax and the quantisation (four tokens a thread),
 // so they are read once and the scale is known before the first byte is written.
 //
-// Measured: norms and rotation of 16383 rows of 40 heads of 128 57.3 us (5.9 TB/s), of 16 rows 2.6; four prompts of
-// 3501-4096 tokens (32 / 8 heads of 128) appended and read back 97.6 us (4.5 TB/s); 16 single tokens appended and
-// their pages read back 7.9.
+// Measured (GPU time in a captured graph; a call from Python takes 4-5 us more): norms and rotation of 16383 rows of 40
+// heads of 128 57.4 us (5.9 TB/s), of 16 rows 2.7; four prompts of 3501-4096 tokens (32 / 8 heads of 128) appended 78.4 us
+// (4.4 TB/s), read back 20.5 (4.6), one after the other 97.6; 16 single tokens appended 5.0, their pages read back
+// 3.4, one after the other 7.9.
 #include <cuda_runtime.h>
 
 #include "internal.h"

@@ -40,9 +40,9 @@
 // finds its run from a scan of kv_len.  An item cut across CTAs is finished by the last of them to
 // arrive.  Two to four CTAs share an SM, so that one's start, join and drain hide behind the others' streams.
 //
-// Measured (32 query heads, 8 kv heads of 128): 64 contexts of 6001-8191 147 us (6.4 TB/s, 94 % of a copy); one of
-// 131071 49.7 (5.4 TB/s with its join); 16 of 257-4099 22.4, where starts and joins take half; windows of 6 tokens on
-// 16 of 1001-5003 40.4, bound by issue slots and latency at 8 warps an SM.
+// Measured (32 query heads, 8 kv heads of 128): 64 contexts of 6001-8191 148 us (6.3 TB/s, 93 % of a copy); one of
+// 131071 49.8 (5.4 TB/s with its join); 16 of 257-4099 22.6, where starts and joins take half; windows of 6 tokens on
+// 16 of 1001-5003 40.6, bound by issue slots and latency at 8 warps an SM.
 #include "kv8_attention.cuh"
 
 namespace w8a8 {

@@ -26,13 +26,13 @@
 //    are in the pipe meanwhile), the next scores into the same tensor memory.
 // Heads of 256: the sums take half of tensor memory, so there is one stream, of one tile, with two places for the
 // scores of a block of 64 tokens: the next block's scores are there when a block's weights are done.  Four warps do the
-// exponentials and eight convert.  (Two prompts of 2048 on contexts of 6000, 32 query heads, 4 kv heads: 503 us, 664
+// exponentials and eight convert.  (Two prompts of 2048 on contexts of 6000, 16 query heads, 4 kv heads: 504 us, 663
 // TFLOP/s; two streams of half the columns each, scoring twice, 886; 16 rows a warp 1923.)
 // The work is cut like that of the other kernel: items (row tile, kv head) laid end to end in units of a
 // block and cut into equal runs; an item cut across CTAs is finished by the last to arrive, parts joined
 // in the CTAs' order, so replays give the same bits.
 //
-// Measured (32 query heads, 8 kv heads of 128): two prompts of 1900-2048 tokens on contexts of 5800-6144 421 us, 794
+// Measured (32 query heads, 8 kv heads of 128): two prompts of 1900-2048 tokens on contexts of 5800-6144 422 us, 791
 // TFLOP/s, 41 % of a large matrix product's rate.  What bounds it is a stream's chain (scores, weights, sums: four waits
 // that wake a role, 250 cycles each, beside 2600 cycles of exponentials a block); the tensor pipe is busy 34 % of the
 // time.
