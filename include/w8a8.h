@@ -18,7 +18,9 @@
  *              same section: the down kernel's R' * w_norm staging with the sums of squares).
  *
  * and, between a layer's QKV product and its output projection: qk_norm_rope, kv8_append,
- * kv8_attention and kv8_read, a key-value cache held in 8 bits with what fills and reads it.
+ * kv8_attention and kv8_read, a key-value cache held in 8 bits with what fills and reads it; and what
+ * closes a speculative decoding loop around them: kv8_attention_shared (requests behind a common prefix),
+ * kv8_plan (the next step's rows and pages), spec_probs and spec_verify.
  *
  * Conventions for every entry point:
  *  - Data pointers are DEVICE pointers (cudaMalloc or equivalent) unless stated otherwise; the
@@ -65,9 +67,10 @@ enum {
                                          the kernel abandoned the call and returned */
     W8A8_DEV_COUNTER_CORRUPT = 2u,    /* an arrival counter held a value outside [0, arrivals):
                                          the workspace was not zeroed, or calls overlapped */
-    W8A8_DEV_BAD_INDEX = 4u           /* qk_norm_rope and kv8_*: an index in device memory (row0,
-                                         kv_len, page_table, positions) was out of range; nothing
-                                         was read or written through it */
+    W8A8_DEV_BAD_INDEX = 4u           /* qk_norm_rope, kv8_* and spec_verify: an index in device
+                                         memory (row0, kv_len, page_table, positions, seq0, tokens,
+                                         ...) was out of range; nothing was read or written through
+                                         it */
 };
 
 /* Launch flags of w8a8_gemm and q8_0_gemv. */
@@ -478,12 +481,137 @@ int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, const void* 
                   int q_heads, void* out, long long out_stride, float* lse, float scale, int window,
                   unsigned flags, int dtype, void* ws, size_t ws_bytes, void* stream);
 
+/* Consecutive sequences of a step that begin with the same tokens.  Group g is sequences seq0[g] ...
+ * seq0[g + 1] - 1, whose first prefix[g] cached tokens are the same (as a rule, the same pages of the cache);
+ * whole pages of them are shared, the rest are each sequence's own.
+ *  seq0 [groups + 1], prefix [groups]: int32, device memory; seq0 ascends
+ *  max_rows  an upper bound of the rows of one group's sequences together (picks the launch)
+ *  groups <= 65535. */
+typedef struct {
+    const int32_t* seq0;
+    const int32_t* prefix;
+    int groups;
+    int max_rows;
+} kv8_groups_t;
+
+/* Workspace bytes of kv8_attention_shared for a step of up to `tokens` rows (0 for arguments it would
+ * reject); more than kv8_workspace_bytes, whose calls may use it too. */
+size_t kv8_shared_workspace_bytes(int tokens, int groups, int q_heads, int kv_heads, int head_dim);
+
+/* kv8_attention (causal, no window) of sequences that share prefixes: the tokens that a group has in
+ * common are read once, from the pages of the group's first sequence, for the rows of all of them.
+ * The result is that of kv8_attention, with its arguments, where the sequences of each group do hold
+ * the same tokens there.  Nothing is shared, and each sequence reads its own pages, in a group of one
+ * sequence, in one whose first sequence holds less than the prefix, and for a sequence with a row that
+ * does not see all of the prefix; sequences of no group are read on their own.
+ * Three launches, otherwise as kv8_attention.  Errors as above. */
+int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* step, const kv8_groups_t* groups,
+                         const void* q, long long q_stride, int q_heads, void* out, long long out_stride,
+                         float* lse, float scale, int dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Free pages of a cache: a ring of page numbers, taken from its head and given back at its tail.
+ *  ring   int32 [capacity] device memory; the free ones are ring[(state[0] + i) % capacity], i < state[1]
+ *  state  int32 [2] device memory: the head's place, the number of free pages
+ *  capacity  at least the pages that are ever free or in use; <= 2^30. */
+typedef struct {
+    int32_t* ring;
+    int32_t* state;
+    int capacity;
+} kv8_pool_t;
+
+/* What kv8_plan writes (int32, device memory; the first four may be the call's own inputs, for a step
+ * that advances in place; the last four may be NULL).
+ *  row0 [seqs + 1], kv_len [seqs]  the next step's
+ *  held [seqs]                     pages in each sequence's row of the table
+ *  pool_state [2]                  the pool's state
+ *  granted [seqs]                  rows that each sequence got: its grow, or 0
+ *  positions, slots, seq_of [tokens]  of each row of the next step: its position in the sequence, its
+ *                                  place in the cache (page * page_tokens + token of the page), its
+ *                                  sequence; entries behind the last row are left as they were */
+typedef struct {
+    int32_t* row0;
+    int32_t* kv_len;
+    int32_t* held;
+    int32_t* pool_state;
+    int32_t* granted;
+    int32_t* positions;
+    int32_t* slots;
+    int32_t* seq_of;
+} kv8_plan_t;
+
+/* The next step of sequences over a paged cache, worked out on the device.  `step` is the one before
+ * (its row0 and kv_len are read, new pages are entered in its page_table; `tokens` is the room of the
+ * next step's rows, and no sequence gets more than max_tokens).
+ *  held    [seqs] pages in each sequence's row of the table, from its start (kept pages are not taken
+ *          back while a sequence lives, so that a shorter kv_len costs nothing)
+ *  pinned  [seqs] of those, the leading ones that are not the sequence's own (a shared prefix): never
+ *          given back; NULL: none
+ *  take    [seqs] rows of the step before that stay, 0 ... n: kept = kv_len - n + take tokens (what
+ *          spec_verify returns; n for a prompt).  Below 0 the sequence has ended: its pages behind
+ *          the pinned ones go back to the pool, kv_len, held and its rows become 0 (its grow is not read)
+ *  grow    [seqs] rows that each sequence is to have next, slots kept ... kept + grow - 1; pages for
+ *          them are taken from the pool in the order of the sequences
+ * From the first sequence on whose rows do not fit into `tokens`, or its pages into the pool, no
+ * sequence gets rows (granted 0; kv_len = kept).  Pages that come back in a call are handed out from the
+ * next one on.  A sequence whose numbers make no sense (more rows taken than there were, a table too
+ * narrow, ...) keeps its tokens, gets nothing, and W8A8_DEV_BAD_INDEX is recorded.
+ * page_tokens as in kv8_cache_t.  Workspace: 256 bytes, any of the attention side's (kv8_workspace_bytes,
+ * kv8_shared_workspace_bytes) or its own.  One launch; errors as above. */
+int kv8_plan(const kv8_step_t* step, int page_tokens, const kv8_pool_t* pool, const int32_t* held,
+             const int32_t* pinned, const int32_t* take, const int32_t* grow, const kv8_plan_t* out, void* ws,
+             size_t ws_bytes, void* stream);
+
 /* The step's tokens out of the cache as 16-bit values: row r of k_out and v_out
  * ([tokens][kv_heads][head_dim]) is (byte - 128) * scale of that row's slot, rounded once.  Every
  * sequence needs n <= kv_len; a step with other row0 than the append's reads any tail of it.
  * Errors as above. */
 int kv8_read(const kv8_cache_t* cache, const kv8_step_t* step, void* k_out, long long k_stride, void* v_out,
              long long v_stride, int dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Ends of a speculative step: probabilities of a vocabulary, verification of drafted tokens.
+ * ------------------------------------------------------------------------------------------- */
+
+enum { SPEC_F32 = 2 };   /* dtype of the calls below, beside KV8_BF16 and KV8_F16 */
+
+/* out[r][i] = exp((x[r][i] - max) * inv_temp[r]) / sum_j exp((x[r][j] - max) * inv_temp[r]), fp32, of
+ * logits x [rows][vocab] of `dtype`, in one pass with fp32 sums; weights below 2^-126 of a row's largest
+ * are 0.  Strides in elements, any that hold a row; rows that begin on boundaries of four values are
+ * read and written four at a time.  out = logits (fp32, same strides) works in place; other overlaps are
+ * not allowed.
+ *  inv_temp  [rows] fp32: 1 / temperature, NULL: 1 everywhere.  +infinity (temperature 0): 1 for the
+ *            first of the row's largest logits and 0 for the others.  Below 0 or NaN: taken as 0
+ * A logit of -infinity (a mask) or NaN has probability 0, logits of +infinity share the row; a row
+ * without anything else than -infinity and NaN is all 0.
+ * 1 <= vocab <= 2^18, rows <= 2^22.  One launch, no workspace.  Errors: INVALID_ARG, MISALIGNED, CUDA. */
+int spec_probs(const void* logits, long long logits_stride, const float* inv_temp, float* out,
+               long long out_stride, int rows, int vocab, int dtype, void* stream);
+
+/* Workspace bytes of spec_verify (0 for arguments it would reject).  Like the attention side's it is not
+ * for other calls. */
+size_t spec_workspace_bytes(int seqs, int vocab);
+
+/* Verification of drafted tokens.  Sequence b has rows row0[b] ... row0[b + 1] - 1 of the call's `rows`:
+ * its last token, then the drafted ones.  Row r holds the target's probabilities p[r] of the token after
+ * it, and the draft's q[r] that the next row's token was drawn from (q NULL: drafts without probabilities,
+ * as if q were 1 at the drafted token and 0 elsewhere).  The next row's token d is accepted where
+ *   accept[r] * q[r][d] < p[r][d]
+ * in exact arithmetic.  The first row r whose successor is not accepted draws the token after it from
+ * w = max(p[r] - q[r], 0) (q NULL: p[r] without d), the window's last row from w = p[r]:
+ *   token = the first k with  sum_{i <= k} w_i > sample[r] * sum_i w_i
+ * with weights in units of 2^-44, so that no order of the sums changes a token.  A w that is zero
+ * everywhere is replaced by p[r]; where that is zero too the token is -1 and W8A8_DEV_BAD_INDEX is recorded,
+ * as it is for a drafted token outside the vocabulary, which is not accepted.
+ *  p, q            [rows][vocab] of `dtype`, strides in elements; values are taken inside [0, 1], a NaN as 0
+ *  tokens          [rows] int32; accept, sample [rows] fp32, uniform in [0, 1)
+ *  next  [rows]    int32 out: the token after each row, up to the row that draws; -1 for the window's rows
+ *                  behind it; rows of no sequence are left as they were
+ *  take  [seqs]    int32 out: rows that stay (accepted tokens and the one before them), 0 without rows
+ * One launch.  1 <= vocab <= 2^18, seqs <= 65535, rows <= 2^22.  Errors: INVALID_ARG, MISALIGNED,
+ * WORKSPACE_TOO_SMALL, CUDA. */
+int spec_verify(const void* p, long long p_stride, const void* q, long long q_stride, const int32_t* tokens,
+                const int32_t* row0, int seqs, int rows, int vocab, const float* accept, const float* sample,
+                int32_t* next, int32_t* take, int dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* Measurement helper (not part of either operator): reads `bytes` (rounded down to a multiple of
  * 16) of device memory at `buf` once with 16-byte vector loads, on 2 x SM-count CTAs of 512

@@ -46,6 +46,14 @@ __all__ = [
     "kv8_attention",
     "kv8_read",
     "qk_norm_rope",
+    "KV8Groups",
+    "KV8Pool",
+    "kv8_shared_workspace_bytes",
+    "kv8_attention_shared",
+    "kv8_plan",
+    "spec_probs",
+    "spec_workspace_bytes",
+    "spec_verify",
 ]
 
 W8A8_OK = 0
@@ -58,6 +66,7 @@ W8A8_DEV_BAD_INDEX = 4
 KV8_BF16 = 0
 KV8_F16 = 1
 KV8_FLAG_NOT_CAUSAL = 1
+SPEC_F32 = 2
 
 # Every symbol include/w8a8.h declares, with its ctypes signature.
 _c_p = ctypes.c_void_p
@@ -100,6 +109,18 @@ class QKPrepT(ctypes.Structure):
                 ("max_pos", _c_i), ("interleaved", _c_i)]
 
 
+class KV8GroupsT(ctypes.Structure):
+    _fields_ = [("seq0", _c_p), ("prefix", _c_p), ("groups", _c_i), ("max_rows", _c_i)]
+
+
+class KV8PoolT(ctypes.Structure):
+    _fields_ = [("ring", _c_p), ("state", _c_p), ("capacity", _c_i)]
+
+
+class KV8PlanT(ctypes.Structure):
+    _fields_ = [(n, _c_p) for n in ("row0", "kv_len", "held", "pool_state", "granted", "positions", "slots", "seq_of")]
+
+
 _c_ll = ctypes.c_longlong
 
 SIGNATURES = {
@@ -138,6 +159,14 @@ SIGNATURES = {
     "kv8_attention": ([_c_p, _c_p, _c_p, _c_ll, _c_i, _c_p, _c_ll, _c_p, ctypes.c_float, _c_i, ctypes.c_uint, _c_i, _c_p,
                        _c_sz, _c_p], _c_i),
     "kv8_read": ([_c_p, _c_p, _c_p, _c_ll, _c_p, _c_ll, _c_i, _c_p, _c_sz, _c_p], _c_i),
+    "kv8_shared_workspace_bytes": ([_c_i, _c_i, _c_i, _c_i, _c_i], _c_sz),
+    "kv8_attention_shared": ([_c_p, _c_p, _c_p, _c_p, _c_ll, _c_i, _c_p, _c_ll, _c_p, ctypes.c_float, _c_i, _c_p, _c_sz, _c_p],
+                             _c_i),
+    "kv8_plan": ([_c_p, _c_i, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_i),
+    "spec_probs": ([_c_p, _c_ll, _c_p, _c_p, _c_ll, _c_i, _c_i, _c_i, _c_p], _c_i),
+    "spec_workspace_bytes": ([_c_i, _c_i], _c_sz),
+    "spec_verify": ([_c_p, _c_ll, _c_p, _c_ll, _c_p, _c_p, _c_i, _c_i, _c_i, _c_p, _c_p, _c_p, _c_p, _c_i, _c_p, _c_sz, _c_p],
+                    _c_i),
 }
 
 _lib = None
@@ -702,3 +731,178 @@ def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
         _on_cuda(k_out=k_out, v_out=v_out, ws=ws)
     _check("kv8_read", lib().kv8_read(cache.addr, step.addr, k_out.data_ptr(), ks, v_out.data_ptr(), vs, dt, wp, wn, _stream(stream)))
     return k_out, v_out
+
+
+# ---------------------------------------------------------------------------------------------
+# A speculative decoding loop around the cache: requests behind a common prefix, the next step's rows and pages, the
+# probabilities of a vocabulary and the verification of drafted tokens.
+
+def _int32(t, name, shape):
+    """The address of an int32 tensor of `shape` (a length -1: any)."""
+    if t.dim() != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _dev(t, name, esize=4)
+    if t.is_floating_point():
+        raise ValueError(f"{name}: expected int32, got {t.dtype}")
+    return t.data_ptr()
+
+
+class KV8Groups:
+    """Consecutive sequences that begin with the same tokens: group g is sequences seq0[g] ... seq0[g + 1] - 1 with
+    prefix[g] tokens in common; seq0 [groups + 1], prefix [groups], int32 tensors that may be rewritten between calls;
+    max_rows: at most as many rows of one group."""
+
+    def __init__(self, seq0, prefix, max_rows: int):
+        _int32(prefix, "prefix", (-1,))
+        groups = prefix.shape[0]
+        _int32(seq0, "seq0", (groups + 1,))
+        _on_cuda(seq0=seq0, prefix=prefix)
+        self.seq0, self.prefix, self.groups = seq0, prefix, groups
+        self.c = KV8GroupsT(seq0.data_ptr(), prefix.data_ptr(), groups, max_rows)
+        self.addr = ctypes.addressof(self.c)
+
+
+class KV8Pool:
+    """A cache's free pages: ring int32 [capacity] of page numbers and state int32 [2], the head's place and the number
+    of free pages behind it."""
+
+    def __init__(self, ring, state):
+        _int32(ring, "ring", (-1,))
+        _int32(state, "state", (2,))
+        _on_cuda(ring=ring, state=state)
+        self.ring, self.state = ring, state
+        self.c = KV8PoolT(ring.data_ptr(), state.data_ptr(), ring.shape[0])
+        self.addr = ctypes.addressof(self.c)
+
+
+def kv8_shared_workspace_bytes(tokens: int, groups: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of the workspace of kv8_attention_shared for steps of up to `tokens` rows, on the current device."""
+    return int(lib().kv8_shared_workspace_bytes(tokens, groups, q_heads, kv_heads, head_dim))
+
+
+def kv8_attention_shared(cache, step, groups, q, ws, out=None, lse=None, scale=None, stream=None):
+    """kv8_attention of sequences that share prefixes (groups: KV8Groups): what a group has in common is read once."""
+    rows, dim = step.tokens, cache.head_dim
+    dt, dtype = _kv8_dtype(q, "q"), q.dtype
+    q_heads = q.shape[1]
+    if out is None:
+        out = q.new_empty((rows, q_heads, dim))
+    qs, os_ = _heads(q, "q", rows, q_heads, dim, dtype), _heads(out, "out", rows, q_heads, dim, dtype)
+    lp = None
+    if lse is not None:
+        _fp32(lse, "lse", 4 * rows * q_heads)
+        lp = lse.data_ptr()
+    wp, wn = _ws(ws)
+    if not (q.is_cuda and out.is_cuda and ws.is_cuda and (lse is None or lse.is_cuda)):
+        _on_cuda(q=q, out=out, lse=lse, ws=ws)
+    rc = lib().kv8_attention_shared(cache.addr, step.addr, groups.addr, q.data_ptr(), qs, q_heads, out.data_ptr(), os_, lp,
+                                    dim ** -0.5 if scale is None else scale, dt, wp, wn, _stream(stream))
+    _check("kv8_attention_shared", rc)
+    return out
+
+
+def kv8_plan(step, page_tokens: int, pool, held, take, grow, ws, pinned=None, row0_out=None, kv_len_out=None, held_out=None,
+             pool_out=None, granted=None, positions=None, slots=None, seq_of=None, stream=None):
+    """The step after `step` on the device: a sequence keeps `take` rows of it (below 0: it has ended), gets `grow` new ones
+    and pages for them.  All int32: held, pinned, take, grow, granted [seqs]; positions, slots, seq_of [step.tokens].  What
+    is not given of the first four outputs is updated in place (step.row0, step.kv_len, held, pool.state)."""
+    seqs, rows = step.kv_len.shape[0], step.tokens
+    out = {"row0_out": step.row0 if row0_out is None else row0_out, "kv_len_out": step.kv_len if kv_len_out is None else kv_len_out,
+           "held_out": held if held_out is None else held_out, "pool_out": pool.state if pool_out is None else pool_out,
+           "granted": granted, "positions": positions, "slots": slots, "seq_of": seq_of}
+    tensors = dict(held=held, pinned=pinned, take=take, grow=grow)
+    ptrs = [None if t is None else _int32(t, n, (seqs,)) for n, t in tensors.items()]
+    lengths = (seqs + 1, seqs, seqs, 2, seqs, rows, rows, rows)
+    c = KV8PlanT(*(None if t is None else _int32(t, n, (k,)) for (n, t), k in zip(out.items(), lengths)))
+    wp, wn = _ws(ws)
+    _on_cuda(**tensors, **out, ws=ws)
+    rc = lib().kv8_plan(step.addr, page_tokens, pool.addr, *ptrs, ctypes.addressof(c), wp, wn, _stream(stream))
+    _check("kv8_plan", rc)
+
+
+_spec_dtypes = None
+
+
+def _spec_dtype(t, name):
+    global _spec_dtypes
+    if _spec_dtypes is None:
+        import torch
+
+        _spec_dtypes = {torch.bfloat16: KV8_BF16, torch.float16: KV8_F16, torch.float32: SPEC_F32}
+    code = _spec_dtypes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _vocab_rows(t, name, rows, vocab, dtype):
+    """A [rows, vocab] tensor whose rows may be strided: its row stride."""
+    if t.shape != (rows, vocab):
+        raise ValueError(f"{name}: expected shape {(rows, vocab)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    s0, s1 = t.stride()
+    if s1 != 1 and vocab > 1:
+        raise ValueError(f"{name}: expected contiguous rows (strides {tuple(t.stride())})")
+    return s0 if rows > 1 else vocab
+
+
+def _f32s(t, name, rows):
+    if t.dim() != 1 or t.shape[0] != rows:
+        raise ValueError(f"{name}: expected shape {(rows,)}, got {tuple(t.shape)}")
+    _fp32(t, name)
+    return t.data_ptr()
+
+
+def spec_probs(logits, inv_temp=None, out=None, stream=None):
+    """Probabilities fp32 [rows, vocab] of logits (bf16, fp16 or fp32): softmax of logits * inv_temp[row] (None: 1;
+    infinity: 1 for the first of the largest)."""
+    import torch
+
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected [rows, vocab], got {tuple(logits.shape)}")
+    rows, vocab = logits.shape
+    dt = _spec_dtype(logits, "logits")
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=torch.float32, device=logits.device)
+    xs, os_ = _vocab_rows(logits, "logits", rows, vocab, logits.dtype), _vocab_rows(out, "out", rows, vocab, torch.float32)
+    ip = None if inv_temp is None else _f32s(inv_temp, "inv_temp", rows)
+    if not (logits.is_cuda and out.is_cuda and (inv_temp is None or inv_temp.is_cuda)):
+        _on_cuda(logits=logits, inv_temp=inv_temp, out=out)
+    rc = lib().spec_probs(logits.data_ptr(), xs, ip, out.data_ptr(), os_, rows, vocab, dt, _stream(stream))
+    _check("spec_probs", rc)
+    return out
+
+
+def spec_workspace_bytes(seqs: int, vocab: int) -> int:
+    """Bytes of the workspace of spec_verify on the current device."""
+    return int(lib().spec_workspace_bytes(seqs, vocab))
+
+
+def spec_verify(p, tokens, row0, accept, sample, ws, q=None, next=None, take=None, stream=None):
+    """Verification of drafted tokens: (next [rows], take [seqs]) int32, from the target's probabilities p [rows, vocab], the
+    draft's q (None: drafts without probabilities), tokens [rows] and row0 [seqs + 1] int32, accept and sample [rows] fp32
+    uniform in [0, 1).  next[r]: the token after row r, -1 behind the row that draws; take[b]: rows that stay."""
+    import torch
+
+    if p.dim() != 2:
+        raise ValueError(f"p: expected [rows, vocab], got {tuple(p.shape)}")
+    rows, vocab = p.shape
+    dt = _spec_dtype(p, "p")
+    ps = _vocab_rows(p, "p", rows, vocab, p.dtype)
+    qp, qs = (None, 0) if q is None else (q.data_ptr(), _vocab_rows(q, "q", rows, vocab, p.dtype))
+    rp = _int32(row0, "row0", (-1,))
+    seqs = row0.shape[0] - 1
+    if next is None:
+        next = torch.full((rows,), -1, dtype=torch.int32, device=p.device)
+    if take is None:
+        take = torch.empty(max(seqs, 0), dtype=torch.int32, device=p.device)
+    tp, np_, kp = _int32(tokens, "tokens", (rows,)), _int32(next, "next", (rows,)), _int32(take, "take", (seqs,))
+    ap, sp = _f32s(accept, "accept", rows), _f32s(sample, "sample", rows)
+    wp, wn = _ws(ws)
+    if not (p.is_cuda and tokens.is_cuda and row0.is_cuda and accept.is_cuda and sample.is_cuda and ws.is_cuda and next.is_cuda and
+            take.is_cuda and (q is None or q.is_cuda)):
+        _on_cuda(p=p, q=q, tokens=tokens, row0=row0, accept=accept, sample=sample, next=next, take=take, ws=ws)
+    rc = lib().spec_verify(p.data_ptr(), ps, qp, qs, tp, rp, seqs, rows, vocab, ap, sp, np_, kp, dt, wp, wn, _stream(stream))
+    _check("spec_verify", rc)
+    return next, take

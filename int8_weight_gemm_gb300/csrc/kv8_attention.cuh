@@ -43,6 +43,13 @@ struct Params {
   uint32_t* counters;      // [CTA] arrivals at the item that crosses the end of its run, zero between calls
   uint32_t* group_counters;   // [CTA][2] arrivals at a group of parts, by its first part's place, zero between calls
   float* parts;            // [CTA][2] parts of split items
+  // Sequences that share prefixes (kv8_attention_shared; groups = 0: none do).
+  const int* seq0;         // [groups + 1] first sequence of each group
+  const int* prefix;       // [groups] tokens that its sequences have in common
+  int groups, all_seqs;
+  int by_group;            // the "sequences" of this launch are the groups, over their prefixes
+  float* rows32;           // not NULL: rows go here instead of out and lse, unnormalised: [tokens][q_heads] of D sums, (m, l, r, -)
+  int4* items;             // by_group: where an item's parts lie (item_of): first CTA, parts, place in the first one, -
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -61,20 +68,90 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// A sequence of a launch: also its first token that is not another launch's, and its row of the page table.
+struct Rows : Seq {
+  int lo, table;
+};
+
+// The tokens of group g's shared prefix, in whole pages, and its first sequence; 0 where nothing is shared: a single
+// sequence, or a first one that does not hold the prefix.
+__device__ __forceinline__ int group_prefix(const Params& p, int g, int& first, int& last) {
+  first = __ldg(p.seq0 + g), last = __ldg(p.seq0 + g + 1);
+  if (first < 0 || last < first || last > p.all_seqs) {
+    atomicOr(p.status, W8A8_DEV_BAD_INDEX);
+    first = last = 0;
+    return 0;
+  }
+  const int whole = __ldg(p.prefix + g) & ~((1 << p.page_shift) - 1);
+  if (last - first < 2 || whole <= 0 || __ldg(p.step.kv_len + first) < whole ||
+      (long long)whole > (long long)p.step.table_width << p.page_shift)
+    return 0;
+  return whole;
+}
+
+// The group of sequence b (-1: of none).
+__device__ __forceinline__ int group_of(const Params& p, int b) {
+  int lo = 0, n = p.groups;   // the last group that begins at or before b
+  while (n > 1) {
+    const int half = n >> 1;
+    if (__ldg(p.seq0 + lo + half) <= b) lo += half;
+    n -= half;
+  }
+  return __ldg(p.seq0 + lo) <= b && b < __ldg(p.seq0 + lo + 1) ? lo : -1;
+}
+
+// Group g as a sequence: the rows of all its sequences over the shared prefix (no rows where nothing is shared).
+__device__ __forceinline__ void load_group(const Params& p, int g, Rows& s) {
+  int last;
+  s.lo = s.row0 = s.n = 0;
+  s.len = group_prefix(p, g, s.table, last);
+  if (s.len == 0) return;
+  const int r0 = __ldg(p.step.row0 + s.table), r1 = __ldg(p.step.row0 + last);
+  if (r0 >= 0 && r1 >= r0 && r1 <= p.step.tokens) s.row0 = r0, s.n = r1 - r0;
+}
+
+// Tokens of sequence b that its group's launch covers, and that group: all of the shared prefix where every row of the
+// sequence sees all of it, else none.
+__device__ __forceinline__ int shared_tokens(const Params& p, int b, const Seq& s, int& g, Rows& of) {
+  if ((g = group_of(p, b)) < 0) return 0;
+  load_group(p, g, of);
+  return of.len > 0 && s.len - s.n >= of.len && s.row0 >= of.row0 && s.row0 + s.n <= of.row0 + of.n ? of.len : 0;
+}
+
+// Reads "sequence" b of the launch.
+__device__ __forceinline__ void load_rows(const Params& p, int b, Rows& s) {
+  if (p.by_group) return load_group(p, b, s);
+  s.lo = 0;
+  s.table = b;
+  load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  if (p.groups > 0) {
+    int g;
+    Rows of;
+    s.lo = shared_tokens(p, b, s, g, of);
+  }
+}
+
+// The place of a row tile's entry in `items`: tiles of `rows` of the group's rows, which begin at row r0 of the step.
+// (A group of x tiles' worth of rows has ceil(x) tiles; floor(a + x) - floor(a) + 1 places are never fewer.)
+__device__ __forceinline__ size_t item_of(const Params& p, int g, int r0, int rows, int tile, int h) {
+  return ((size_t)((long long)r0 * p.group / rows) + g + tile) * p.kv_heads + h;
+}
+
 // What the rows of a sequence cover: items of `tiles` row tiles and kv heads, each of `units` units
 // from token `lo` (a granule's start) to `hi`; `span` = the lead and the units, its length in the split.
 struct Span {
-  Seq s;
+  Rows s;
   int tiles, units, span, lo, hi;
 };
 
-template <typename L>
+template <typename L, bool kShared>
 __device__ __forceinline__ Span load_span(const Params& p, int b) {
   Span x;
-  load_seq(p.step, b, 1 << p.page_shift, false, p.status, x.s);
+  if (kShared) load_rows(p, b, x.s);
+  else load_seq(p.step, b, 1 << p.page_shift, false, p.status, x.s);
   x.tiles = (int)quotient((long long)x.s.n * p.group + L::kRows - 1, L::kRows);
   x.hi = x.s.len;
-  x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : 0;
+  x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : kShared ? x.s.lo : 0;
   x.units = max(1, (x.hi - x.lo + L::kUnit - 1) / L::kUnit);   // one that sees nothing still writes its rows
   x.span = L::kLead + x.units;
   return x;
@@ -94,6 +171,14 @@ struct Runs {
 // The kernel of many query rows (kv8_attention_tc.cu); its share of the workspace.
 cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
 size_t many_parts_bytes(int head_dim, int sms);
+// Rows of one of its tiles for sequences of up to `rows` rows of a kv head.
+int many_tile_rows(int head_dim, long long rows);
+
+// kv8_attention.cu: arguments that both entry points check and fill in alike.
+int check_call(const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride, int q_heads, const void* out,
+               long long out_stride, const float* lse, float scale, int dtype);
+cudaError_t fill_params(Params& p, const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride, int q_heads,
+                        void* out, long long out_stride, float* lse, float scale, void* ws, int sms);
 
 }  // namespace attn
 }  // namespace w8a8

@@ -1,0 +1,233 @@
+// Attention over the 8-bit paged cache for sequences that share prefixes (kv8_attention_shared): the tokens that a
+// group of sequences has in common are read once, for all of their rows.
+//
+// Mathematics.  The tokens that a row sees are the prefix, then its sequence's own.  Each side gives sums o relative to a
+// reference r, and (m, l) of its softmax (kv8_attention.cu); the two, and the parts of a side that was cut, join as
+//   M = max m_i,  R = max r_i,  l = sum l_i 2^(m_i - M),  o = sum o_i 2^(r_i - R),  out = o 2^(R - M) / l.
+//
+// What bounds it: with the prefix read once its products do.  64 rows' heads of 4 a kv head are 256 rows over every
+// prefix byte, work for the kernel of many rows (kv8_attention_tc.cu); the own tokens are a decode step's and stream at
+// HBM speed (kv8_attention.cu, or the other for many rows).  So a call is three launches: the groups over their
+// prefixes as if each were one sequence, not causal; the sequences over their own tokens; and the join.  The first two
+// leave fp32 rows.  A prefix of few items (a kv head's 256 rows each) is cut over all SMs, some twenty parts an item,
+// which one CTA an item would read for longer than the products take: the join below has a warp for each (row, head),
+// on all SMs.
+#include "kv8_attention_few.cuh"
+
+namespace w8a8 {
+namespace attn {
+
+constexpr int kJoinThreads = 256;
+
+struct JoinParams {
+  Params p;
+  const float* own;      // [tokens][q_heads] of D sums, (m, l, r, -): over the sequences' own tokens
+  const float* whole;    // the same over the prefixes, of items that were not cut
+  const float* parts;    // of items that were
+  int tile_shift;        // rows of an item: 2^tile_shift
+};
+
+// A warp for each row and query head.
+template <bool kF16, int D>
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ JoinParams j) {
+  const Params& p = j.p;
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x, head = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  if (head >= p.q_heads) return;
+  const size_t at = (size_t)row * p.q_heads + head;
+  // The row's sequence: the last that begins at or before it.
+  int b = 0;
+  for (int n = p.step.seqs; n > 1;) {
+    const int step = (n + 31) / 32;
+    const bool in = lane * step < n && __ldg(p.step.row0 + b + lane * step) <= row;
+    const uint32_t mask = __ballot_sync(0xffffffffu, in);
+    const int k = mask ? 31 - __clz(mask) : 0;
+    b += k * step;
+    n = min(step, n - k * step);
+  }
+  Seq s;
+  load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  if (row < s.row0 || row >= s.row0 + s.n) return;   // behind the last sequence
+  // Values of the row: four a lane (D = 64: by half a warp, the other half takes every other part; 256: two times four).
+  constexpr int kV = D == 256 ? 2 : 1, kAt = D == 64 ? 2 : 1;
+  const int d = 4 * (lane & (D == 64 ? 15 : 31));
+  const float* const own = j.own + at * (D + 4);
+  const float4 t0 = __ldcg(reinterpret_cast<const float4*>(own + D));
+  float M = t0.x, R = t0.z, l = t0.y;
+  float4 acc[kV];
+#pragma unroll
+  for (int v = 0; v < kV; ++v) acc[v] = __ldcg(reinterpret_cast<const float4*>(own + d + 128 * v));
+
+  int g, parts = 0;
+  Rows of;
+  int4 item = make_int4(0, 0, 0, 0);
+  int within = 0;
+  if (shared_tokens(p, b, s, g, of) > 0) {
+    const long long ri = (long long)(row - of.row0) * p.group + head % p.group;
+    const int tile = (int)(ri >> j.tile_shift);
+    within = (int)ri & ((1 << j.tile_shift) - 1);
+    item = __ldcg(p.items + item_of(p, g, of.row0, 1 << j.tile_shift, tile, head / p.group));
+    parts = item.y;
+  }
+  const size_t part_floats = (size_t)(D + 4) << j.tile_shift;
+  auto sums_of = [&](int i) {
+    return parts == 1 ? j.whole + at * (D + 4) : j.parts + ((size_t)(item.x + i) * 2 + (i == 0 ? item.z : 0)) * part_floats + (size_t)within * D;
+  };
+  auto stats_of = [&](int i) {
+    return __ldcg(reinterpret_cast<const float4*>(parts == 1 ? sums_of(0) + D : sums_of(i) - (size_t)within * D + ((size_t)D << j.tile_shift) + within * 4));
+  };
+  if (parts > 0) {
+    // References first: a lane for each part.
+    float4 t = make_float4(kFloor, 0.f, kFloor, 0.f);
+    if (lane < parts) t = stats_of(lane);
+    float mm = t.x, rm = t.z, lt = t.y;
+    for (int i = lane + 32; i < parts; i += 32) {
+      const float4 x = stats_of(i);
+      const float mn = fmaxf(mm, x.x);
+      lt = lt * ex2(mm - mn) + x.y * ex2(x.x - mn);
+      mm = mn;
+      rm = fmaxf(rm, x.z);
+    }
+    float mn = fmaxf(M, mm), rn = fmaxf(R, rm);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      rn = fmaxf(rn, __shfl_xor_sync(0xffffffffu, rn, o));
+    }
+    lt *= ex2(mm - mn);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    l = fmaf(l, ex2(M - mn), lt);
+    const float a0 = D == 64 && lane >= 16 ? 0.f : ex2(R - rn);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) acc[v].x *= a0, acc[v].y *= a0, acc[v].z *= a0, acc[v].w *= a0;
+    M = mn;
+    R = rn;
+    const int odd = D == 64 ? lane >> 4 : 0;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      float a = 0.f;
+      if (i0 + lane < parts) a = ex2((i0 ? stats_of(i0 + lane).z : t.z) - R);
+      const int n = min(32, parts - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; i += kAt) {
+        const float f = __shfl_sync(0xffffffffu, a, (i + odd) & 31);
+        if (i + odd < n) {
+          const float* const src = sums_of(i0 + i + odd) + d;
+#pragma unroll
+          for (int v = 0; v < kV; ++v) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 128 * v));
+            acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
+          }
+        }
+      }
+    }
+    if (D == 64) {
+      acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
+      acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
+    }
+  }
+  const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(R - M);
+  if (D > 64 || lane < 16) {
+    uint16_t* const dst = p.out + row * p.out_stride + head * D + d;
+#pragma unroll
+    for (int v = 0; v < kV; ++v)
+      *reinterpret_cast<uint2*>(dst + 128 * v) =
+          make_uint2(pack2<kF16>(acc[v].x * z, acc[v].y * z), pack2<kF16>(acc[v].z * z, acc[v].w * z));
+  }
+  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + lg2(l)) * 0.69314718056f;
+}
+
+template <bool kF16, int D>
+static cudaError_t launch_join(const JoinParams& j, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)j.p.step.tokens, (unsigned)((j.p.q_heads + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_join_kernel<kF16, D>, j);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool kF16>
+static cudaError_t launch_join_of(const JoinParams& j, int head_dim, cudaStream_t s) {
+  return head_dim == 64 ? launch_join<kF16, 64>(j, s) : head_dim == 128 ? launch_join<kF16, 128>(j, s) : launch_join<kF16, 256>(j, s);
+}
+
+// The workspace behind that of kv8_attention: parts of cut prefixes, their places, and two buffers of fp32 rows.
+struct SharedLayout {
+  size_t parts, items, whole, own, bytes;
+  SharedLayout(int tokens, int groups, int q_heads, int kv_heads, int head_dim, int sms) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t rows = up((size_t)tokens * q_heads * (head_dim + 4) * sizeof(float));
+    parts = up(kv8_workspace_bytes(q_heads, kv_heads, head_dim));
+    items = parts + up(many_parts_bytes(head_dim, sms));
+    whole = items + up(((size_t)tokens * (q_heads / kv_heads) / many_tile_rows(head_dim, 1) + groups + 1) * kv_heads * sizeof(int4));
+    own = whole + rows;
+    bytes = own + rows;
+  }
+};
+
+}  // namespace attn
+}  // namespace w8a8
+
+using namespace w8a8;
+
+extern "C" size_t kv8_shared_workspace_bytes(int tokens, int groups, int q_heads, int kv_heads, int head_dim) {
+  if (kv8_check_dims(kv_heads, head_dim) != W8A8_OK || q_heads < 1 || q_heads > 4096 || q_heads % kv_heads != 0 || tokens < 0 ||
+      tokens > (1 << 22) || groups < 1 || groups > 65535)
+    return 0;
+  return attn::SharedLayout(tokens, groups, q_heads, kv_heads, head_dim, device_sm_count()).bytes;
+}
+
+extern "C" int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* step, const kv8_groups_t* groups, const void* q,
+                                    long long q_stride, int q_heads, void* out, long long out_stride, float* lse, float scale,
+                                    int dtype, void* ws, size_t ws_bytes, void* stream) {
+  int rc = kv8_check_cache(cache);
+  if (rc == W8A8_OK) rc = kv8_check_step(step, cache);
+  if (rc != W8A8_OK) return rc;
+  if (!groups || !groups->seq0 || !groups->prefix || groups->groups < 1 || groups->groups > 65535 || groups->max_rows < 1 ||
+      groups->max_rows > (1 << 22))
+    return W8A8_ERR_INVALID_ARG;
+  if (!kv8_aligned(groups->seq0, 4) || !kv8_aligned(groups->prefix, 4)) return W8A8_ERR_MISALIGNED;
+  if ((rc = attn::check_call(cache, step, q, q_stride, q_heads, out, out_stride, lse, scale, dtype)) != W8A8_OK) return rc;
+  if (step->tokens == 0) return W8A8_OK;
+  const int D = cache->head_dim, sms = device_sm_count();
+  const attn::SharedLayout at(step->tokens, groups->groups, q_heads, cache->kv_heads, D, sms);
+  if ((rc = kv8_check_ws(ws, ws_bytes, at.bytes)) != W8A8_OK) return rc;
+  uint8_t* const w = static_cast<uint8_t*>(ws);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == KV8_F16;
+  attn::JoinParams j;
+  cudaError_t e = attn::fill_params(j.p, cache, step, q, q_stride, q_heads, out, out_stride, lse, scale, ws, sms);
+  if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
+  j.p.seq0 = groups->seq0;
+  j.p.prefix = groups->prefix;
+  j.p.groups = groups->groups;
+  j.p.items = reinterpret_cast<int4*>(w + at.items);
+  // The groups over their prefixes.
+  attn::Params a = j.p;
+  a.by_group = 1, a.causal = 0;
+  a.step.seqs = groups->groups;
+  a.step.max_tokens = groups->max_rows;
+  a.parts = reinterpret_cast<float*>(w + at.parts);
+  a.rows32 = reinterpret_cast<float*>(w + at.whole);
+  e = attn::launch_many(a, D, f16, sms, s);
+  if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
+  // The sequences over their own tokens.
+  attn::Params b = j.p;
+  b.rows32 = reinterpret_cast<float*>(w + at.own);
+  e = f16 ? attn::launch_rows<true, true>(b, D, sms, s) : attn::launch_rows<false, true>(b, D, sms, s);
+  if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
+  j.own = b.rows32;
+  j.whole = a.rows32;
+  j.parts = a.parts;
+  j.tile_shift = attn::many_tile_rows(D, (long long)groups->max_rows * j.p.group) == 128 ? 7 : 8;
+  e = f16 ? attn::launch_join_of<true>(j, D, s) : attn::launch_join_of<false>(j, D, s);
+  return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention_shared");
+}

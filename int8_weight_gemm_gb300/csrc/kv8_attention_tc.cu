@@ -78,12 +78,12 @@ struct TileSpan {
 };
 
 template <typename L>
-__device__ __forceinline__ TileSpan tile_span(const Params& p, const Seq& s, int tile) {
+__device__ __forceinline__ TileSpan tile_span(const Params& p, const Rows& s, int tile) {
   TileSpan t;
   const int first = (int)quotient((long long)tile * L::kRows, p.group);
   const int last = min(s.n - 1, (int)quotient((long long)tile * L::kRows + L::kRows - 1, p.group));
   t.hi = p.causal ? max(0, s.len - s.n + last + 1) : s.len;
-  t.lo = p.window > 0 ? max(0, s.len - s.n + first - p.window + 1) & ~(kGranule - 1) : 0;
+  t.lo = p.window > 0 ? max(0, s.len - s.n + first - p.window + 1) & ~(kGranule - 1) : s.lo;
   t.units = max(1, (t.hi - t.lo + L::kBlock - 1) / L::kBlock);
   return t;
 }
@@ -109,7 +109,7 @@ constexpr int kSegments = 4;   // segments under way
 template <typename L>
 struct Walk {
   long long u, u1, item_u0;
-  Seq s;
+  Rows s;
   TileSpan t;
   int b, h, tile, tiles, ub, ue;
   // Set on the item (b, h, tile) that begins at item_u0 at or before u.
@@ -122,7 +122,7 @@ struct Walk {
           if (++h == p.kv_heads) {
             h = 0;
             do {
-              load_seq(p.step, ++b, 1 << p.page_shift, false, p.status, s);
+              load_rows(p, ++b, s);
               tiles = tiles_of<L>(p, s);
             } while (tiles == 0);
           }
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   __shared__ uint32_t turns[kScales][kGrans];   // fp16 factors of a granule's keys (low half) and values: 1 or -1
   __shared__ long long scan_sm[kTcThreads / 32];
   __shared__ struct {
-    Seq s;
+    Rows s;
     int b;
     long long u;
   } start_sm;
@@ -302,15 +302,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   const int per = (p.step.seqs + kTcThreads - 1) / kTcThreads;   // sequences a thread scans
   const int s0 = min(p.step.seqs, (int)threadIdx.x * per), s1 = min(p.step.seqs, s0 + per);
   long long mine = 0;
-  auto seq_units = [&](int b, Seq& s) {
-    load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  auto seq_units = [&](int b, Rows& s) {
+    load_rows(p, b, s);
     const int tiles = tiles_of<L>(p, s);
     long long n = 0;
     for (int t = 0; t < tiles; ++t) n += L::kLead + tile_span<L>(p, s, t).units;
     return n * p.kv_heads;
   };
   for (int b = s0; b < s1; ++b) {
-    Seq s;
+    Rows s;
     mine += seq_units(b, s);
   }
   long long incl = mine;
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   if (active && u0 >= before && u0 < before + mine) {
     long long at = before;
     for (int b = s0; b < s1; ++b) {
-      Seq s;
+      Rows s;
       const long long n = seq_units(b, s);
       if (u0 < at + n) {
         start_sm.s = s;
@@ -396,13 +396,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           g.first = runs.owner(wk.item_u0 + L::kLead);
           g.parts = runs.owner(wk.item_u0 + L::kLead + wk.t.units - 1) - g.first + 1;
           g.slot0 = wk.item_u0 <= runs.begin(g.first) ? 0 : 1;
+          if (p.by_group && wk.ub == 0) p.items[item_of(p, wk.b, wk.s.row0, L::kRows, wk.tile, wk.h)] = make_int4(g.first, g.parts, g.slot0, 0);
         }
         segs[seg % kSegments] = g;
       }
       arrive_warp(&seg_full[seg % kSegments]);
       if (!more) break;
       const int T0 = wk.t.lo + wk.ub * kBlock, T1 = min(wk.t.hi, wk.t.lo + wk.ue * kBlock);
-      const int* const table = p.step.page_table + (size_t)wk.b * p.step.table_width;
+      const int* const table = p.step.page_table + (size_t)wk.s.table * p.step.table_width;
       constexpr int kFetch = 32 / kGrans;   // blocks
       for (int base = 0; ok && base < nb; base += kFetch) {
         // Lane: granule lane % kGrans of block base + lane / kGrans.
@@ -867,6 +868,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
       }
       const bool whole = g->whole;
       float* const part = p.parts + ((size_t)blockIdx.x * 2 + g->slot) * L::kPart;
+      float* const row32 = p.rows32 + ((size_t)(g->row0 + tok) * p.q_heads + head) * (D + 4);   // (rows32 given)
       const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(r - m);
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
@@ -895,7 +897,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
           v[k] = __uint_as_float(o[k]);
           if (kAlternate) v[k] = fmaf(v[k], scale_own, scale_other == 0.f ? 0.f : xch[(c0 % kX + k) * kTileRows + row] * scale_other);
         }
-        if (live && whole) {
+        if (live && (!whole || p.rows32)) {
+          float4* const dst = reinterpret_cast<float4*>((whole ? row32 : part + irow * D) + c0);
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+        } else if (live) {
           uint4* const dst = reinterpret_cast<uint4*>(p.out + (g->row0 + tok) * p.out_stride + head * D + c0);
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
@@ -908,19 +914,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
             }
             dst[k / 8] = pack8<kF16>(y);
           }
-        } else if (live) {
-          float4* const dst = reinterpret_cast<float4*>(part + irow * D + c0);
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) dst[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
       }
       if (!ok) break;
       if (live && (kTiles == 2 || st == 0)) {
-        if (!whole) *reinterpret_cast<float4*>(part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
+        if (!whole || p.rows32) *reinterpret_cast<float4*>(whole ? row32 + D : part + L::kRows * D + irow * 4) = make_float4(m, l, r, 0.f);
         else if (p.lse) p.lse[(size_t)(g->row0 + tok) * p.q_heads + head] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.69314718056f;
       }
       tc_fence_before();
-      if (!whole) {
+      if (!whole && !p.by_group) {   // (the parts of shared prefixes are joined by another kernel)
         // The part is written; the last CTA to arrive joins all of the item's, in the CTAs' order.  (The
         // meeting orders the warps' stores before thread 0's release, and its acquire before their reads.)
         // Many parts join first in groups of about sqrt(n), each by the last of its CTAs, so that no CTA reads more than
@@ -1013,6 +1015,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
               const float4 t = row_sm[rw];
               const int oi = g->tile * L::kRows + rw;
               const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
+              if (p.rows32) {
+                float* const dst = p.rows32 + ((size_t)orow * p.q_heads + oh) * (D + 4);
+                *reinterpret_cast<float4*>(dst + d) = acc[y];
+                if (d == 0) *reinterpret_cast<float4*>(dst + D) = t;
+                continue;
+              }
               const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
               *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
                   make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
@@ -1062,7 +1070,7 @@ static cudaError_t launch_tc(const Params& p, int sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s) {
-  const bool one = (long long)p.step.max_tokens * p.group <= kTileRows;
+  const bool one = many_tile_rows(head_dim, (long long)p.step.max_tokens * p.group) == kTileRows;
   if (head_dim == 256) return f16 ? launch_tc<true, 256, 1>(p, sms, s) : launch_tc<false, 256, 1>(p, sms, s);
   if (head_dim == 64)
     return f16 ? (one ? launch_tc<true, 64, 1>(p, sms, s) : launch_tc<true, 64, 2>(p, sms, s))
@@ -1070,6 +1078,8 @@ cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaSt
   return f16 ? (one ? launch_tc<true, 128, 1>(p, sms, s) : launch_tc<true, 128, 2>(p, sms, s))
              : (one ? launch_tc<false, 128, 1>(p, sms, s) : launch_tc<false, 128, 2>(p, sms, s));
 }
+
+int many_tile_rows(int head_dim, long long rows) { return head_dim == 256 || rows <= kTileRows ? kTileRows : 2 * kTileRows; }
 
 size_t many_parts_bytes(int head_dim, int sms) {
   const int part = head_dim == 64 ? TcLayout<64, 2>::kPart : head_dim == 128 ? TcLayout<128, 2>::kPart : TcLayout<256, 1>::kPart;
