@@ -1,5 +1,7 @@
 // Ends of a speculative decoding step: the probabilities of a vocabulary from its logits (spec_probs), and the
 // verification of drafted tokens against them from given random numbers (spec_verify).
+#include <mutex>
+
 #include "internal.h"
 #include "kv8.cuh"
 
@@ -35,12 +37,17 @@ struct Type<SPEC_F32> {
 // ------------------------------------------------------------------------------------------------ probabilities
 //   p_i = exp((x_i - m) / T) / sum_j exp((x_j - m) / T),   m = max x
 //
-// What bounds it: HBM, two bytes in and four out for each of a row's values (bf16), some ten instructions beside them.
+// What bounds it: HBM, two bytes in and four out for each of a row's values (bf16), eight instructions beside them.
 // A row is held in the registers of a cluster of up to eight CTAs, so it is read once and its exponentials are taken
-// once: relative to the CTA's own maximum, then times one factor that follows from all CTAs' maxima and sums, which go
-// through distributed shared memory.
+// once: relative to the warp's own maximum, then times one factor that follows from all warps' maxima and sums, which go
+// to every CTA through distributed shared memory, as stores that count towards its barrier: a barrier of the cluster
+// would first wait for the previous row's stores to HBM.  A warp waits for the others once a row.  Clusters stay for
+// several rows: a warp copies its part of the next row into shared memory as soon as it has this one's in registers, and
+// the row after that is fetched into L2, so that loads hide behind a whole row's work (320 rows of 131072: loads into
+// registers behind the stores 58 us, without the fetch into L2 94).
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
 struct ProbsParams {
   const void* x;
@@ -48,7 +55,7 @@ struct ProbsParams {
   const float* inv_temp;
   float* out;
   long long out_stride;
-  int vocab, share, ctas;   // a CTA's values (a multiple of four), a row's CTAs
+  int rows, vocab, share, ctas;   // a CTA's values (a multiple of four), a row's CTAs
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -56,130 +63,193 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// exp(t) for t <= 0 (a NaN: 0): the product with log2 e in two parts, as its rounding alone would be a relative error of
-// 2^-18 at t = -64.
-__device__ __forceinline__ float exp_of(float t) {
-  t = fmaxf(t, -200.f);
-  const float hi = t * 1.44269504f;
-  const float lo = fmaf(t, 1.92596299e-8f, fmaf(t, 1.44269504f, -hi));   // 1.92596299e-8 = log2 e - 1.44269504f
-  const float y = ex2(hi);
-  return fmaf(y, lo * 0.69314718f, y);
-}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster_v2f(uint32_t addr, float a, float b) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(a), "f"(b) : "memory");
+// Two floats into a CTA's shared memory, eight bytes towards the phase of its barrier.
+__device__ __forceinline__ void st_async_v2f(uint32_t addr, float a, float b, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(a), "f"(b),
+               "r"(bar)
+               : "memory");
+}
+// Wait for a phase of this CTA's barrier, about a second at most (every warp of the row sends to it, so it does complete).
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+  if (mbar_test_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_suspend(bar, parity))
+    if (clock64() - t0 > kWaitTimeoutCycles) return false;
+  return true;
 }
 
-// kE: values a thread holds.  kVec: four neighbours at a time (rows and strides aligned for it), else one.
+// kE: values a thread holds, of its warp's 32 kE consecutive ones.  kVec: four neighbours at a time, by way of shared memory
+// (rows, strides and the vocabulary in whole 16 bytes); else one, into the register.
 template <int kType, int kE, bool kVec>
 __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(const __grid_constant__ ProbsParams p) {
   using Ty = Type<kType>;
-  __shared__ float red_sm[2][kWarps];
-  __shared__ int best_sm[kWarps];
-  __shared__ __align__(8) float2 peers_sm[8];   // (maximum, sum) of each CTA of the row
-  __shared__ __align__(8) float2 first_sm[8];   // greedy: index of each CTA's first largest value (as bits)
+  using T = typename Ty::T;
+  // Of each warp of the row, for two rows in turn: its maximum, and the sum of its exponentials (temperature 0: the place
+  // of its first largest value).
+  __shared__ __align__(8) float2 peers_sm[2][kMaxCluster * kWarps];
+  __shared__ __align__(8) uint64_t full[2];
+  __shared__ __align__(8) uint64_t loaded[kWarps];
+  extern __shared__ __align__(16) uint8_t smem_raw[];   // kVec: a warp's part of the next row
   const int rank = (int)cluster_ctarank(), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x / p.ctas;
-  cluster_arrive();   // the other CTAs' shared memory may be written once they have begun
+  const int stride = gridDim.x / p.ctas;   // clusters
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1), mbar_init(&full[1], 1);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) mbar_init(&loaded[w], 1);
+    mbar_fence_init();
+  }
+  __syncwarp();
+  // Behind this barrier every CTA has begun, and its barriers may be used: by its own warps too.
+  cluster_arrive();
   pdl_trigger();
   pdl_wait();
+  __syncwarp();
+  cluster_wait();
   const int begin = rank * p.share, end = min(p.vocab, begin + p.share);
-  const typename Ty::T* const src = static_cast<const typename Ty::T*>(p.x) + row * p.x_stride;
-  float* const dst = p.out + row * p.out_stride;
-  // A thread's values: i-th of v at place begin + first + (i / kN) * kThreads * kN + i % kN.
+  // A thread's values: i-th of v at place first + (i / kN) * 32 * kN + i % kN of the row.
   constexpr int kN = kVec ? 4 : 1;
-  const int left = end - begin - kN * (int)threadIdx.x;   // values from the thread's first on
-  const size_t first = (size_t)begin + kN * threadIdx.x;
-  auto place = [](int i) { return (i / kN) * kThreads * kN + i % kN; };
-
+  const int warp_first = begin + warp * 32 * kE;
+  const size_t first = (size_t)warp_first + kN * lane;
+  const int left = end - (int)first;   // values from the thread's first on
+  auto place = [](int i) { return (i / kN) * 32 * kN + i % kN; };
   float v[kE];
-#pragma unroll
-  for (int i = 0; i < kE; i += kN) {
-    float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    if (kVec && place(i) + kN <= left) {
-      Ty::load4(src + first + place(i), f);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kN; ++k)
-        if (place(i) + k < left) f[k] = Ty::load(src + first + place(i) + k);
+  T* const part = reinterpret_cast<T*>(smem_raw) + warp * 32 * kE;
+  const uint32_t part_bytes = (uint32_t)(max(0, min(32 * kE, end - warp_first)) * (int)sizeof(T));
+  auto fetch = [&](int row) {   // this warp's part of a row, by one lane
+    if (kVec && lane == 0 && row < p.rows && part_bytes > 0) {
+      mbar_arrive_expect_tx(&loaded[warp], part_bytes);
+      bulk_g2s(part, static_cast<const T*>(p.x) + row * p.x_stride + warp_first, part_bytes, &loaded[warp]);
     }
-#pragma unroll
-    for (int k = 0; k < kN; ++k) v[i + k] = f[k];
-  }
-  const float inv = p.inv_temp ? fmaxf(p.inv_temp[row], 0.f) : 1.f;   // (a NaN: 0)
-  const bool greedy = inv == INFINITY;
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kE; ++i) m = fmaxf(m, v[i]);   // (a NaN is passed over)
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red_sm[0][warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_sm[0][w]);
-  float sum = 0.f;
-  if (!greedy) {
-    // Values of +inf share the row; a CTA without a value above -inf has none.
-    const bool top = m == INFINITY;
-    const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      v[i] = exp_of(top ? (v[i] == INFINITY ? 0.f : -INFINITY) : (v[i] - ref) * inv);
-      sum += v[i];
+  };
+  auto ahead = [&](int row) {
+    if (threadIdx.x == 0 && row < p.rows && end > begin) {
+      // Whole 16-byte pieces of the CTA's share.
+      const uintptr_t a = (reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + row * p.x_stride + begin) + 15) & ~uintptr_t(15);
+      const uintptr_t b = reinterpret_cast<uintptr_t>(static_cast<const T*>(p.x) + row * p.x_stride + end) & ~uintptr_t(15);
+      if (b > a) bulk_prefetch_l2(reinterpret_cast<const void*>(a), (uint32_t)(b - a));
     }
-  }
+  };
+  int row = blockIdx.x / p.ctas;
+  fetch(row);
+  ahead(row + stride);
+  for (uint32_t n = 0; row < p.rows; row += stride, ++n) {
+    // (The place of row n is written again for row n + 2 by warps that have every warp's numbers of row n + 1, which
+    // each sends when it has read those of row n.)
+    const uint32_t turn = n & 1u;
+    bool got = true;
+    if (kVec && part_bytes > 0) got = wait_phase(&loaded[warp], n & 1u);
+    const T* const src = static_cast<const T*>(p.x) + row * p.x_stride + first;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) red_sm[1][warp] = sum;
-  __syncthreads();
-  sum = 0.f;
+    for (int i = 0; i < kE; i += kN) {
+      float f[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (place(i) < left) {
+        if (kVec) Ty::load4(part + kN * lane + place(i), f);
+        else f[0] = Ty::load(src + place(i));
+      }
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sum += red_sm[1][w];
-  cluster_wait();
-  if ((int)threadIdx.x < p.ctas) st_cluster_v2f(cluster_map(smem_addr(&peers_sm[rank]), threadIdx.x), m, sum);
-  cluster_arrive();
-  cluster_wait();
-  float M = -INFINITY;
-  for (int c = 0; c < p.ctas; ++c) M = fmaxf(M, peers_sm[c].x);
-  float factor = 0.f;
-  int best = p.vocab;
-  if (!greedy) {
-    auto weight = [&](float x) { return x == M ? 1.f : exp_of((x - M) * inv); };
-    float S = 0.f;
-    for (int c = 0; c < p.ctas; ++c) S = fmaf(peers_sm[c].y, weight(peers_sm[c].x), S);
-    factor = S > 0.f ? __fdiv_rn(weight(m), S) : 0.f;
-  } else {
-    // The first of the largest values, in the order of the row.
-    int at = p.vocab;
-    if (M > -INFINITY) {
+      for (int k = 0; k < kN; ++k) v[i + k] = f[k];
+    }
+    if (kVec) {
+      // (The copy's writes are the asynchronous proxy's: they come after the lanes' reads.)
+      fence_async_shared();
+      __syncwarp();
+      fetch(row + stride);
+    }
+    ahead(row + 2 * stride);
+    const float inv = p.inv_temp ? fmaxf(p.inv_temp[row], 0.f) : 1.f;   // (a NaN: 0)
+    const bool greedy = inv == INFINITY;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) m = fmaxf(m, v[i]);   // (a NaN is passed over)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float second;
+    if (greedy) {
+      int at = p.vocab;
 #pragma unroll
       for (int i = kE - 1; i >= 0; --i)
-        if (v[i] == M) at = (int)first + place(i);
-    }
-    at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == 0) best_sm[warp] = at;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) best = min(best, best_sm[w]);
-    if ((int)threadIdx.x < p.ctas) st_cluster_v2f(cluster_map(smem_addr(&first_sm[rank]), threadIdx.x), __int_as_float(best), 0.f);
-    cluster_arrive();
-    cluster_wait();
-    for (int c = 0; c < p.ctas; ++c) best = min(best, __float_as_int(first_sm[c].x));
-  }
-#pragma unroll
-  for (int i = 0; i < kE; i += kN) {
-    const int at = (int)first + place(i);
-    float f[4];
-#pragma unroll
-    for (int k = 0; k < kN; ++k) f[k] = greedy ? (at + k == best ? 1.f : 0.f) : v[i + k] * factor;
-    if (kVec && place(i) + kN <= left) {
-      *reinterpret_cast<float4*>(dst + first + place(i)) = make_float4(f[0], f[1], f[2], f[3]);
+        if (v[i] == m) at = min(at, (int)first + place(i));
+      second = __int_as_float(m == -INFINITY ? p.vocab : __reduce_min_sync(0xffffffffu, at));
     } else {
+      if (m == INFINITY) {
+        // Values of +inf share the row.
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
-        if (place(i) + k < left) dst[first + place(i) + k] = f[k];
+        for (int i = 0; i < kE; ++i) v[i] = v[i] == INFINITY ? 0.f : -INFINITY;
+      }
+      // The product with log2 e is one factor with 1 / T.
+      const float ref = fabsf(m) == INFINITY ? 0.f : m, k2 = inv * 1.44269504f;
+      const uint64_t ref2 = pair(-ref, -ref), k22 = pair(k2, k2);
+      uint64_t sum2[2] = {0, 0};   // (0, 0)
+#pragma unroll
+      for (int i = 0; i < kE; i += 2) {
+        float a, b;
+        unpair(mul2(add2(pair(v[i], v[i + 1]), ref2), k22), a, b);
+        v[i] = ex2(a);
+        v[i + 1] = ex2(b);
+        sum2[(i >> 1) & 1] = add2(sum2[(i >> 1) & 1], pair(v[i], v[i + 1]));
+      }
+      auto total = [&]() {
+        float a, b;
+        unpair(add2(sum2[0], sum2[1]), a, b);
+        a += b;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        return a;
+      };
+      second = total();
+      if (second != second) {
+        // Of logits that are NaN, or masked ones times 0: no weight.
+        sum2[0] = sum2[1] = 0;
+#pragma unroll
+        for (int i = 0; i < kE; i += 2) {
+          v[i] = v[i] != v[i] ? 0.f : v[i];
+          v[i + 1] = v[i + 1] != v[i + 1] ? 0.f : v[i + 1];
+          sum2[0] = add2(sum2[0], pair(v[i], v[i + 1]));
+        }
+        second = total();
+      }
+    }
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[turn], (uint32_t)(p.ctas * kWarps * sizeof(float2)));
+    if (lane < p.ctas)
+      st_async_v2f(cluster_map(smem_addr(&peers_sm[turn][rank * kWarps + warp]), lane), m, second, cluster_map(smem_addr(&full[turn]), lane));
+    got = wait_phase(&full[turn], (n >> 1) & 1u) && got;
+    const float2* const peers = peers_sm[turn];
+    float M = -INFINITY;
+    for (int c = lane; c < p.ctas * kWarps; c += 32) M = fmaxf(M, peers[c].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float factor = 0.f;
+    int best = p.vocab;
+    if (greedy) {
+      for (int c = lane; c < p.ctas * kWarps; c += 32)
+        if (peers[c].x == M) best = min(best, __float_as_int(peers[c].y));
+      best = __reduce_min_sync(0xffffffffu, best);
+    } else {
+      const float k2 = inv * 1.44269504f;
+      auto weight = [&](float x) { return x == M ? 1.f : ex2(fmaxf((x - M) * k2, -200.f)); };
+      float S = 0.f;
+      for (int c = lane; c < p.ctas * kWarps; c += 32) S = fmaf(peers[c].y, weight(peers[c].x), S);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+      factor = S > 0.f ? __fdiv_rn(weight(m), S) : 0.f;
+      if (!got) factor = NAN;
+    }
+    float* const dst = p.out + row * p.out_stride;
+    if (greedy) {
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] = (int)first + place(i) == best ? 1.f : 0.f;
+      factor = 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kE; i += kN) {
+      if (place(i) < left) {
+        float* const to = dst + first + place(i);
+        if (kVec) *reinterpret_cast<float4*>(to) = make_float4(v[i] * factor, v[i + 1] * factor, v[i + 2] * factor, v[i + 3] * factor);
+        else *to = v[i] * factor;
+      }
     }
   }
 }
@@ -199,7 +269,6 @@ constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMinSegment = 512;
 constexpr int kCtasPerSm = 4;
-constexpr float kUnits = 17592186044416.f;   // 2^44
 
 struct VerifyParams {
   const void *p, *q;
@@ -213,7 +282,22 @@ struct VerifyParams {
   long long* sums;      // [seqs][ctas * kVWarps]
 };
 
-__device__ __forceinline__ long long units(float x) { return __float2ll_rn(__saturatef(x) * kUnits); }   // (a NaN: 0)
+// x, taken inside [0, 1] (a NaN: 0), in units of 2^-44 as two whole numbers, hi 2^23 + lo: the last bits of sums with
+// constants whose own last bit is 2^-21 and 2^-44.  (Two of the conversions to 64 bits a value set the pace before: 64 rows of
+// 131072 42 us.)  The constants' bits are still in, and leave in the difference of two values.
+struct Units {
+  int hi, lo;
+};
+constexpr float kHiStep = 6.f, kLoStep = 7.152557373046875e-07f;   // 1.5 * 2^2, 1.5 * 2^-21
+__device__ __forceinline__ Units units(float x) {
+  x = __saturatef(x);
+  const float hi = __fadd_rn(x, kHiStep);
+  const float lo = __fadd_rn(__fsub_rn(x, __fsub_rn(hi, kHiStep)), kLoStep);   // (the differences are exact)
+  return {__float_as_int(hi), __float_as_int(lo)};
+}
+__device__ __forceinline__ long long weight_of(Units a, Units b) {
+  return max((long long)(a.hi - b.hi) * (1 << 23) + (a.lo - b.lo), 0ll);
+}
 
 // What a row draws from.
 struct Draw {
@@ -283,34 +367,40 @@ __global__ void __launch_bounds__(kVThreads, kCtasPerSm) spec_verify_kernel(cons
   const T* const qrow = p.q && !draw.last ? static_cast<const T*>(p.q) + draw.row * p.q_stride : nullptr;
   const int none = draw.last || qrow ? -1 : draw.token;   // the token without weight
 
-  // The sum of the weights of [a, b) that this lane takes (`target`: of p alone).
+  // The sum of the weights of [a, b), a lane's share each (`target`: of p alone).  A token without weight is taken off by
+  // the lane that has it.
+  const Units zero = units(0.f);
+  auto weight_at = [&](int i, bool target) {
+    const bool diff = qrow && !target;
+    return !target && i == none ? 0 : weight_of(units(Ty::load(prow + i)), diff ? units(Ty::load(qrow + i)) : zero);
+  };
   auto weigh = [&](int a, int b, bool target) {
     long long s = 0;
-    const bool diff = qrow && !target;
-    const int skip = target ? -1 : none;
     if (kVec) {
       int i = a + 4 * lane;
+      if (qrow && !target) {
 #pragma unroll 4
-      for (; i + 4 <= b; i += 128) {
-        float f[4], g[4] = {0.f, 0.f, 0.f, 0.f};
-        Ty::load4(prow + i, f);
-        if (diff) Ty::load4(qrow + i, g);
+        for (; i + 4 <= b; i += 128) {
+          float f[4], g[4];
+          Ty::load4(prow + i, f);
+          Ty::load4(qrow + i, g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const long long w = units(f[k]) - (diff ? units(g[k]) : 0);
-          s += i + k == skip ? 0 : max(w, 0ll);
+          for (int k = 0; k < 4; ++k) s += weight_of(units(f[k]), units(g[k]));
         }
+      } else {
+#pragma unroll 8
+        for (; i + 4 <= b; i += 128) {
+          float f[4];
+          Ty::load4(prow + i, f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s += weight_of(units(f[k]), zero);
+        }
+        if (!target && none >= a && none < i && ((none - a) >> 2) % 32 == lane) s -= weight_of(units(Ty::load(prow + none)), zero);
       }
-      for (int k = i; k < min(b, i + 4); ++k) {
-        const long long w = units(Ty::load(prow + k)) - (diff ? units(Ty::load(qrow + k)) : 0);
-        s += k == skip ? 0 : max(w, 0ll);
-      }
+      for (int k = i; k < min(b, i + 4); ++k) s += weight_at(k, target);
     } else {
 #pragma unroll 8
-      for (int i = a + lane; i < b; i += 32) {
-        const long long w = units(Ty::load(prow + i)) - (diff ? units(Ty::load(qrow + i)) : 0);
-        s += i == skip ? 0 : max(w, 0ll);
-      }
+      for (int i = a + lane; i < b; i += 32) s += weight_at(i, target);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -388,20 +478,15 @@ __global__ void __launch_bounds__(kVThreads, kCtasPerSm) spec_verify_kernel(cons
       segment_of(found_sm[0], a, b);
       const int share = (b - a + kVThreads - 1) / kVThreads;
       const int i0 = min(b, a + (int)threadIdx.x * share), i1 = min(b, i0 + share);
-      const bool diff = qrow && !target;
-      const int skip = target ? -1 : none;
-      auto weight = [&](int i) {
-        const long long w = units(Ty::load(prow + i)) - (diff ? units(Ty::load(qrow + i)) : 0);
-        return i == skip ? 0 : max(w, 0ll);
-      };
       mine = 0;
-      for (int i = i0; i < i1; ++i) mine += weight(i);
+#pragma unroll 8
+      for (int i = i0; i < i1; ++i) mine += weight_at(i, target);
       const long long ahead = scan(mine, all);
       at = at_sm;
       if (at >= ahead && at < ahead + mine) {
         at -= ahead;
         int i = i0;
-        for (long long x; i + 1 < i1 && at >= (x = weight(i)); ++i) at -= x;
+        for (long long x; i + 1 < i1 && at >= (x = weight_at(i, target)); ++i) at -= x;
         found_sm[1] = i;
       }
       __syncthreads();
@@ -440,10 +525,11 @@ static int check_rows(const void* x, long long stride, int rows, int vocab, int 
 }
 
 template <typename P>
-static cudaError_t launch(void (*kernel)(const P), long long grid, int threads, int cluster, const P& p, cudaStream_t stream) {
+static cudaError_t launch(void (*kernel)(const P), long long grid, int threads, int cluster, int smem, const P& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -473,6 +559,43 @@ static Kernel<VerifyParams> verify_kernel(int dtype) {
                             : spec_verify_kernel<KV8_BF16, kVec>;
 }
 
+// Clusters of `ctas` CTAs that the current device holds at once.  (A cluster lies within one of its groups of SMs, so this is
+// less than the SMs' places over the size; asked once for each kernel, size and device.)
+static cudaError_t resident_clusters(Kernel<ProbsParams> kernel, int ctas, int smem, int* clusters) {
+  struct Entry {
+    const void* kernel;
+    int ctas, device, clusters;
+  };
+  static Entry table[512];
+  static int used = 0;
+  static std::mutex mu;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < used; ++i)
+    if (table[i].kernel == (const void*)kernel && table[i].ctas == ctas && table[i].device == device) {
+      *clusters = table[i].clusters;
+      return cudaSuccess;
+    }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  if (smem > 0 && (e = ensure_smem_attribute((const void*)kernel, smem)) != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(clusters, (const void*)kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*clusters < 1) *clusters = 1;
+  if (used < 512) table[used++] = Entry{(const void*)kernel, ctas, device, *clusters};
+  return cudaSuccess;
+}
+
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kMaxSeqs = 65535;
 // (For any number of sequences: a workspace may serve calls of different ones, whose counters are zero between calls.)
@@ -499,21 +622,28 @@ extern "C" int spec_probs(const void* logits, long long logits_stride, const flo
   if (rc == W8A8_OK) rc = spec::check_rows(out, out_stride, rows, vocab, 4);
   if (rc != W8A8_OK) return rc;
   if (!kv8_aligned(inv_temp, 4)) return W8A8_ERR_MISALIGNED;
-  // A row's CTAs: eight for few rows, so that every SM has some; else as few as hold it at 32 values a thread (64 for a
-  // vocabulary that eight would not hold).
-  const int sms = device_sm_count();
-  const bool wide = vocab > 8 * 32 * spec::kThreads;
-  int ctas = (vocab + (wide ? 64 : 32) * spec::kThreads - 1) / ((wide ? 64 : 32) * spec::kThreads);
-  while (ctas < 8 && (long long)rows * ctas < 2 * sms) ++ctas;
-  spec::ProbsParams p{logits, logits_stride, inv_temp, out, out_stride, vocab, ((vocab + ctas - 1) / ctas + 3) / 4 * 4, ctas};
-  const int each = (p.share + spec::kThreads - 1) / spec::kThreads;
-  const bool vec = spec::vectors(logits, logits_stride, size) && spec::vectors(out, out_stride, 4);
+  // A row's CTAs (1, 2, 4 or 8: other clusters leave more of the SMs' places empty): as few as hold it at 32 values a
+  // thread (64 for a vocabulary that eight would not hold), more while rows are few, so that every SM has some.
+  const int sms = device_sm_count(), most = (vocab > 8 * 32 * spec::kThreads ? 64 : 32) * spec::kThreads;
+  int ctas = 1;
+  while (ctas < spec::kMaxCluster && ((long long)ctas * most < vocab || (long long)rows * ctas < sms)) ctas *= 2;
+  spec::ProbsParams p{logits, logits_stride, inv_temp, out, out_stride, rows, vocab, ((vocab + ctas - 1) / ctas + 7) / 8 * 8, ctas};
+  const int each = (p.share + spec::kThreads - 1) / spec::kThreads, held = each <= 8 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : 64;
+  auto whole = [](const void* x, long long stride, int vocab, int size) {
+    return kv8_aligned(x, 16) && stride * size % 16 == 0 && vocab * size % 16 == 0;
+  };
+  const bool vec = whole(logits, logits_stride, vocab, size) && whole(out, out_stride, vocab, 4);
   spec::Kernel<spec::ProbsParams> k =
-      vec ? (each <= 8 ? spec::probs_kernel<8, true>(dtype) : each <= 16 ? spec::probs_kernel<16, true>(dtype)
-             : each <= 32 ? spec::probs_kernel<32, true>(dtype) : spec::probs_kernel<64, true>(dtype))
-          : (each <= 8 ? spec::probs_kernel<8, false>(dtype) : each <= 16 ? spec::probs_kernel<16, false>(dtype)
-             : each <= 32 ? spec::probs_kernel<32, false>(dtype) : spec::probs_kernel<64, false>(dtype));
-  const cudaError_t e = spec::launch<spec::ProbsParams>(k, (long long)rows * ctas, spec::kThreads, ctas, p, static_cast<cudaStream_t>(stream));
+      vec ? (held == 8 ? spec::probs_kernel<8, true>(dtype) : held == 16 ? spec::probs_kernel<16, true>(dtype)
+             : held == 32 ? spec::probs_kernel<32, true>(dtype) : spec::probs_kernel<64, true>(dtype))
+          : (held == 8 ? spec::probs_kernel<8, false>(dtype) : held == 16 ? spec::probs_kernel<16, false>(dtype)
+             : held == 32 ? spec::probs_kernel<32, false>(dtype) : spec::probs_kernel<64, false>(dtype));
+  const int smem = vec ? spec::kThreads * held * size : 0;
+  int clusters = 0;
+  cudaError_t e = spec::resident_clusters(k, ctas, smem, &clusters);
+  if (e != cudaSuccess) return record_cuda_error(e, "spec_probs");
+  const int grid = rows < clusters ? rows : clusters;
+  e = spec::launch<spec::ProbsParams>(k, (long long)grid * ctas, spec::kThreads, ctas, smem, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "spec_probs");
 }
 
@@ -552,6 +682,6 @@ extern "C" int spec_verify(const void* p, long long p_stride, const void* q, lon
   a.sums = reinterpret_cast<long long*>(w + kWsHeaderBytes + spec::kCounterBytes);
   const bool vec = spec::vectors(p, p_stride, size) && (!q || spec::vectors(q, q_stride, size));
   const cudaError_t e = spec::launch<spec::VerifyParams>(vec ? spec::verify_kernel<true>(dtype) : spec::verify_kernel<false>(dtype),
-                                                         (long long)seqs * ctas, spec::kVThreads, 0, a, static_cast<cudaStream_t>(stream));
+                                                         (long long)seqs * ctas, spec::kVThreads, 0, 0, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "spec_verify");
 }

@@ -310,3 +310,19 @@ def test_probabilities_in_place_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_probabilities_back_to_back():
+    # Launches that begin while the one before ends, several rows a cluster.
+    x = [torch.randn(160, 32768, device="cuda").to(torch.bfloat16) for _ in range(3)]
+    want = [lib8.spec_probs(t) for t in x]
+    outs = [torch.empty_like(w) for w in want]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        for i in range(12):
+            lib8.spec_probs(x[i % 3], out=outs[i % 3])
+    for _ in range(20):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, outs))
