@@ -133,6 +133,8 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
     }
   };
   int row = blockIdx.x / p.ctas;
+  auto factor_of = [&](int row) { return p.inv_temp && row < p.rows ? fmaxf(p.inv_temp[row], 0.f) : 1.f; };   // (a NaN: 0)
+  float next_inv = factor_of(row);
   fetch(row);
   ahead(row + stride);
   for (uint32_t n = 0; row < p.rows; row += stride, ++n) {
@@ -159,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
       fetch(row + stride);
     }
     ahead(row + 2 * stride);
-    const float inv = p.inv_temp ? fmaxf(p.inv_temp[row], 0.f) : 1.f;   // (a NaN: 0)
+    const float inv = next_inv;
+    next_inv = factor_of(row + stride);
     const bool greedy = inv == INFINITY;
     float m = -INFINITY;
 #pragma unroll
@@ -216,33 +219,38 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
     if (lane < p.ctas)
       st_async_v2f(cluster_map(smem_addr(&peers_sm[turn][rank * kWarps + warp]), lane), m, second, cluster_map(smem_addr(&full[turn]), lane));
     got = wait_phase(&full[turn], (n >> 1) & 1u) && got;
-    const float2* const peers = peers_sm[turn];
+    constexpr int kPeers = kMaxCluster * kWarps / 32;   // a lane's
+    float2 peers[kPeers];
     float M = -INFINITY;
-    for (int c = lane; c < p.ctas * kWarps; c += 32) M = fmaxf(M, peers[c].x);
+#pragma unroll
+    for (int c = 0; c < kPeers; ++c) {
+      peers[c] = make_float2(-INFINITY, greedy ? __int_as_float(p.vocab) : 0.f);
+      if (32 * c + lane < p.ctas * kWarps) peers[c] = peers_sm[turn][32 * c + lane];
+      M = fmaxf(M, peers[c].x);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float factor = 0.f;
+    float factor = 1.f;
     int best = p.vocab;
     if (greedy) {
-      for (int c = lane; c < p.ctas * kWarps; c += 32)
+#pragma unroll
+      for (int c = 0; c < kPeers; ++c)
         if (peers[c].x == M) best = min(best, __float_as_int(peers[c].y));
       best = __reduce_min_sync(0xffffffffu, best);
+#pragma unroll
+      for (int i = 0; i < kE; ++i) v[i] = (int)first + place(i) == best ? 1.f : 0.f;
     } else {
       const float k2 = inv * 1.44269504f;
       auto weight = [&](float x) { return x == M ? 1.f : ex2(fmaxf((x - M) * k2, -200.f)); };
       float S = 0.f;
-      for (int c = lane; c < p.ctas * kWarps; c += 32) S = fmaf(peers[c].y, weight(peers[c].x), S);
+#pragma unroll
+      for (int c = 0; c < kPeers; ++c) S = fmaf(peers[c].y, weight(peers[c].x), S);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
       factor = S > 0.f ? __fdiv_rn(weight(m), S) : 0.f;
-      if (!got) factor = NAN;
     }
+    if (!got) factor = NAN;
     float* const dst = p.out + row * p.out_stride;
-    if (greedy) {
-#pragma unroll
-      for (int i = 0; i < kE; ++i) v[i] = (int)first + place(i) == best ? 1.f : 0.f;
-      factor = 1.f;
-    }
 #pragma unroll
     for (int i = 0; i < kE; i += kN) {
       if (place(i) < left) {
