@@ -60,10 +60,16 @@ cudaError_t fill_params(Params& p, const kv8_cache_t* cache, const kv8_step_t* s
   p.group_counters = p.counters + (size_t)sms * 4;
   p.parts = reinterpret_cast<float*>(w + kWsHeaderBytes + counters_bytes(sms));
   p.seq0 = p.prefix = nullptr;
-  p.groups = p.by_group = 0, p.all_seqs = step->seqs;
+  p.groups = 0;
   p.rows32 = nullptr;
   p.items = nullptr;
+  p.sms = sms, p.tile_rows = p.block = 0;
+  p.prefix_fixed = p.prefix_unit = p.own_fixed = p.own_token = 0.f;
   return cudaSuccess;
+}
+
+cudaError_t launch_plain(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s) {
+  return f16 ? launch_rows<true, kPlain>(p, head_dim, sms, s) : launch_rows<false, kPlain>(p, head_dim, sms, s);
 }
 
 }  // namespace attn
@@ -97,6 +103,6 @@ extern "C" int kv8_attention(const kv8_cache_t* cache, const kv8_step_t* step, c
   // any number of rows.
   p.window = window < (1 << 30) ? window : 1 << 30, p.causal = (flags & KV8_FLAG_NOT_CAUSAL) ? 0 : 1;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  e = dtype == KV8_F16 ? attn::launch_rows<true, false>(p, D, sms, s) : attn::launch_rows<false, false>(p, D, sms, s);
+  e = attn::launch_plain(p, D, dtype == KV8_F16, sms, s);
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention");
 }

@@ -43,14 +43,20 @@ struct Params {
   uint32_t* counters;      // [CTA] arrivals at the item that crosses the end of its run, zero between calls
   uint32_t* group_counters;   // [CTA][2] arrivals at a group of parts, by its first part's place, zero between calls
   float* parts;            // [CTA][2] parts of split items
-  // Sequences that share prefixes (kv8_attention_shared; groups = 0: none do).
+  // Sequences that share prefixes (kPrefixes, kOwn).
   const int* seq0;         // [groups + 1] first sequence of each group
   const int* prefix;       // [groups] tokens that its sequences have in common
-  int groups, all_seqs;
-  int by_group;            // the "sequences" of this launch are the groups, over their prefixes
-  float* rows32;           // not NULL: rows go here instead of out and lse, unnormalised: [tokens][q_heads] of D sums, (m, l, r, -)
-  int4* items;             // by_group: where an item's parts lie (item_of): first CTA, parts, place in the first one, -
+  int groups;
+  float* rows32;           // [tokens][q_heads] of D sums, (m, l, r, -): rows go here, unnormalised
+  int4* items;             // kPrefixes: where an item's parts lie (item_of): first CTA, parts, place in the first one, -
+  int sms;
+  int tile_rows, block;    // rows of an item and tokens of a unit of kPrefixes' launch
+  float prefix_fixed, prefix_unit, own_fixed, own_token;   // what the two launches cost an SM, in ns (prefix_sms)
 };
+
+// What a launch does: sequences over all they see (kv8_attention); groups of sequences over their shared prefixes, as if
+// each group were one sequence that sees all of them; sequences over what is not shared.
+enum Mode { kPlain, kPrefixes, kOwn };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -73,22 +79,6 @@ struct Rows : Seq {
   int lo, table;
 };
 
-// The tokens of group g's shared prefix, in whole pages, and its first sequence; 0 where nothing is shared: a single
-// sequence, or a first one that does not hold the prefix.
-__device__ __forceinline__ int group_prefix(const Params& p, int g, int& first, int& last) {
-  first = __ldg(p.seq0 + g), last = __ldg(p.seq0 + g + 1);
-  if (first < 0 || last < first || last > p.all_seqs) {
-    atomicOr(p.status, W8A8_DEV_BAD_INDEX);
-    first = last = 0;
-    return 0;
-  }
-  const int whole = __ldg(p.prefix + g) & ~((1 << p.page_shift) - 1);
-  if (last - first < 2 || whole <= 0 || __ldg(p.step.kv_len + first) < whole ||
-      (long long)whole > (long long)p.step.table_width << p.page_shift)
-    return 0;
-  return whole;
-}
-
 // The group of sequence b (-1: of none).
 __device__ __forceinline__ int group_of(const Params& p, int b) {
   int lo = 0, n = p.groups;   // the last group that begins at or before b
@@ -100,14 +90,23 @@ __device__ __forceinline__ int group_of(const Params& p, int b) {
   return __ldg(p.seq0 + lo) <= b && b < __ldg(p.seq0 + lo + 1) ? lo : -1;
 }
 
-// Group g as a sequence: the rows of all its sequences over the shared prefix (no rows where nothing is shared).
+// Group g as a sequence: the rows of all its sequences over their shared prefix, in whole pages; `table`: its first
+// sequence.  No rows and no tokens where nothing is shared: a single sequence, or a first one that does not hold the
+// prefix.  (Two rounds of loads: what depends on the first is asked for at once, at indices held in range.)
 __device__ __forceinline__ void load_group(const Params& p, int g, Rows& s) {
-  int last;
-  s.lo = s.row0 = s.n = 0;
-  s.len = group_prefix(p, g, s.table, last);
-  if (s.len == 0) return;
-  const int r0 = __ldg(p.step.row0 + s.table), r1 = __ldg(p.step.row0 + last);
-  if (r0 >= 0 && r1 >= r0 && r1 <= p.step.tokens) s.row0 = r0, s.n = r1 - r0;
+  const int first = __ldg(p.seq0 + g), last = __ldg(p.seq0 + g + 1);
+  const int whole = __ldg(p.prefix + g) & ~((1 << p.page_shift) - 1);
+  const bool ok = first >= 0 && last >= first && last <= p.step.seqs;
+  const int f = ok ? min(first, p.step.seqs - 1) : 0;
+  const int len = __ldg(p.step.kv_len + f), r0 = __ldg(p.step.row0 + f), r1 = __ldg(p.step.row0 + (ok ? last : 0));
+  if (!ok) atomicOr(p.status, W8A8_DEV_BAD_INDEX);
+  s.lo = 0;
+  s.table = f;
+  const bool shared = ok && last - first >= 2 && whole > 0 && len >= whole && (long long)whole <= (long long)p.step.table_width << p.page_shift &&
+                      r0 >= 0 && r1 >= r0 && r1 <= p.step.tokens;
+  s.len = shared ? whole : 0;
+  s.row0 = shared ? r0 : 0;
+  s.n = shared ? r1 - r0 : 0;
 }
 
 // Tokens of sequence b that its group's launch covers, and that group: all of the shared prefix where every row of the
@@ -119,16 +118,23 @@ __device__ __forceinline__ int shared_tokens(const Params& p, int b, const Seq& 
 }
 
 // Reads "sequence" b of the launch.
+template <Mode kMode>
 __device__ __forceinline__ void load_rows(const Params& p, int b, Rows& s) {
-  if (p.by_group) return load_group(p, b, s);
+  if (kMode == kPrefixes) return load_group(p, b, s);
   s.lo = 0;
   s.table = b;
   load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
-  if (p.groups > 0) {
+  if (kMode == kOwn) {
     int g;
     Rows of;
     s.lo = shared_tokens(p, b, s, g, of);
   }
+}
+
+// Sequences of the launch.
+template <Mode kMode>
+__device__ __forceinline__ int count_of(const Params& p) {
+  return kMode == kPrefixes ? p.groups : p.step.seqs;
 }
 
 // The place of a row tile's entry in `items`: tiles of `rows` of the group's rows, which begin at row r0 of the step.
@@ -144,14 +150,13 @@ struct Span {
   int tiles, units, span, lo, hi;
 };
 
-template <typename L, bool kShared>
+template <typename L, Mode kMode>
 __device__ __forceinline__ Span load_span(const Params& p, int b) {
   Span x;
-  if (kShared) load_rows(p, b, x.s);
-  else load_seq(p.step, b, 1 << p.page_shift, false, p.status, x.s);
+  load_rows<kMode>(p, b, x.s);
   x.tiles = (int)quotient((long long)x.s.n * p.group + L::kRows - 1, L::kRows);
   x.hi = x.s.len;
-  x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : kShared ? x.s.lo : 0;
+  x.lo = p.window > 0 ? max(0, x.s.len - x.s.n - p.window + 1) & ~(kGranule - 1) : kMode == kOwn ? x.s.lo : 0;
   x.units = max(1, (x.hi - x.lo + L::kUnit - 1) / L::kUnit);   // one that sees nothing still writes its rows
   x.span = L::kLead + x.units;
   return x;
@@ -168,15 +173,71 @@ struct Runs {
   }
 };
 
-// The kernel of many query rows (kv8_attention_tc.cu); its share of the workspace.
-cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
-size_t many_parts_bytes(int head_dim, int sms);
-// Rows of one of its tiles for sequences of up to `rows` rows of a kv head.
-int many_tile_rows(int head_dim, long long rows);
+// The SMs that the groups' launch takes while the other takes the rest, worked out alike by every CTA of both (the whole
+// block takes part): prefixes cost the matrix products' chain of waits, own tokens HBM's bandwidth, so side by side
+// they finish sooner than one after the other.  The time of either falls with its SMs; the count is that of the
+// smallest maximum, or all of them (the other launch then follows) where that is sooner, and where own_fixed is below 0.
+// 0: nothing is shared.
+// scratch: shared memory, 24 bytes a warp, free again behind the block's next barrier.
+template <int kThreads>
+__device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
+  long long (*const sums_sm)[kThreads / 32] = static_cast<long long (*)[kThreads / 32]>(scratch);
+  uint32_t* const best_sm = reinterpret_cast<uint32_t*>(sums_sm + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long units = 0, own = 0;
+  for (int b = threadIdx.x; b < p.step.seqs; b += kThreads) own += max(0, __ldg(p.step.kv_len + b));
+  for (int g = threadIdx.x; g < p.groups; g += kThreads) {
+    Rows s;
+    load_group(p, g, s);
+    if (s.n > 0) {
+      units += ((long long)s.n * p.group + p.tile_rows - 1) / p.tile_rows * (3 + (s.len + p.block - 1) / p.block);
+      own -= (long long)s.len * (__ldg(p.seq0 + g + 1) - s.table);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    units += __shfl_xor_sync(0xffffffffu, units, o);
+    own += __shfl_xor_sync(0xffffffffu, own, o);
+  }
+  if (lane == 0) sums_sm[0][warp] = units, sums_sm[1][warp] = own;
+  __syncthreads();
+  units = own = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) units += sums_sm[0][w], own += sums_sm[1][w];
+  if (units == 0) return 0;
+  if (p.own_fixed < 0.f) return p.sms;
+  units *= p.kv_heads;
+  const float a = p.prefix_unit * (float)units, b = p.own_token * (float)max(own, 0ll) * (float)p.kv_heads;
+  uint32_t best = 0xffffffffu;
+  const int sms = min(p.sms, 255);
+  for (int n = threadIdx.x + 1; n <= sms; n += kThreads) {
+    const float ta = p.prefix_fixed + fmaxf(a / n, p.prefix_unit), tb = p.own_fixed + b / (n < sms ? sms - n : sms);
+    best = min(best, ((uint32_t)fminf(n < sms ? fmaxf(ta, tb) : ta + tb, 1.6e7f) << 8) | (uint32_t)n);
+  }
+  best = __reduce_min_sync(0xffffffffu, best);
+  if (lane == 0) best_sm[warp] = best;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) best = min(best, best_sm[w]);
+  return (int)(best & 255u) == sms ? p.sms : (int)(best & 255u);
+}
 
-// kv8_attention.cu: arguments that both entry points check and fill in alike.
+// SMs of the launch of the sequences' own tokens beside `n` of the other.
+__device__ __forceinline__ int own_sms(const Params& p, int n) { return n < p.sms ? p.sms - n : p.sms; }
+
+// The kernel of many query rows (kv8_attention_many.cuh): each mode's instances; its share of the workspace.
+cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
+cudaError_t launch_many_prefixes(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
+cudaError_t launch_many_own(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
+size_t many_parts_bytes(int head_dim, int sms);
+// Rows of one of its tiles for sequences of up to `rows` rows of a kv head; tokens of a unit.
+int many_tile_rows(int head_dim, long long rows);
+int many_block(int head_dim);
+
+// kv8_attention.cu: arguments that both entry points check and fill in alike, and kv8_attention's launch.
 int check_call(const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride, int q_heads, const void* out,
                long long out_stride, const float* lse, float scale, int dtype);
+cudaError_t launch_plain(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
 cudaError_t fill_params(Params& p, const kv8_cache_t* cache, const kv8_step_t* step, const void* q, long long q_stride, int q_heads,
                         void* out, long long out_stride, float* lse, float scale, void* ws, int sms);
 

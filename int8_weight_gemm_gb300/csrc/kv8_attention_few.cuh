@@ -98,13 +98,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return t;
 }
 
-// Four output values at d of one joined query row, and with the first of them the row's lse.  (kShared: what
-// kv8_attention_shared adds is in instances of its own, as it costs registers.)
-template <bool kF16, bool kShared>
+// Four output values at d of one joined query row, and with the first of them the row's lse.  (kOwn: in instances of its own,
+// as it costs registers.)
+template <bool kF16, Mode kMode>
 __device__ __forceinline__ void store_row(const Params& p, int row0, int ri, int h, int d, int D, float4 acc, float M, float lt,
                                           float Rf) {
   const int orow = row0 + ri / p.group, head = h * p.group + ri % p.group;
-  if (kShared) {
+  if (kMode == kOwn) {
     float* const dst = p.rows32 + ((size_t)orow * p.q_heads + head) * (D + 4);
     *reinterpret_cast<float4*>(dst + d) = acc;
     if (d == 0) *reinterpret_cast<float4*>(dst + D) = make_float4(M, lt, Rf, 0.f);
@@ -116,7 +116,7 @@ __device__ __forceinline__ void store_row(const Params& p, int row0, int ri, int
   if (p.lse && d == 0) p.lse[(size_t)orow * p.q_heads + head] = lt == 0.f ? -INFINITY : (M + lg2(lt)) * 0.69314718056f;
 }
 
-template <bool kF16, int D, int NT, bool kShared>
+template <bool kF16, int D, int NT, Mode kMode>
 __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     kv8_attention_kernel(const __grid_constant__ Params p) {
   using L = Layout<D, NT>;
@@ -154,7 +154,11 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     }
   }
   pdl_trigger();
-  pdl_wait();
+  // (kOwn starts beside the groups' launch, every CTA of which has seen the work before it complete when this one
+  // begins; it waits for that launch at its end.)
+  if (kMode != kOwn) pdl_wait();
+  // CTAs that take part.
+  const int room = kMode == kOwn ? min((int)gridDim.x, own_sms(p, prefix_sms<kThreads>(p, ring)) * L::kCtas) : (int)gridDim.x;
 
   // ---------------------------------------------------------------- this CTA's run of units
   const int per = (p.step.seqs + kThreads - 1) / kThreads;   // sequences a thread scans
@@ -163,7 +167,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   int items = 0, longest = 0;
   Span x;   // the last sequence that this thread looked at
   for (int b = s0; b < s1; ++b) {
-    x = load_span<L, kShared>(p, b);
+    x = load_span<L, kMode>(p, b);
     mine += (long long)x.tiles * x.span;
     items = (int)min((long long)items + (long long)x.tiles * p.kv_heads, 1LL << 20);   // (more than any grid: all alike)
     if (x.tiles > 0) longest = max(longest, x.units);
@@ -191,13 +195,16 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   }
   // Few short items: one to a CTA, at the length of the longest, and no parts to join.
   int even = 0;
-  if (longest <= L::kWhole && all_items <= (int)gridDim.x) {
+  if (longest <= L::kWhole && all_items <= room) {
     even = L::kLead + longest;
     before = (long long)before_items * even, mine = (long long)items * even, U = (long long)all_items * even;
     x.span = even;
   }
-  const int ctas = even ? all_items : (int)min((long long)gridDim.x, U);
-  if ((int)blockIdx.x >= ctas) return;
+  const int ctas = even ? all_items : (int)min((long long)room, U);
+  if ((int)blockIdx.x >= ctas) {
+    if (kMode == kOwn && blockIdx.x == 0) pdl_wait();
+    return;
+  }
   if (threadIdx.x == 0) even_sm = even;
   const Runs runs(U, ctas);
   const long long u0 = runs.begin(blockIdx.x), u1 = runs.begin(blockIdx.x + 1);
@@ -206,7 +213,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     long long at = before;
     int b = s0;
     for (; per > 1; ++b) {
-      x = load_span<L, kShared>(p, b);
+      x = load_span<L, kMode>(p, b);
       if (even) x.span = even;
       const long long n = (long long)x.tiles * x.span * p.kv_heads;
       if (u0 < at + n) break;
@@ -227,7 +234,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     // ---------------------------------------------------------------- the next segment: one item's part of the run
     while (u >= seq_u0 + (long long)x.tiles * x.span * p.kv_heads) {
       seq_u0 += (long long)x.tiles * x.span * p.kv_heads;
-      x = load_span<L, kShared>(p, ++b);
+      x = load_span<L, kMode>(p, ++b);
       if (even_sm) x.span = even_sm;
     }
     const int item = (int)quotient(u - seq_u0, x.span);
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     const int granules = (T1 - T0 + kGranule - 1) / kGranule;
     const int mine_n = granules > warp ? (granules - warp + kWarps - 1) / kWarps : 0;
     const int rows_left = x.s.n * p.group - tile * L::kRows;   // rows of the tile that exist
-    const int* const table = p.step.page_table + (size_t)(kShared ? x.s.table : b) * p.step.table_width;
+    const int* const table = p.step.page_table + (size_t)(kMode == kOwn ? x.s.table : b) * p.step.table_width;
 
     // The page, scales and cache row of this warp's granule j, held by lane j % 32 (batches of 32,
     // two in registers: the ring runs ahead of the use).
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
         acc.x = fmaf(v.x, a, acc.x), acc.y = fmaf(v.y, a, acc.y), acc.z = fmaf(v.z, a, acc.z), acc.w = fmaf(v.w, a, acc.w);
       }
       if (whole) {
-        store_row<kF16, kShared>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc, M, lt, Rf);
+        store_row<kF16, kMode>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc, M, lt, Rf);
       } else {
         *reinterpret_cast<float4*>(part + row * D + d) = acc;
         if (d == 0) *reinterpret_cast<float4*>(part + L::kRows * D + row * 4) = make_float4(M, lt, Rf, 0.f);
@@ -721,7 +728,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
             if (at >= rows * kVec) continue;
             const int row = at / kVec, d = 4 * (at % kVec);
             if (top) {
-              store_row<kF16, kShared>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc[y], M[y], lt[y], Rf[y]);
+              store_row<kF16, kMode>(p, x.s.row0, tile * L::kRows + row, h, d, D, acc[y], M[y], lt[y], Rf[y]);
             } else {
               // The group's sums take the place of its first part's; its statistics once every thread has read them.
               *(reinterpret_cast<float4*>(part_of(base)) + at) = acc[y];
@@ -744,12 +751,13 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
       __syncthreads();
     }
   }
+  if (kMode == kOwn && blockIdx.x == 0) pdl_wait();   // (the grid is not complete before it)
 }
 
-template <bool kF16, int D, int NT, bool kShared>
+template <bool kF16, int D, int NT, Mode kMode>
 static cudaError_t launch_few(const Params& p, int sms, cudaStream_t stream) {
   using L = Layout<D, NT>;
-  auto kern = kv8_attention_kernel<kF16, D, NT, kShared>;
+  auto kern = kv8_attention_kernel<kF16, D, NT, kMode>;
   cudaError_t e = ensure_smem_attribute((const void*)kern, L::kSmem);
   if (e != cudaSuccess) return e;
   // No more CTAs than units there can be (lengths are known to the device alone).
@@ -782,21 +790,21 @@ static bool takes_many(const Params& p, int head_dim, long long rows) {
 }
 
 // The narrowest variant that holds a sequence's rows in one tile, else the widest.
-template <bool kF16, bool kShared>
+template <bool kF16, Mode kMode>
 static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
   const long long rows = (long long)p.step.max_tokens * p.group;
-  if (takes_many(p, head_dim, rows)) return launch_many(p, head_dim, kF16, sms, s);
+  if (takes_many(p, head_dim, rows)) return kMode == kOwn ? launch_many_own(p, head_dim, kF16, sms, s) : launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
-    return rows <= 8    ? launch_few<kF16, 64, 1, kShared>(p, sms, s)
-           : rows <= 16 ? launch_few<kF16, 64, 2, kShared>(p, sms, s)
-           : rows <= 24 ? launch_few<kF16, 64, 3, kShared>(p, sms, s)
-                        : launch_few<kF16, 64, 4, kShared>(p, sms, s);
+    return rows <= 8    ? launch_few<kF16, 64, 1, kMode>(p, sms, s)
+           : rows <= 16 ? launch_few<kF16, 64, 2, kMode>(p, sms, s)
+           : rows <= 24 ? launch_few<kF16, 64, 3, kMode>(p, sms, s)
+                        : launch_few<kF16, 64, 4, kMode>(p, sms, s);
   if (head_dim == 128)
-    return rows <= 8    ? launch_few<kF16, 128, 1, kShared>(p, sms, s)
-           : rows <= 16 ? launch_few<kF16, 128, 2, kShared>(p, sms, s)
-           : rows <= 24 ? launch_few<kF16, 128, 3, kShared>(p, sms, s)
-                        : launch_few<kF16, 128, 4, kShared>(p, sms, s);
-  return rows <= 8 ? launch_few<kF16, 256, 1, kShared>(p, sms, s) : launch_few<kF16, 256, 2, kShared>(p, sms, s);
+    return rows <= 8    ? launch_few<kF16, 128, 1, kMode>(p, sms, s)
+           : rows <= 16 ? launch_few<kF16, 128, 2, kMode>(p, sms, s)
+           : rows <= 24 ? launch_few<kF16, 128, 3, kMode>(p, sms, s)
+                        : launch_few<kF16, 128, 4, kMode>(p, sms, s);
+  return rows <= 8 ? launch_few<kF16, 256, 1, kMode>(p, sms, s) : launch_few<kF16, 256, 2, kMode>(p, sms, s);
 }
 
 }  // namespace attn

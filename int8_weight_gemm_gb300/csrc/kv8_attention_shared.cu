@@ -18,6 +18,7 @@ namespace w8a8 {
 namespace attn {
 
 constexpr int kJoinThreads = 256;
+constexpr long long kSmallRead = 24ll << 20;
 
 struct JoinParams {
   Params p;
@@ -27,17 +28,14 @@ struct JoinParams {
   int tile_shift;        // rows of an item: 2^tile_shift
 };
 
-// A warp for each row and query head.
+// A CTA for a row and some of its query heads: a warp for each, in turns where there are many rows.
 template <bool kF16, int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ JoinParams j) {
   const Params& p = j.p;
   pdl_trigger();
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x, head = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  if (head >= p.q_heads) return;
-  const size_t at = (size_t)row * p.q_heads + head;
-  // The row's sequence: the last that begins at or before it.
+  const int lane = threadIdx.x & 31, row = blockIdx.x;
+  // The row's sequence (the last that begins at or before it) and group.  None of this is written by the launches that
+  // this one waits for.
   int b = 0;
   for (int n = p.step.seqs; n > 1;) {
     const int step = (n + 31) / 32;
@@ -49,100 +47,107 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   }
   Seq s;
   load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  int g;
+  Rows of;
+  const bool shared = shared_tokens(p, b, s, g, of) > 0;
+  pdl_wait();
   if (row < s.row0 || row >= s.row0 + s.n) return;   // behind the last sequence
-  // Values of the row: four a lane (D = 64: by half a warp, the other half takes every other part; 256: two times four).
+  // Values of a head: four a lane (D = 64: by half a warp, the other half takes every other part; 256: two times four).
   constexpr int kV = D == 256 ? 2 : 1, kAt = D == 64 ? 2 : 1;
   const int d = 4 * (lane & (D == 64 ? 15 : 31));
-  const float* const own = j.own + at * (D + 4);
-  const float4 t0 = __ldcg(reinterpret_cast<const float4*>(own + D));
-  float M = t0.x, R = t0.z, l = t0.y;
-  float4 acc[kV];
-#pragma unroll
-  for (int v = 0; v < kV; ++v) acc[v] = __ldcg(reinterpret_cast<const float4*>(own + d + 128 * v));
-
-  int g, parts = 0;
-  Rows of;
-  int4 item = make_int4(0, 0, 0, 0);
-  int within = 0;
-  if (shared_tokens(p, b, s, g, of) > 0) {
-    const long long ri = (long long)(row - of.row0) * p.group + head % p.group;
-    const int tile = (int)(ri >> j.tile_shift);
-    within = (int)ri & ((1 << j.tile_shift) - 1);
-    item = __ldcg(p.items + item_of(p, g, of.row0, 1 << j.tile_shift, tile, head / p.group));
-    parts = item.y;
-  }
   const size_t part_floats = (size_t)(D + 4) << j.tile_shift;
-  auto sums_of = [&](int i) {
-    return parts == 1 ? j.whole + at * (D + 4) : j.parts + ((size_t)(item.x + i) * 2 + (i == 0 ? item.z : 0)) * part_floats + (size_t)within * D;
-  };
-  auto stats_of = [&](int i) {
-    return __ldcg(reinterpret_cast<const float4*>(parts == 1 ? sums_of(0) + D : sums_of(i) - (size_t)within * D + ((size_t)D << j.tile_shift) + within * 4));
-  };
-  if (parts > 0) {
-    // References first: a lane for each part.
-    float4 t = make_float4(kFloor, 0.f, kFloor, 0.f);
-    if (lane < parts) t = stats_of(lane);
-    float mm = t.x, rm = t.z, lt = t.y;
-    for (int i = lane + 32; i < parts; i += 32) {
-      const float4 x = stats_of(i);
-      const float mn = fmaxf(mm, x.x);
-      lt = lt * ex2(mm - mn) + x.y * ex2(x.x - mn);
-      mm = mn;
-      rm = fmaxf(rm, x.z);
+  for (int head = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); head < p.q_heads; head += gridDim.y * (kJoinThreads / 32)) {
+    const size_t at = (size_t)row * p.q_heads + head;
+    int4 item = make_int4(0, 0, 0, 0);   // first CTA, parts, place in the first
+    int within = 0;
+    if (shared) {
+      const long long ri = (long long)(row - of.row0) * p.group + head % p.group;
+      within = (int)ri & ((1 << j.tile_shift) - 1);
+      item = p.items[item_of(p, g, of.row0, 1 << j.tile_shift, (int)(ri >> j.tile_shift), head / p.group)];
     }
-    float mn = fmaxf(M, mm), rn = fmaxf(R, rm);
+    const int parts = item.y;
+    const float* const own = j.own + at * (D + 4);
+    const float4 t0 = *reinterpret_cast<const float4*>(own + D);
+    float M = t0.x, R = t0.z, l = t0.y;
+    float4 acc[kV];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      rn = fmaxf(rn, __shfl_xor_sync(0xffffffffu, rn, o));
-    }
-    lt *= ex2(mm - mn);
+    for (int v = 0; v < kV; ++v) acc[v] = *reinterpret_cast<const float4*>(own + d + 128 * v);
+    // (An item that was not cut: its rows as they are; a part: [D / 4][rows] of four columns, then the rows' statistics.
+    // Neighbouring heads' columns share a line, so these loads stay in the L1 cache.)
+    auto part_of = [&](int i) { return j.parts + ((size_t)(item.x + i) * 2 + (i == 0 ? item.z : 0)) * part_floats; };
+    auto sums_of = [&](int i, int d) {
+      return *reinterpret_cast<const float4*>(parts == 1 ? j.whole + at * (D + 4) + d : part_of(i) + ((size_t)(d >> 2) << j.tile_shift) * 4 + within * 4);
+    };
+    auto stats_of = [&](int i) {
+      return *reinterpret_cast<const float4*>(parts == 1 ? j.whole + at * (D + 4) + D : part_of(i) + ((size_t)D << j.tile_shift) + within * 4);
+    };
+    if (parts > 0) {
+      // References first: a lane for each part.
+      float4 t = make_float4(kFloor, 0.f, kFloor, 0.f);
+      if (lane < parts) t = stats_of(lane);
+      float mm = t.x, rm = t.z, lt = t.y;
+      for (int i = lane + 32; i < parts; i += 32) {
+        const float4 x = stats_of(i);
+        const float mn = fmaxf(mm, x.x);
+        lt = lt * ex2(mm - mn) + x.y * ex2(x.x - mn);
+        mm = mn;
+        rm = fmaxf(rm, x.z);
+      }
+      float mn = fmaxf(M, mm), rn = fmaxf(R, rm);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
-    l = fmaf(l, ex2(M - mn), lt);
-    const float a0 = D == 64 && lane >= 16 ? 0.f : ex2(R - rn);
+      for (int o = 16; o > 0; o >>= 1) {
+        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+        rn = fmaxf(rn, __shfl_xor_sync(0xffffffffu, rn, o));
+      }
+      lt *= ex2(mm - mn);
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v].x *= a0, acc[v].y *= a0, acc[v].z *= a0, acc[v].w *= a0;
-    M = mn;
-    R = rn;
-    const int odd = D == 64 ? lane >> 4 : 0;
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-      float a = 0.f;
-      if (i0 + lane < parts) a = ex2((i0 ? stats_of(i0 + lane).z : t.z) - R);
-      const int n = min(32, parts - i0);
+      for (int o = 16; o > 0; o >>= 1) lt += __shfl_xor_sync(0xffffffffu, lt, o);
+      l = fmaf(l, ex2(M - mn), lt);
+      const float a0 = D == 64 && lane >= 16 ? 0.f : ex2(R - rn);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[v].x *= a0, acc[v].y *= a0, acc[v].z *= a0, acc[v].w *= a0;
+      M = mn;
+      R = rn;
+      const int odd = D == 64 ? lane >> 4 : 0;
+      for (int i0 = 0; i0 < parts; i0 += 32) {
+        float a = 0.f;
+        if (i0 + lane < parts) a = ex2((i0 ? stats_of(i0 + lane).z : t.z) - R);
+        const int n = min(32, parts - i0);
 #pragma unroll 4
-      for (int i = 0; i < n; i += kAt) {
-        const float f = __shfl_sync(0xffffffffu, a, (i + odd) & 31);
-        if (i + odd < n) {
-          const float* const src = sums_of(i0 + i + odd) + d;
+        for (int i = 0; i < n; i += kAt) {
+          const float f = __shfl_sync(0xffffffffu, a, (i + odd) & 31);
+          if (i + odd < n) {
 #pragma unroll
-          for (int v = 0; v < kV; ++v) {
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(src + 128 * v));
-            acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
+            for (int v = 0; v < kV; ++v) {
+              const float4 x = sums_of(i0 + i + odd, d + 128 * v);
+              acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
+            }
           }
         }
       }
+      if (D == 64) {
+        acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
+        acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
+      }
     }
-    if (D == 64) {
-      acc[0].x += __shfl_xor_sync(0xffffffffu, acc[0].x, 16), acc[0].y += __shfl_xor_sync(0xffffffffu, acc[0].y, 16);
-      acc[0].z += __shfl_xor_sync(0xffffffffu, acc[0].z, 16), acc[0].w += __shfl_xor_sync(0xffffffffu, acc[0].w, 16);
-    }
-  }
-  const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(R - M);
-  if (D > 64 || lane < 16) {
-    uint16_t* const dst = p.out + row * p.out_stride + head * D + d;
+    const float z = l == 0.f ? 0.f : __fdividef(1.f, l) * ex2(R - M);
+    if (D > 64 || lane < 16) {
+      uint16_t* const dst = p.out + row * p.out_stride + head * D + d;
 #pragma unroll
-    for (int v = 0; v < kV; ++v)
-      *reinterpret_cast<uint2*>(dst + 128 * v) =
-          make_uint2(pack2<kF16>(acc[v].x * z, acc[v].y * z), pack2<kF16>(acc[v].z * z, acc[v].w * z));
+      for (int v = 0; v < kV; ++v)
+        *reinterpret_cast<uint2*>(dst + 128 * v) =
+            make_uint2(pack2<kF16>(acc[v].x * z, acc[v].y * z), pack2<kF16>(acc[v].z * z, acc[v].w * z));
+    }
+    if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + lg2(l)) * 0.69314718056f;
   }
-  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (M + lg2(l)) * 0.69314718056f;
 }
 
 template <bool kF16, int D>
 static cudaError_t launch_join(const JoinParams& j, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)j.p.step.tokens, (unsigned)((j.p.q_heads + kJoinThreads / 32 - 1) / (kJoinThreads / 32)));
+  // Enough CTAs for every SM's places; beyond that a row's lookups serve several heads.
+  const int most = (j.p.q_heads + kJoinThreads / 32 - 1) / (kJoinThreads / 32), want = (4 * j.p.sms + j.p.step.tokens - 1) / j.p.step.tokens;
+  cfg.gridDim = dim3((unsigned)j.p.step.tokens, (unsigned)(want < most ? want : most));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -157,6 +162,16 @@ static cudaError_t launch_join(const JoinParams& j, cudaStream_t stream) {
 template <bool kF16>
 static cudaError_t launch_join_of(const JoinParams& j, int head_dim, cudaStream_t s) {
   return head_dim == 64 ? launch_join<kF16, 64>(j, s) : head_dim == 128 ? launch_join<kF16, 128>(j, s) : launch_join<kF16, 256>(j, s);
+}
+
+// What the two launches cost an SM, in ns, for prefix_sms: measured.  (Many rows on either side: both are bound by
+// their products, and one follows the other.)
+static void set_costs(Params& p, int head_dim, bool many) {
+  p.prefix_fixed = 12000.f;
+  p.prefix_unit = head_dim == 256 ? 1900.f : p.tile_rows == 256 ? 3000.f : 1700.f;
+  p.own_fixed = many ? -1.f : 9000.f;
+  const long long rows = (long long)p.step.max_tokens * p.group;
+  p.own_token = (head_dim == 256 ? 2.f : 1.f) * (rows <= 8 ? 7.5f : rows <= 16 ? 9.f : 25.f);
 }
 
 // The workspace behind that of kv8_attention: parts of cut prefixes, their places, and two buffers of fp32 rows.
@@ -206,28 +221,35 @@ extern "C" int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* 
   attn::JoinParams j;
   cudaError_t e = attn::fill_params(j.p, cache, step, q, q_stride, q_heads, out, out_stride, lse, scale, ws, sms);
   if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
+  // A step whose whole table is a small read (a few us of HBM's rate) is read as it is: the three launches take longer.
+  const long long bytes = 2ll * step->seqs * step->table_width * cache->page_tokens * cache->kv_heads * D;
+  if (bytes <= attn::kSmallRead && !attn::takes_many(j.p, D, (long long)step->max_tokens * j.p.group)) {
+    e = attn::launch_plain(j.p, D, f16, sms, s);
+    return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention_shared");
+  }
   j.p.seq0 = groups->seq0;
   j.p.prefix = groups->prefix;
   j.p.groups = groups->groups;
   j.p.items = reinterpret_cast<int4*>(w + at.items);
+  const long long group_rows = (long long)groups->max_rows * j.p.group;
+  j.p.tile_rows = attn::many_tile_rows(D, group_rows);
+  j.p.block = attn::many_block(D);
+  attn::set_costs(j.p, D, attn::takes_many(j.p, D, (long long)step->max_tokens * j.p.group));
   // The groups over their prefixes.
   attn::Params a = j.p;
-  a.by_group = 1, a.causal = 0;
-  a.step.seqs = groups->groups;
-  a.step.max_tokens = groups->max_rows;
   a.parts = reinterpret_cast<float*>(w + at.parts);
   a.rows32 = reinterpret_cast<float*>(w + at.whole);
-  e = attn::launch_many(a, D, f16, sms, s);
+  e = attn::launch_many_prefixes(a, D, f16, sms, s);
   if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
   // The sequences over their own tokens.
   attn::Params b = j.p;
   b.rows32 = reinterpret_cast<float*>(w + at.own);
-  e = f16 ? attn::launch_rows<true, true>(b, D, sms, s) : attn::launch_rows<false, true>(b, D, sms, s);
+  e = f16 ? attn::launch_rows<true, attn::kOwn>(b, D, sms, s) : attn::launch_rows<false, attn::kOwn>(b, D, sms, s);
   if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
   j.own = b.rows32;
   j.whole = a.rows32;
   j.parts = a.parts;
-  j.tile_shift = attn::many_tile_rows(D, (long long)groups->max_rows * j.p.group) == 128 ? 7 : 8;
+  j.tile_shift = j.p.tile_rows == 128 ? 7 : 8;
   e = f16 ? attn::launch_join_of<true>(j, D, s) : attn::launch_join_of<false>(j, D, s);
   return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention_shared");
 }

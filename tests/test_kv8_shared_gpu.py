@@ -14,8 +14,13 @@ i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
 class Shared(Case):
     """A Case whose groups (first sequences seq0, tokens in common prefix) hold the same pages."""
 
-    def __init__(self, ns, lens, seq0, prefix, *heads, **kw):
+    def __init__(self, ns, lens, seq0, prefix, *heads, wide=True, **kw):
         super().__init__(ns, lens, *heads, **kw)
+        if wide:
+            # Room for so many tokens that the step does not count as a small read.
+            width = -(-(25 << 20) // (2 * len(ns) * self.P * self.Hkv * self.D))
+            self.table = np.pad(self.table, ((0, 0), (0, max(0, width - self.table.shape[1]))), constant_values=-1)
+            self.width = self.table.shape[1]
         self.seq0, self.prefix = seq0, prefix
         self.max_rows = 1
         self.share()
@@ -210,6 +215,12 @@ def test_the_workspace_serves_plain_attention_too():
         c.check_attention(a, None, 128 ** -0.5)
         c.check_attention(b, None, 128 ** -0.5)
     assert c.status() == 0
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_small_reads(dim):
+    # (The launch of kv8_attention: every sequence reads its own pages.)
+    Shared([1, 3, 1, 2], [150, 200, 140, 90], [0, 3, 4], [128, 64], 8, 2, dim, 64, seed=2, wide=False, pad=8).check(pad_out=16)
 
 
 def test_another_stream():
