@@ -737,14 +737,23 @@ def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
 # A speculative decoding loop around the cache: requests behind a common prefix, the next step's rows and pages, the
 # probabilities of a vocabulary and the verification of drafted tokens.
 
-def _int32(t, name, shape):
-    """The address of an int32 tensor of `shape` (a length -1: any)."""
-    if t.dim() != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _dev(t, name, esize=4)
-    if t.is_floating_point():
+def _int32(t, name, n=-1):
+    """The address of an int32 tensor [n] (-1: of any length)."""
+    global _torch_int32
+    if _torch_int32 is None:
+        import torch
+
+        _torch_int32 = torch.int32
+    shape = t.shape
+    if len(shape) != 1 or (shape[0] != n and n >= 0):
+        raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(shape)}")
+    if t.dtype is not _torch_int32 or not t.is_contiguous():
+        _dev(t, name, esize=4)
         raise ValueError(f"{name}: expected int32, got {t.dtype}")
     return t.data_ptr()
+
+
+_torch_int32 = None
 
 
 class KV8Groups:
@@ -753,12 +762,11 @@ class KV8Groups:
     max_rows: at most as many rows of one group."""
 
     def __init__(self, seq0, prefix, max_rows: int):
-        _int32(prefix, "prefix", (-1,))
-        groups = prefix.shape[0]
-        _int32(seq0, "seq0", (groups + 1,))
+        pp, groups = _int32(prefix, "prefix"), prefix.shape[0]
+        sp = _int32(seq0, "seq0", groups + 1)
         _on_cuda(seq0=seq0, prefix=prefix)
         self.seq0, self.prefix, self.groups = seq0, prefix, groups
-        self.c = KV8GroupsT(seq0.data_ptr(), prefix.data_ptr(), groups, max_rows)
+        self.c = KV8GroupsT(sp, pp, groups, max_rows)
         self.addr = ctypes.addressof(self.c)
 
 
@@ -767,11 +775,10 @@ class KV8Pool:
     of free pages behind it."""
 
     def __init__(self, ring, state):
-        _int32(ring, "ring", (-1,))
-        _int32(state, "state", (2,))
+        rp, sp = _int32(ring, "ring"), _int32(state, "state", 2)
         _on_cuda(ring=ring, state=state)
         self.ring, self.state = ring, state
-        self.c = KV8PoolT(ring.data_ptr(), state.data_ptr(), ring.shape[0])
+        self.c = KV8PoolT(rp, sp, ring.shape[0])
         self.addr = ctypes.addressof(self.c)
 
 
@@ -806,17 +813,24 @@ def kv8_plan(step, page_tokens: int, pool, held, take, grow, ws, pinned=None, ro
     """The step after `step` on the device: a sequence keeps `take` rows of it (below 0: it has ended), gets `grow` new ones
     and pages for them.  All int32: held, pinned, take, grow, granted [seqs]; positions, slots, seq_of [step.tokens].  What
     is not given of the first four outputs is updated in place (step.row0, step.kv_len, held, pool.state)."""
-    seqs, rows = step.kv_len.shape[0], step.tokens
-    out = {"row0_out": step.row0 if row0_out is None else row0_out, "kv_len_out": step.kv_len if kv_len_out is None else kv_len_out,
-           "held_out": held if held_out is None else held_out, "pool_out": pool.state if pool_out is None else pool_out,
-           "granted": granted, "positions": positions, "slots": slots, "seq_of": seq_of}
-    tensors = dict(held=held, pinned=pinned, take=take, grow=grow)
-    ptrs = [None if t is None else _int32(t, n, (seqs,)) for n, t in tensors.items()]
-    lengths = (seqs + 1, seqs, seqs, 2, seqs, rows, rows, rows)
-    c = KV8PlanT(*(None if t is None else _int32(t, n, (k,)) for (n, t), k in zip(out.items(), lengths)))
+    seqs, rows = step.c.seqs, step.tokens
+    hp, tp, gp = _int32(held, "held", seqs), _int32(take, "take", seqs), _int32(grow, "grow", seqs)
+    pp = None if pinned is None else _int32(pinned, "pinned", seqs)
+    # (Checks and addresses alone cost more than the kernel: none is made twice.)
+    c = KV8PlanT(step.c.row0 if row0_out is None else _int32(row0_out, "row0_out", seqs + 1),
+                 step.c.kv_len if kv_len_out is None else _int32(kv_len_out, "kv_len_out", seqs),
+                 hp if held_out is None else _int32(held_out, "held_out", seqs),
+                 pool.c.state if pool_out is None else _int32(pool_out, "pool_out", 2),
+                 None if granted is None else _int32(granted, "granted", seqs),
+                 None if positions is None else _int32(positions, "positions", rows),
+                 None if slots is None else _int32(slots, "slots", rows),
+                 None if seq_of is None else _int32(seq_of, "seq_of", rows))
     wp, wn = _ws(ws)
-    _on_cuda(**tensors, **out, ws=ws)
-    rc = lib().kv8_plan(step.addr, page_tokens, pool.addr, *ptrs, ctypes.addressof(c), wp, wn, _stream(stream))
+    for t in (held, take, grow, ws, pinned, row0_out, kv_len_out, held_out, pool_out, granted, positions, slots, seq_of):
+        if t is not None and not t.is_cuda:
+            _on_cuda(held=held, take=take, grow=grow, ws=ws, pinned=pinned, row0_out=row0_out, kv_len_out=kv_len_out, held_out=held_out,
+                     pool_out=pool_out, granted=granted, positions=positions, slots=slots, seq_of=seq_of)
+    rc = lib().kv8_plan(step.addr, page_tokens, pool.addr, hp, pp, tp, gp, ctypes.addressof(c), wp, wn, _stream(stream))
     _check("kv8_plan", rc)
 
 
@@ -848,10 +862,20 @@ def _vocab_rows(t, name, rows, vocab, dtype):
 
 
 def _f32s(t, name, rows):
-    if t.dim() != 1 or t.shape[0] != rows:
+    global _torch_float32
+    if _torch_float32 is None:
+        import torch
+
+        _torch_float32 = torch.float32
+    if t.shape != (rows,):
         raise ValueError(f"{name}: expected shape {(rows,)}, got {tuple(t.shape)}")
-    _fp32(t, name)
+    if t.dtype is not _torch_float32 or not t.is_contiguous():
+        _fp32(t, name)
+        raise ValueError(f"{name}: expected float32, got {t.dtype}")
     return t.data_ptr()
+
+
+_torch_float32 = None
 
 
 def spec_probs(logits, inv_temp=None, out=None, stream=None):
@@ -891,13 +915,12 @@ def spec_verify(p, tokens, row0, accept, sample, ws, q=None, next=None, take=Non
     dt = _spec_dtype(p, "p")
     ps = _vocab_rows(p, "p", rows, vocab, p.dtype)
     qp, qs = (None, 0) if q is None else (q.data_ptr(), _vocab_rows(q, "q", rows, vocab, p.dtype))
-    rp = _int32(row0, "row0", (-1,))
-    seqs = row0.shape[0] - 1
+    rp, seqs = _int32(row0, "row0"), row0.shape[0] - 1
     if next is None:
         next = torch.full((rows,), -1, dtype=torch.int32, device=p.device)
     if take is None:
         take = torch.empty(max(seqs, 0), dtype=torch.int32, device=p.device)
-    tp, np_, kp = _int32(tokens, "tokens", (rows,)), _int32(next, "next", (rows,)), _int32(take, "take", (seqs,))
+    tp, np_, kp = _int32(tokens, "tokens", rows), _int32(next, "next", rows), _int32(take, "take", seqs)
     ap, sp = _f32s(accept, "accept", rows), _f32s(sample, "sample", rows)
     wp, wn = _ws(ws)
     if not (p.is_cuda and tokens.is_cuda and row0.is_cuda and accept.is_cuda and sample.is_cuda and ws.is_cuda and next.is_cuda and

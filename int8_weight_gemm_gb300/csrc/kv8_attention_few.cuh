@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
     const int granules = (T1 - T0 + kGranule - 1) / kGranule;
     const int mine_n = granules > warp ? (granules - warp + kWarps - 1) / kWarps : 0;
     const int rows_left = x.s.n * p.group - tile * L::kRows;   // rows of the tile that exist
-    const int* const table = p.step.page_table + (size_t)(kMode == kOwn ? x.s.table : b) * p.step.table_width;
+    const int* const table = p.step.page_table + (size_t)b * p.step.table_width;
 
     // The page, scales and cache row of this warp's granule j, held by lane j % 32 (batches of 32,
     // two in registers: the ring runs ahead of the use).

@@ -168,7 +168,7 @@ static cudaError_t launch_join_of(const JoinParams& j, int head_dim, cudaStream_
 // their products, and one follows the other.)
 static void set_costs(Params& p, int head_dim, bool many) {
   p.prefix_fixed = 12000.f;
-  p.prefix_unit = head_dim == 256 ? 1900.f : p.tile_rows == 256 ? 3000.f : 1700.f;
+  p.prefix_unit = head_dim == 256 ? 1900.f : p.tile_rows == 256 ? 3000.f : 2200.f;
   p.own_fixed = many ? -1.f : 9000.f;
   const long long rows = (long long)p.step.max_tokens * p.group;
   p.own_token = (head_dim == 256 ? 2.f : 1.f) * (rows <= 8 ? 7.5f : rows <= 16 ? 9.f : 25.f);

@@ -115,7 +115,9 @@ def test_handles_check_their_tensors():
 def test_call_checks_come_before_the_library():
     class Stub:          # what the calls read of the handles
         tokens, kv_heads, head_dim = 4, 2, 64
-        row0, kv_len, state = torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+
+        class c:
+            seqs, row0, kv_len, state = 2, 0, 0, 0
 
     s = Stub()
     x, ws = torch.zeros((4, 2, 64), dtype=torch.bfloat16), torch.zeros(1024, dtype=torch.uint8)
