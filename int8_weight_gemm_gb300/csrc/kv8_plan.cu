@@ -21,8 +21,10 @@ namespace w8a8 {
 namespace plan {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kRowsPerThread = 4;   // rows of the step's buffers for each thread: the grid's size
+constexpr int kRowsPerThread = 1;   // rows of the step's buffers for each thread: the grid's size (4: prompts among 1000 13.9 us, 1: 11.2)
 constexpr int kMaxCtas = 128;
+constexpr int kMost = (1 << 30) + 1;
+__device__ __forceinline__ int plus(int a, int b) { return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)kMost); }   // of numbers up to kMost
 constexpr int kCounterWord = 16;    // of the workspace's header: arrivals of this call's CTAs, zero between calls
 
 struct Params {
@@ -67,9 +69,8 @@ __device__ __forceinline__ Seq load(const Params& p, int b, bool report) {
 }
 
 __global__ void __launch_bounds__(kMaxThreads) kv8_plan_kernel(const __grid_constant__ Params p) {
-  __shared__ long long warp_sm[3][32];
-  __shared__ int rows_sm[kMaxThreads], need_sm[kMaxThreads];   // sums before each thread's sequences
-  __shared__ long long back_sm[kMaxThreads];
+  __shared__ int warp_sm[3][32];
+  __shared__ int rows_sm[kMaxThreads], need_sm[kMaxThreads], back_sm[kMaxThreads];   // sums before each thread's sequences
   __shared__ int fail_sm[32];
   __shared__ int total_sm[2];
   __shared__ int last_sm;
@@ -86,36 +87,40 @@ __global__ void __launch_bounds__(kMaxThreads) kv8_plan_kernel(const __grid_cons
   }
 
   // ---------------------------------------------------------------- sums over the sequences
-  long long mine[3] = {0, 0, 0}, before[3], all[3] = {0, 0, 0};   // rows, pages, pages that come back
+  // Of rows, pages and pages that come back, each held at kMost: more than any limit it is compared with.
+  int mine[3] = {0, 0, 0}, before[3], all[3];
   for (int b = b0; b < b1; ++b) {
     const Seq s = load(p, b, reporter);
-    mine[0] += s.want, mine[1] += s.need, mine[2] += s.back;
+    mine[0] = plus(mine[0], s.want), mine[1] = plus(mine[1], s.need), mine[2] = plus(mine[2], s.back);
   }
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    long long incl = mine[i];
+  auto scan = [&](int v) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      const int t = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = plus(v, t);
     }
+    return v;
+  };
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int incl = scan(mine[i]), prev = __shfl_up_sync(0xffffffffu, incl, 1);
     if (lane == 31) warp_sm[i][warp] = incl;
-    before[i] = incl - mine[i];
+    before[i] = lane > 0 ? prev : 0;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before[i] += warp_sm[i][w];
-      all[i] += warp_sm[i][w];
-    }
+  for (int i = 0; i < 3; ++i) {
+    const int incl = scan(lane < warps ? warp_sm[i][lane] : 0), prev = __shfl_sync(0xffffffffu, incl, (warp + 31) & 31);
+    before[i] = plus(before[i], warp > 0 ? prev : 0);
+    all[i] = __shfl_sync(0xffffffffu, incl, 31);
+  }
   // The first sequence that does not fit: from there on none gets rows.
   int fail = p.seqs;
   if (all[0] > p.rows || all[1] > free) {
-    long long r = before[0], n = before[1];
+    int r = before[0], n = before[1];
     for (int b = b0; b < b1 && fail == p.seqs; ++b) {
       const Seq s = load(p, b, false);
-      r += s.want, n += s.need;
+      r = plus(r, s.want), n = plus(n, s.need);
       if (r > p.rows || n > free) fail = b;
     }
     fail = __reduce_min_sync(0xffffffffu, fail);
@@ -128,22 +133,22 @@ __global__ void __launch_bounds__(kMaxThreads) kv8_plan_kernel(const __grid_cons
         const Seq s = load(p, b, false);
         r += s.want, n += s.need;
       }
-      total_sm[0] = (int)r, total_sm[1] = (int)n;
+      total_sm[0] = r, total_sm[1] = n;
     }
     __syncthreads();
     all[0] = total_sm[0], all[1] = total_sm[1];
   }
-  const int rows = (int)all[0], used = (int)all[1];
-  const long long room = p.capacity - free;   // a ring that would hold more pages than places has been given one twice
-  const int back = (int)min(all[2], room);
+  const int rows = all[0], used = all[1];
+  const int room = p.capacity - free;   // a ring that would hold more pages than places has been given one twice
+  const int back = min(all[2], room);
   if (all[2] > room && reporter && tid == 0) atomicOr(p.status, W8A8_DEV_BAD_INDEX);
-  rows_sm[tid] = (int)min(before[0], (long long)rows);
-  need_sm[tid] = (int)min(before[1], (long long)used);
+  rows_sm[tid] = min(before[0], rows);
+  need_sm[tid] = min(before[1], used);
   back_sm[tid] = before[2];
   __syncthreads();
 
   // The sequence of place k in sums like `sums` (k below their total), and k's place within it.
-  auto find = [&](const auto* sums, auto k, auto count, int& b, Seq& s) {
+  auto find = [&](const int* sums, int k, auto count, int& b, Seq& s) {
     int t = 0;
     for (int step = kMaxThreads / 2; step > 0; step >>= 1)
       if (t + step < threads && sums[t + step] <= k) t += step;
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv8_plan_kernel(const __grid_cons
       k -= count(s);
       s = load(p, ++b, false);
     }
-    return (int)k;
+    return k;
   };
   auto ring_at = [&](int i) {   // i at most the capacity
     const uint32_t at = (uint32_t)head + (uint32_t)i;
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv8_plan_kernel(const __grid_cons
   for (int k = first; k < back; k += stride) {
     int b;
     Seq s;
-    const int i = find(back_sm, (long long)k, [](const Seq& s) { return s.back; }, b, s);
+    const int i = find(back_sm, k, [](const Seq& s) { return s.back; }, b, s);
     p.ring[ring_at(free + k)] = p.table[(size_t)b * p.width + s.pinned + i];
   }
   for (int k = first; k < used; k += stride) {

@@ -118,6 +118,14 @@ def test_what_does_not_fit_is_not_granted(seqs, what):
             assert 0 < sum(g > 0 for g in want["granted"]) < (c.grow > 0).sum() or what == "no rows"
 
 
+@pytest.mark.parametrize("rows", [1000, 1 << 22])
+def test_sums_that_pass_31_bits(rows):
+    c = Plan(6000, 128, 6, max_tokens=1 << 20, rows=rows, spare=9000, longest=300, ahead=1)
+    assert c.grow.astype(np.int64).sum() > 2**31 - 1
+    c.check(c.run(some=rows < 10**4))
+    assert lib8.w8a8_workspace_status(c.ws) == 0
+
+
 def test_optional_arguments():
     c = Plan(50, 32, 5)
     c.check(c.run(pinned=False, some=False), c.expect(pinned=False))
