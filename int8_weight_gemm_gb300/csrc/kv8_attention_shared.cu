@@ -18,6 +18,7 @@ namespace w8a8 {
 namespace attn {
 
 constexpr int kJoinThreads = 256;
+constexpr int kFew = 4;   // parts
 constexpr long long kSmallRead = 24ll << 20;
 
 struct JoinParams {
@@ -56,32 +57,86 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   constexpr int kV = D == 256 ? 2 : 1, kAt = D == 64 ? 2 : 1;
   const int d = 4 * (lane & (D == 64 ? 15 : 31));
   const size_t part_floats = (size_t)(D + 4) << j.tile_shift;
-  for (int head = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); head < p.q_heads; head += gridDim.y * (kJoinThreads / 32)) {
-    const size_t at = (size_t)row * p.q_heads + head;
-    int4 item = make_int4(0, 0, 0, 0);   // first CTA, parts, place in the first
-    int within = 0;
+  // (item_of, by shifts.)
+  const long long first_row = (long long)(row - of.row0) * p.group, first_item = ((long long)of.row0 * p.group >> j.tile_shift) + g;
+  // What a head's own side left, and the place of its item: asked for one head ahead.
+  struct Head {
+    float4 t, acc[kV];
+    int4 item;   // first CTA, parts, place in the first
+    int within;
+  };
+  auto ask = [&](int head, Head& x) {
+    const float* const own = j.own + ((size_t)row * p.q_heads + head) * (D + 4);
+    x.item = make_int4(0, 0, 0, 0);
+    x.within = 0;
     if (shared) {
-      const long long ri = (long long)(row - of.row0) * p.group + head % p.group;
-      within = (int)ri & ((1 << j.tile_shift) - 1);
-      item = p.items[item_of(p, g, of.row0, 1 << j.tile_shift, (int)(ri >> j.tile_shift), head / p.group)];
+      const int h = (int)((uint32_t)head / (uint32_t)p.group);
+      const long long ri = first_row + (head - h * p.group);
+      x.within = (int)ri & ((1 << j.tile_shift) - 1);
+      x.item = p.items[(size_t)(first_item + (ri >> j.tile_shift)) * p.kv_heads + h];
     }
-    const int parts = item.y;
-    const float* const own = j.own + at * (D + 4);
-    const float4 t0 = *reinterpret_cast<const float4*>(own + D);
-    float M = t0.x, R = t0.z, l = t0.y;
+    x.t = *reinterpret_cast<const float4*>(own + D);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) x.acc[v] = *reinterpret_cast<const float4*>(own + d + 128 * v);
+  };
+  const int step = gridDim.y * (kJoinThreads / 32);
+  int head = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  if (head >= p.q_heads) return;
+  Head next;
+  ask(head, next);
+  for (; head < p.q_heads; head += step) {
+    const Head x = next;
+    if (head + step < p.q_heads) ask(head + step, next);
+    const size_t at = (size_t)row * p.q_heads + head;
+    const int4 item = x.item;
+    const int within = x.within, parts = item.y;
+    float M = x.t.x, R = x.t.z, l = x.t.y;
     float4 acc[kV];
 #pragma unroll
-    for (int v = 0; v < kV; ++v) acc[v] = *reinterpret_cast<const float4*>(own + d + 128 * v);
-    // (An item that was not cut: its rows as they are; a part: [D / 4][rows] of four columns, then the rows' statistics.
-    // Neighbouring heads' columns share a line, so these loads stay in the L1 cache.)
-    auto part_of = [&](int i) { return j.parts + ((size_t)(item.x + i) * 2 + (i == 0 ? item.z : 0)) * part_floats; };
-    auto sums_of = [&](int i, int d) {
-      return *reinterpret_cast<const float4*>(parts == 1 ? j.whole + at * (D + 4) + d : part_of(i) + ((size_t)(d >> 2) << j.tile_shift) * 4 + within * 4);
+    for (int v = 0; v < kV; ++v) acc[v] = x.acc[v];
+    // The row's columns from d on, and its statistics, in part i.  (An item that was not cut: its rows as they are; a part:
+    // [D / 4][rows] of four columns, then the rows' statistics.  Neighbouring heads' columns share a line, so these loads
+    // stay in the L1 cache.)
+    const bool cut = parts != 1;
+    const float* const part0 = cut ? j.parts + (size_t)item.x * 2 * part_floats + within * 4 : j.whole + at * (D + 4);
+    const size_t col = cut ? (size_t)d << j.tile_shift : (size_t)d, cols128 = cut ? (size_t)128 << j.tile_shift : 128, stats = cut ? (size_t)D << j.tile_shift : D;
+    auto part_of = [&](int i) { return part0 + (i > 0 ? (size_t)(2 * i) * part_floats : cut && item.z ? part_floats : 0); };
+    auto sums_of = [&](int i, int v) { return *reinterpret_cast<const float4*>(part_of(i) + col + v * cols128); };
+    auto stats_of = [&](int i) { return *reinterpret_cast<const float4*>(part_of(i) + stats); };
+    auto add = [&](const float4 x, float f, int v) {
+      acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
     };
-    auto stats_of = [&](int i) {
-      return *reinterpret_cast<const float4*>(parts == 1 ? j.whole + at * (D + 4) + D : part_of(i) + ((size_t)D << j.tile_shift) + within * 4);
-    };
-    if (parts > 0) {
+    if (parts > 0 && parts <= kFew) {
+      // Few parts: every lane does what a lane each would have to share (1848 rows of 32 heads XX -> XX us).
+      float4 t[kFew], x[kFew][kV];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        t[i] = make_float4(kFloor, 0.f, kFloor, 0.f);
+        if (i < parts) {
+          t[i] = stats_of(i);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) x[i][v] = sums_of(i, v);
+        }
+      }
+      float mn = M, rn = R;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) mn = fmaxf(mn, t[i].x), rn = fmaxf(rn, t[i].z);
+      l *= ex2(M - mn);
+      const float a0 = ex2(R - rn);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) acc[v].x *= a0, acc[v].y *= a0, acc[v].z *= a0, acc[v].w *= a0;
+      M = mn;
+      R = rn;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (i < parts) {
+          l = fmaf(t[i].y, ex2(t[i].x - M), l);
+          const float f = ex2(t[i].z - R);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) add(x[i][v], f, v);
+        }
+      }
+    } else if (parts > 0) {
       // References first: a lane for each part.
       float4 t = make_float4(kFloor, 0.f, kFloor, 0.f);
       if (lane < parts) t = stats_of(lane);
@@ -118,10 +173,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
           const float f = __shfl_sync(0xffffffffu, a, (i + odd) & 31);
           if (i + odd < n) {
 #pragma unroll
-            for (int v = 0; v < kV; ++v) {
-              const float4 x = sums_of(i0 + i + odd, d + 128 * v);
-              acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
-            }
+            for (int v = 0; v < kV; ++v) add(sums_of(i0 + i + odd, v), f, v);
           }
         }
       }
