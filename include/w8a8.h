@@ -555,6 +555,9 @@ typedef struct {
  * sequence gets rows (granted 0; kv_len = kept).  Pages that come back in a call are handed out from the
  * next one on.  A sequence whose numbers make no sense (more rows taken than there were, a table too
  * narrow, ...) keeps its tokens, gets nothing, and W8A8_DEV_BAD_INDEX is recorded.
+ * A step whose `tokens` is room for more rows than it has, as in a captured graph, goes to the other calls
+ * as it is: rows behind the last sequence are left alone or computed for nobody.  (kv8_append then takes
+ * `positions` from here, so that those rows have one inside the rotation table.)
  * page_tokens as in kv8_cache_t.  Workspace: 256 bytes, any of the attention side's (kv8_workspace_bytes,
  * kv8_shared_workspace_bytes) or its own.  One launch; errors as above. */
 int kv8_plan(const kv8_step_t* step, int page_tokens, const kv8_pool_t* pool, const int32_t* held,
