@@ -610,7 +610,7 @@ size_t spec_workspace_bytes(int seqs, int vocab);
  *  next  [rows]    int32 out: the token after each row, up to the row that draws; -1 for the window's rows
  *                  behind it; rows of no sequence are left as they were
  *  take  [seqs]    int32 out: rows that stay (accepted tokens and the one before them), 0 without rows
- * One launch.  1 <= vocab <= 2^18, seqs <= 65535, rows <= 2^22.  Errors: INVALID_ARG, MISALIGNED,
+ * No output may overlap an input.  One launch.  1 <= vocab <= 2^18, seqs <= 65535, rows <= 2^22.  Errors: INVALID_ARG, MISALIGNED,
  * WORKSPACE_TOO_SMALL, CUDA. */
 int spec_verify(const void* p, long long p_stride, const void* q, long long q_stride, const int32_t* tokens,
                 const int32_t* row0, int seqs, int rows, int vocab, const float* accept, const float* sample,

@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   // CTAs that take part.
   const int room = kMode == kOwn ? min((int)gridDim.x, own_sms(p, prefix_sms<kThreads>(p, ring)) * L::kCtas) : (int)gridDim.x;
 
+  if (kMode == kOwn) fence_async_shared();   // (the scratch of prefix_sms lies where copies will land)
+
   // ---------------------------------------------------------------- this CTA's run of units
   const int per = (p.step.seqs + kThreads - 1) / kThreads;   // sequences a thread scans
   const int s0 = min(p.step.seqs, (int)threadIdx.x * per), s1 = min(p.step.seqs, s0 + per);

@@ -89,7 +89,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
     if (head + step < p.q_heads) ask(head + step, next);
     const size_t at = (size_t)row * p.q_heads + head;
     const int4 item = x.item;
-    const int within = x.within, parts = item.y;
+    const int within = x.within;
+    int parts = item.y;
+    if (item.x < 0 || parts < 0 || parts > p.sms - item.x || (uint32_t)item.z > 1u) {
+      // No launch that ended well leaves this: nothing is read through it.
+      if (lane == 0) atomicOr(p.status, W8A8_DEV_BAD_INDEX);
+      parts = 0;
+    }
     float M = x.t.x, R = x.t.z, l = x.t.y;
     float4 acc[kV];
 #pragma unroll
