@@ -503,8 +503,11 @@ size_t kv8_shared_workspace_bytes(int tokens, int groups, int q_heads, int kv_he
  * The result is that of kv8_attention, with its arguments, where the sequences of each group do hold
  * the same tokens there.  Nothing is shared, and each sequence reads its own pages, in a group of one
  * sequence, in one whose first sequence holds less than the prefix, and for a sequence with a row that
- * does not see all of the prefix; sequences of no group are read on their own.
- * Three launches, otherwise as kv8_attention.  Errors as above. */
+ * does not see all of the prefix; sequences of no group are read on their own.  Nor is anything shared in a
+ * step that kv8_attention reads as fast by itself: one of many rows a sequence (80 of a kv head), or of a page
+ * table with room for few tokens (seqs * table_width * page_tokens * kv_heads up to 400,000 or 700,000, by
+ * rows); the table need be no wider than the step.
+ * Three launches (one where nothing is shared), otherwise as kv8_attention.  Errors as above. */
 int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* step, const kv8_groups_t* groups,
                          const void* q, long long q_stride, int q_heads, void* out, long long out_stride,
                          float* lse, float scale, int dtype, void* ws, size_t ws_bytes, void* stream);

@@ -176,8 +176,7 @@ struct Runs {
 // The SMs that the groups' launch takes while the other takes the rest, worked out alike by every CTA of both (the whole
 // block takes part): prefixes cost the matrix products' chain of waits, own tokens HBM's bandwidth, so side by side
 // they finish sooner than one after the other.  The time of either falls with its SMs; the count is that of the
-// smallest maximum, or all of them (the other launch then follows) where that is sooner, and where own_fixed is below 0.
-// 0: nothing is shared.
+// smallest maximum, or all of them (the other launch then follows) where that is sooner.  0: nothing is shared.
 // scratch: shared memory, 24 bytes a warp, free again behind the block's next barrier.
 template <int kThreads>
 __device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
@@ -205,7 +204,6 @@ __device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) units += sums_sm[0][w], own += sums_sm[1][w];
   if (units == 0) return 0;
-  if (p.own_fixed < 0.f) return p.sms;
   units *= p.kv_heads;
   const float a = p.prefix_unit * (float)units, b = p.own_token * (float)max(own, 0ll) * (float)p.kv_heads;
   uint32_t best = 0xffffffffu;
@@ -225,10 +223,9 @@ __device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
 // SMs of the launch of the sequences' own tokens beside `n` of the other.
 __device__ __forceinline__ int own_sms(const Params& p, int n) { return n < p.sms ? p.sms - n : p.sms; }
 
-// The kernel of many query rows (kv8_attention_many.cuh): each mode's instances; its share of the workspace.
+// The kernel of many query rows (kv8_attention_many.cuh), kPlain and kPrefixes; its share of the workspace.
 cudaError_t launch_many(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
 cudaError_t launch_many_prefixes(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
-cudaError_t launch_many_own(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s);
 size_t many_parts_bytes(int head_dim, int sms);
 // Rows of one of its tiles for sequences of up to `rows` rows of a kv head; tokens of a unit.
 int many_tile_rows(int head_dim, long long rows);

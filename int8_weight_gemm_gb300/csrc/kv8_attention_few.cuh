@@ -795,7 +795,7 @@ static bool takes_many(const Params& p, int head_dim, long long rows) {
 template <bool kF16, Mode kMode>
 static cudaError_t launch_rows(const Params& p, int head_dim, int sms, cudaStream_t s) {
   const long long rows = (long long)p.step.max_tokens * p.group;
-  if (takes_many(p, head_dim, rows)) return kMode == kOwn ? launch_many_own(p, head_dim, kF16, sms, s) : launch_many(p, head_dim, kF16, sms, s);
+  if (kMode == kPlain && takes_many(p, head_dim, rows)) return launch_many(p, head_dim, kF16, sms, s);
   if (head_dim == 64)
     return rows <= 8    ? launch_few<kF16, 64, 1, kMode>(p, sms, s)
            : rows <= 16 ? launch_few<kF16, 64, 2, kMode>(p, sms, s)

@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged key-value cache: many query rows (prompts, long verify windows), on the
-// fifth-generation tensor cores (tcgen05, sm_103a).  The operator is that of kv8_attention.cu.
+// fifth-generation tensor cores (tcgen05, sm_103a).  The operator is that of kv8_attention_few.cuh.
 //
 // What bounds it: a cached byte feeds 2 (rows that share its head) multiply-adds, so from some 300 rows
 // on the products do: a block of 128 tokens against 128 rows is 2 x 128 x 128 x D multiply-adds, 1024
@@ -303,14 +303,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   }
   if (warp == kMmaWarp) tmem_alloc(&tmem_base, 512);
   tc_fence_before();
-  // The launch of the sequences' own tokens starts when every CTA of the groups' has seen the work before it complete,
-  // and waits for that launch at its end.
-  if (kMode != kPrefixes) pdl_trigger();
-  if (kMode != kOwn) pdl_wait();
+  // (kPrefixes: the launch of the sequences' own tokens starts when every CTA of this one has seen the work before it
+  // complete.)
+  if (kMode == kPlain) pdl_trigger();
+  pdl_wait();
   if (kMode == kPrefixes) pdl_trigger();
   // CTAs that take part.
-  const int beside = kMode == kPlain ? 0 : prefix_sms<kTcThreads>(p, qtile);
-  const int room = min((int)gridDim.x, kMode == kPrefixes ? beside : kMode == kOwn ? own_sms(p, beside) : (int)gridDim.x);
+  const int room = kMode == kPrefixes ? min((int)gridDim.x, prefix_sms<kTcThreads>(p, qtile)) : (int)gridDim.x;
 
   // ---------------------------------------------------------------- this CTA's run of units
   const int seqs = count_of<kMode>(p), per = (seqs + kTcThreads - 1) / kTcThreads;   // sequences a thread scans
@@ -728,7 +727,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
         }
       }
       const int pos = g->pos0 + tok;
-      const int end = !live ? 0x7fffffff : kMode == kOwn || (kMode == kPlain && p.causal) ? min(pos + 1, g->len) : g->len;
+      const int end = !live ? 0x7fffffff : kMode == kPlain && p.causal ? min(pos + 1, g->len) : g->len;
       const int beg = kMode == kPlain && live && p.window > 0 ? max(0, pos - p.window + 1) : 0;
       const int full_hi = __reduce_min_sync(0xffffffffu, end), full_lo = __reduce_max_sync(0xffffffffu, beg);
 
@@ -1038,12 +1037,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
               const float4 t = row_sm[rw];
               const int oi = g->tile * L::kRows + rw;
               const int orow = g->row0 + oi / p.group, oh = g->h * p.group + oi % p.group;
-              if (kMode != kPlain) {
-                float* const dst = p.rows32 + ((size_t)orow * p.q_heads + oh) * (D + 4);
-                *reinterpret_cast<float4*>(dst + d) = acc[y];
-                if (d == 0) *reinterpret_cast<float4*>(dst + D) = t;
-                continue;
-              }
               const float zz = t.y == 0.f ? 0.f : __fdividef(1.f, t.y) * ex2(t.z - t.x);
               *reinterpret_cast<uint2*>(p.out + orow * p.out_stride + oh * D + d) =
                   make_uint2(pack2<kF16>(acc[y].x * zz, acc[y].y * zz), pack2<kF16>(acc[y].z * zz, acc[y].w * zz));
@@ -1070,7 +1063,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv8_attention_tc_kernel(const _
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem_base, 512);
-  if (kMode == kOwn && blockIdx.x == 0) pdl_wait();   // (the grid is not complete before it)
 }
 
 template <bool kF16, int D, int kTiles, Mode kMode>

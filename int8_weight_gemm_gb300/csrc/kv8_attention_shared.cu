@@ -2,16 +2,23 @@
 // group of sequences has in common are read once, for all of their rows.
 //
 // Mathematics.  The tokens that a row sees are the prefix, then its sequence's own.  Each side gives sums o relative to a
-// reference r, and (m, l) of its softmax (kv8_attention.cu); the two, and the parts of a side that was cut, join as
+// reference r, and (m, l) of its softmax (kv8_attention_few.cuh); the two, and the parts of a side that was cut, join as
 //   M = max m_i,  R = max r_i,  l = sum l_i 2^(m_i - M),  o = sum o_i 2^(r_i - R),  out = o 2^(R - M) / l.
 //
 // What bounds it: with the prefix read once its products do.  64 rows' heads of 4 a kv head are 256 rows over every
-// prefix byte, work for the kernel of many rows (kv8_attention_tc.cu); the own tokens are a decode step's and stream at
-// HBM speed (kv8_attention.cu, or the other for many rows).  So a call is three launches: the groups over their
-// prefixes as if each were one sequence, not causal; the sequences over their own tokens; and the join.  The first two
-// leave fp32 rows.  A prefix of few items (a kv head's 256 rows each) is cut over all SMs, some twenty parts an item,
-// which one CTA an item would read for longer than the products take: the join below has a warp for each (row, head),
-// on all SMs.
+// prefix byte, work for the kernel of many rows (kv8_attention_many.cuh), which is bound by a chain of waits; the own
+// tokens are a decode step's and stream at HBM speed (kv8_attention_few.cuh).  So a call is three launches: the groups
+// over their prefixes as if each were one sequence, not causal; beside it, on the other SMs (prefix_sms), the sequences
+// over their own tokens; and the join of the fp32 rows that the two leave.  A prefix of few items (a kv head's 256 rows
+// each) is cut into several parts an item, which one CTA an item would read for longer than the products take: the join
+// has a warp for each (row, head), on all SMs.
+//
+// Launches.  The groups' CTAs let the second launch begin when they have seen the work before them complete, so it may read
+// what that work wrote; it waits for the groups' at its end, so that the join, which waits for it, sees both.
+//
+// Measured (32 query heads, 8 kv heads of 128; in brackets kv8_attention, whose re-reads hit L2): 64 sequences of 6101-8191
+// tokens behind one prefix of 6016 66 us (141), 35 us of it 148 MB of own tokens' stream and products beside it, 5 the
+// start, 5 the join; one launch after the other 89, the parts joined by rows (uncoalesced) 70.
 #include "kv8_attention_few.cuh"
 
 namespace w8a8 {
@@ -19,7 +26,9 @@ namespace attn {
 
 constexpr int kJoinThreads = 256;
 constexpr int kFew = 4;   // parts
-constexpr long long kSmallRead = 24ll << 20;
+// Steps that kv8_attention's launch takes as they are (worth_sharing).
+constexpr int kManyRows = 80;                                    // of a sequence and kv head
+constexpr long long kFewTokens = 700000, kFewTokensWide = 400000;   // times kv heads, up to 16 rows and more
 
 struct JoinParams {
   Params p;
@@ -113,7 +122,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
       acc[v].x = fmaf(x.x, f, acc[v].x), acc[v].y = fmaf(x.y, f, acc[v].y), acc[v].z = fmaf(x.z, f, acc[v].z), acc[v].w = fmaf(x.w, f, acc[v].w);
     };
     if (parts > 0 && parts <= kFew) {
-      // Few parts: every lane does what a lane each would have to share (1848 rows of 32 heads XX -> XX us).
+      // Few parts: every lane does what a lane each would have to share (64 rows of 32 heads, 4 parts: the call 67.5 -> 66.4 us).
       float4 t[kFew], x[kFew][kV];
 #pragma unroll
       for (int i = 0; i < kFew; ++i) {
@@ -222,14 +231,24 @@ static cudaError_t launch_join_of(const JoinParams& j, int head_dim, cudaStream_
   return head_dim == 64 ? launch_join<kF16, 64>(j, s) : head_dim == 128 ? launch_join<kF16, 128>(j, s) : launch_join<kF16, 256>(j, s);
 }
 
-// What the two launches cost an SM, in ns, for prefix_sms: measured.  (Many rows on either side: both are bound by
-// their products, and one follows the other.)
-static void set_costs(Params& p, int head_dim, bool many) {
+// What the two launches cost an SM, in ns, for prefix_sms: measured.
+static void set_costs(Params& p, int head_dim, long long rows) {
   p.prefix_fixed = 12000.f;
   p.prefix_unit = head_dim == 256 ? 1900.f : p.tile_rows == 256 ? 3000.f : 2200.f;
-  p.own_fixed = many ? -1.f : 9000.f;
-  const long long rows = (long long)p.step.max_tokens * p.group;
-  p.own_token = (head_dim == 256 ? 2.f : 1.f) * (rows <= 8 ? 7.5f : rows <= 16 ? 9.f : 25.f);
+  p.own_fixed = 9000.f;
+  p.own_token = (head_dim == 256 ? 2.f : 1.f) * (rows <= 8 ? 7.5f : rows <= 16 ? 9.f : rows <= 32 ? 25.f : 0.8f * (float)rows);
+}
+
+// Whether a step can gain by sharing, as far as the host can tell.  Sequences of many rows fill the products' tiles on their
+// own, and those are the bound (us, as they are / shared): 32 windows of 16 tokens behind 4096, 32 query and 8 kv heads (64
+// rows) 133 / 110; of 23 (92 rows) 137 / 145; 8 prompts of 256 (1024) 197 / 236.
+// And the re-reads of a prefix hit L2, so a small cache, by what the page table has room for, is read in less time than the
+// three launches take (128-wide heads): 16 sequences on 1424 tokens, 4 kv heads (24 MB) 11.6 / 21.7; 64 of
+// 1700, 8 (213 MB) 46 / 47; 64 of 2700 (341 MB) 64 / 49; 64 of 7000 (897 MB) 141 / 66; 16 windows of 6 on 4300 (134 MB, 24 rows)
+// 48 / 45; heads of 64, 32 of 3000, 16 kv heads (196 MB) 49 / 41.
+static bool worth_sharing(const kv8_cache_t* cache, const kv8_step_t* step, long long rows) {
+  const long long tokens = (long long)step->seqs * step->table_width * cache->page_tokens * cache->kv_heads;
+  return rows < kManyRows && tokens > (rows <= 16 ? kFewTokens : kFewTokensWide);
 }
 
 // The workspace behind that of kv8_attention: parts of cut prefixes, their places, and two buffers of fp32 rows.
@@ -279,9 +298,8 @@ extern "C" int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* 
   attn::JoinParams j;
   cudaError_t e = attn::fill_params(j.p, cache, step, q, q_stride, q_heads, out, out_stride, lse, scale, ws, sms);
   if (e != cudaSuccess) return record_cuda_error(e, "kv8_attention_shared");
-  // A step whose whole table is a small read (a few us of HBM's rate) is read as it is: the three launches take longer.
-  const long long bytes = 2ll * step->seqs * step->table_width * cache->page_tokens * cache->kv_heads * D;
-  if (bytes <= attn::kSmallRead && !attn::takes_many(j.p, D, (long long)step->max_tokens * j.p.group)) {
+  const long long rows = (long long)step->max_tokens * j.p.group;
+  if (!attn::worth_sharing(cache, step, rows)) {
     e = attn::launch_plain(j.p, D, f16, sms, s);
     return e == cudaSuccess ? W8A8_OK : record_cuda_error(e, "kv8_attention_shared");
   }
@@ -292,7 +310,7 @@ extern "C" int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* 
   const long long group_rows = (long long)groups->max_rows * j.p.group;
   j.p.tile_rows = attn::many_tile_rows(D, group_rows);
   j.p.block = attn::many_block(D);
-  attn::set_costs(j.p, D, attn::takes_many(j.p, D, (long long)step->max_tokens * j.p.group));
+  attn::set_costs(j.p, D, rows);
   // The groups over their prefixes.
   attn::Params a = j.p;
   a.parts = reinterpret_cast<float*>(w + at.parts);

@@ -8,9 +8,5 @@ cudaError_t launch_many_prefixes(const Params& p, int head_dim, bool f16, int sm
   return launch_many_of<kPrefixes>(p, p.tile_rows, head_dim, f16, sms, s);
 }
 
-cudaError_t launch_many_own(const Params& p, int head_dim, bool f16, int sms, cudaStream_t s) {
-  return launch_many_of<kOwn>(p, (long long)p.step.max_tokens * p.group, head_dim, f16, sms, s);
-}
-
 }  // namespace attn
 }  // namespace w8a8

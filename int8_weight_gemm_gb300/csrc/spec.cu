@@ -45,6 +45,8 @@ struct Type<SPEC_F32> {
 // several rows: a warp copies its part of the next row into shared memory as soon as it has this one's in registers, and
 // the row after that is fetched into L2, so that loads hide behind a whole row's work (320 rows of 131072: loads into
 // registers behind the stores 58 us, without the fetch into L2 94).
+//
+// Measured: 320 rows of 131072 (bf16) 48.9 us, 5.1 TB/s, 76 % of a copy's rate; 16 rows of 32000 3.6 us.
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -273,6 +275,9 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
 //
 // What bounds it: HBM, p and q of one row a sequence, read once.  A sequence's row is cut into segments, one a warp;
 // the last CTA to arrive finds the segment in which the draw lies from their sums and reads it again (out of L2).
+//
+// Measured: 64 windows of 2 to 8 over 131072 (fp32, with the draft's) 19.3 us, half of it 67 MB at HBM's rate, the rest a chain of
+// loads before (offsets, token, its probabilities) and after (arrival, sums, segment); one window of 6 over 32000 6.0 us.
 constexpr int kVThreads = 256;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMinSegment = 512;

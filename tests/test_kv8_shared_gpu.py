@@ -17,8 +17,8 @@ class Shared(Case):
     def __init__(self, ns, lens, seq0, prefix, *heads, wide=True, **kw):
         super().__init__(ns, lens, *heads, **kw)
         if wide:
-            # Room for so many tokens that the step does not count as a small read.
-            width = -(-(25 << 20) // (2 * len(ns) * self.P * self.Hkv * self.D))
+            # Room for so many tokens that the step is worth sharing.
+            width = 700000 // (len(ns) * self.P * self.Hkv) + 1
             self.table = np.pad(self.table, ((0, 0), (0, max(0, width - self.table.shape[1]))), constant_values=-1)
             self.width = self.table.shape[1]
         self.seq0, self.prefix = seq0, prefix
@@ -221,6 +221,16 @@ def test_the_workspace_serves_plain_attention_too():
 def test_small_reads(dim):
     # (The launch of kv8_attention: every sequence reads its own pages.)
     Shared([1, 3, 1, 2], [150, 200, 140, 90], [0, 3, 4], [128, 64], 8, 2, dim, 64, seed=2, wide=False, pad=8).check(pad_out=16)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("longest", [9, 16, 19, 20])
+def test_windows_of_some_tens_of_rows(dim, longest):
+    # Rows of a kv head in one tile of the sequences' own launch, and in several.
+    rng = np.random.default_rng(longest)
+    ns = [longest, 1, 0] + rng.integers(1, longest + 1, 9).tolist()
+    lens = [512 + n + int(rng.integers(0, 300)) for n in ns]
+    Shared(ns, lens, [0, 12], [512], 8, 2, dim, 32, seed=longest, pad=8).check(pad_out=16)
 
 
 def test_another_stream():
