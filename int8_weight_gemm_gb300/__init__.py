@@ -737,23 +737,39 @@ def kv8_read(cache, step, ws, k_out=None, v_out=None, dtype=None, stream=None):
 # A speculative decoding loop around the cache: requests behind a common prefix, the next step's rows and pages, the
 # probabilities of a vocabulary and the verification of drafted tokens.
 
-def _int32(t, name, n=-1):
-    """The address of an int32 tensor [n] (-1: of any length)."""
+_torch_int32 = _torch_float32 = None
+
+
+def _vector(t, name, n, dtype):
+    """Why a tensor is not a contiguous one of n values of dtype."""
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(t.shape)}")
+    _dev(t, name, esize=4)
+    raise ValueError(f"{name}: expected {str(dtype).removeprefix('torch.')}, got {t.dtype}")
+
+
+def _int32(t, name, n):
+    """The address of an int32 tensor [n]."""
     global _torch_int32
     if _torch_int32 is None:
         import torch
 
         _torch_int32 = torch.int32
-    shape = t.shape
-    if len(shape) != 1 or (shape[0] != n and n >= 0):
-        raise ValueError(f"{name}: expected shape {(n,)}, got {tuple(shape)}")
-    if t.dtype is not _torch_int32 or not t.is_contiguous():
-        _dev(t, name, esize=4)
-        raise ValueError(f"{name}: expected int32, got {t.dtype}")
+    if t.dtype is not _torch_int32 or t.numel() != n or not t.is_contiguous():
+        _vector(t, name, n, _torch_int32)
     return t.data_ptr()
 
 
-_torch_int32 = None
+def _f32s(t, name, n):
+    """The same of an fp32 one."""
+    global _torch_float32
+    if _torch_float32 is None:
+        import torch
+
+        _torch_float32 = torch.float32
+    if t.dtype is not _torch_float32 or t.numel() != n or not t.is_contiguous():
+        _vector(t, name, n, _torch_float32)
+    return t.data_ptr()
 
 
 class KV8Groups:
@@ -762,7 +778,8 @@ class KV8Groups:
     max_rows: at most as many rows of one group."""
 
     def __init__(self, seq0, prefix, max_rows: int):
-        pp, groups = _int32(prefix, "prefix"), prefix.shape[0]
+        groups = prefix.numel()
+        pp = _int32(prefix, "prefix", groups)
         sp = _int32(seq0, "seq0", groups + 1)
         _on_cuda(seq0=seq0, prefix=prefix)
         self.seq0, self.prefix, self.groups = seq0, prefix, groups
@@ -775,10 +792,10 @@ class KV8Pool:
     of free pages behind it."""
 
     def __init__(self, ring, state):
-        rp, sp = _int32(ring, "ring"), _int32(state, "state", 2)
+        rp, sp = _int32(ring, "ring", ring.numel()), _int32(state, "state", 2)
         _on_cuda(ring=ring, state=state)
         self.ring, self.state = ring, state
-        self.c = KV8PoolT(rp, sp, ring.shape[0])
+        self.c = KV8PoolT(rp, sp, ring.numel())
         self.addr = ctypes.addressof(self.c)
 
 
@@ -861,23 +878,6 @@ def _vocab_rows(t, name, rows, vocab, dtype):
     return s0 if rows > 1 else vocab
 
 
-def _f32s(t, name, rows):
-    global _torch_float32
-    if _torch_float32 is None:
-        import torch
-
-        _torch_float32 = torch.float32
-    if t.shape != (rows,):
-        raise ValueError(f"{name}: expected shape {(rows,)}, got {tuple(t.shape)}")
-    if t.dtype is not _torch_float32 or not t.is_contiguous():
-        _fp32(t, name)
-        raise ValueError(f"{name}: expected float32, got {t.dtype}")
-    return t.data_ptr()
-
-
-_torch_float32 = None
-
-
 def spec_probs(logits, inv_temp=None, out=None, stream=None):
     """Probabilities fp32 [rows, vocab] of logits (bf16, fp16 or fp32): softmax of logits * inv_temp[row] (None: 1;
     infinity: 1 for the first of the largest)."""
@@ -915,7 +915,8 @@ def spec_verify(p, tokens, row0, accept, sample, ws, q=None, next=None, take=Non
     dt = _spec_dtype(p, "p")
     ps = _vocab_rows(p, "p", rows, vocab, p.dtype)
     qp, qs = (None, 0) if q is None else (q.data_ptr(), _vocab_rows(q, "q", rows, vocab, p.dtype))
-    rp, seqs = _int32(row0, "row0"), row0.shape[0] - 1
+    seqs = row0.numel() - 1
+    rp = _int32(row0, "row0", seqs + 1)
     if next is None:
         next = torch.full((rows,), -1, dtype=torch.int32, device=p.device)
     if take is None:

@@ -155,8 +155,9 @@ __global__ void __launch_bounds__(Layout<D, NT>::kThreads, Layout<D, NT>::kCtas)
   }
   pdl_trigger();
   // (kOwn starts beside the groups' launch, every CTA of which has seen the work before it complete when this one
-  // begins; it waits for that launch at its end.)
+  // begins; it waits for that launch at its end.  The fence, of acquire too, leaves nothing older in this SM's L1 cache.)
   if (kMode != kOwn) pdl_wait();
+  else __threadfence();
   // CTAs that take part.
   const int room = kMode == kOwn ? min((int)gridDim.x, own_sms(p, prefix_sms<kThreads>(p, ring)) * L::kCtas) : (int)gridDim.x;
 

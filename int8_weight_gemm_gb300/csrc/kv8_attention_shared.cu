@@ -43,6 +43,7 @@ template <bool kF16, int D>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_constant__ JoinParams j) {
   const Params& p = j.p;
   pdl_trigger();
+  __threadfence();   // (what is read before the wait is not older than the first launch's wait)
   const int lane = threadIdx.x & 31, row = blockIdx.x;
   // The row's sequence (the last that begins at or before it) and group.  None of this is written by the launches that
   // this one waits for.

@@ -205,6 +205,30 @@ def test_a_graph_follows_lengths_and_prefixes():
         assert torch.equal(first[0], out) and torch.equal(first[1], lse)
 
 
+def test_lengths_that_change_between_two_calls():
+    # Device work between two calls of one graph rewrites what the second and third launches read early.
+    c = Shared([1] * 6, [300, 310, 330, 420, 322, 370], [0, 6], [256], 8, 2, 128, 64, seed=3)
+    c.tensors()
+    lens = [i32([300, 310, 330, 420, 322, 370]), i32([257, 290, 258, 270, 300, 310])]
+    prefix = [i32([256]), i32([192])]
+    outs = [torch.empty_like(c.q.contiguous()) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        for i in range(2):
+            c.step.kv_len.copy_(lens[i])
+            c.groups.prefix.copy_(prefix[i])
+            lib8.kv8_attention_shared(c.cache, c.step, c.groups, c.q, c.ws, out=outs[i])
+    for _ in range(50):
+        g.replay()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    for i in range(2):
+        c.lens = lens[i].tolist()
+        c.check_attention(outs[i], None, 128 ** -0.5)
+
+
 def test_the_workspace_serves_plain_attention_too():
     c = Shared([1] * 5, [700, 650, 680, 900, 640], [0, 5], [640], 8, 2, 128, 64, seed=5)
     c.tensors()
