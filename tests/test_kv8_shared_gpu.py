@@ -266,3 +266,31 @@ def test_another_stream():
         out = how()
         s.synchronize()
         c.check_attention(out, None, 128 ** -0.5)
+
+
+def test_two_streams_at_once():
+    # Two steps with workspaces of their own, under each other's load: the bits of each alone.
+    cs = [Shared([1] * 40, [2048 + 17 * b + 1 for b in range(40)], [0, 40], [2048], 8, 2, 128, 64, seed=1),
+          Shared([3] * 12, [1024 + 33 * b + 3 for b in range(12)], [0, 5, 12], [1024, 1000], 16, 4, 128, 32, seed=2)]
+    alone, outs, graphs = [], [], []
+    for c in cs:
+        c.tensors()
+        out = torch.empty_like(c.q.contiguous())
+        lib8.kv8_attention_shared(c.cache, c.step, c.groups, c.q, c.ws, out=out)
+        torch.cuda.synchronize()
+        alone.append(out.clone())
+        outs.append(out)
+        g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=side):
+            for _ in range(20):
+                lib8.kv8_attention_shared(c.cache, c.step, c.groups, c.q, c.ws, out=out)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    for _ in range(20):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for c, a, o in zip(cs, alone, outs):
+        assert c.status() == 0 and torch.equal(a, o)
