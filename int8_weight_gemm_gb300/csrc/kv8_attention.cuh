@@ -185,7 +185,7 @@ __device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long units = 0, own = 0;
   for (int b = threadIdx.x; b < p.step.seqs; b += kThreads) own += max(0, __ldg(p.step.kv_len + b));
-  for (int g = threadIdx.x; g < p.groups; g += kThreads) {
+  for (int g = kThreads - 1 - (int)threadIdx.x; g < p.groups; g += kThreads) {   // (by other warps: their loads go side by side)
     Rows s;
     load_group(p, g, s);
     if (s.n > 0) {
