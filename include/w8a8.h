@@ -582,7 +582,7 @@ enum { SPEC_F32 = 2 };   /* dtype of the calls below, beside KV8_BF16 and KV8_F1
 
 /* out[r][i] = exp((x[r][i] - max) * inv_temp[r]) / sum_j exp((x[r][j] - max) * inv_temp[r]), fp32, of
  * logits x [rows][vocab] of `dtype`, in one pass with fp32 sums; weights below 2^-126 of a row's largest
- * are 0.  Strides in elements, any that hold a row; rows that begin on boundaries of four values are
+ * may be 0, and differences beyond fp32's range count as -infinity.  Strides in elements, any that hold a row; rows that begin on boundaries of four values are
  * read and written four at a time.  out = logits (fp32, same strides) works in place; other overlaps are
  * not allowed.
  *  inv_temp  [rows] fp32: 1 / temperature, NULL: 1 everywhere.  +infinity (temperature 0): 1 for the

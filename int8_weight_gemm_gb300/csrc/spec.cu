@@ -166,6 +166,9 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
     const float inv = next_inv;
     next_inv = factor_of(row + stride);
     const bool greedy = inv == INFINITY;
+    // The product with log2 e is one factor with 1 / T; where it would pass the largest float, the differences take four of it.
+    const bool steep = !greedy && inv > 0x1p126f;
+    const float k2 = (steep ? 0.25f * inv : inv) * 1.44269504f;
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kE; ++i) m = fmaxf(m, v[i]);   // (a NaN is passed over)
@@ -184,8 +187,12 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
 #pragma unroll
         for (int i = 0; i < kE; ++i) v[i] = v[i] == INFINITY ? 0.f : -INFINITY;
       }
-      // The product with log2 e is one factor with 1 / T.
-      const float ref = fabsf(m) == INFINITY ? 0.f : m, k2 = inv * 1.44269504f;
+      float ref = fabsf(m) == INFINITY ? 0.f : m;
+      if (steep) {
+#pragma unroll
+        for (int i = 0; i < kE; ++i) v[i] = 4.f * (v[i] - ref);
+        ref = 0.f;
+      }
       const uint64_t ref2 = pair(-ref, -ref), k22 = pair(k2, k2);
       uint64_t sum2[2] = {0, 0};   // (0, 0)
 #pragma unroll
@@ -242,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, kE <= 32 ? 2 : 1) spec_probs_kernel(
 #pragma unroll
       for (int i = 0; i < kE; ++i) v[i] = (int)first + place(i) == best ? 1.f : 0.f;
     } else {
-      const float k2 = inv * 1.44269504f;
-      auto weight = [&](float x) { return x == M ? 1.f : ex2(fmaxf((x - M) * k2, -200.f)); };
+      auto weight = [&](float x) { return x == M ? 1.f : ex2(fmaxf((steep ? 4.f * (x - M) : x - M) * k2, -200.f)); };
       float S = 0.f;
 #pragma unroll
       for (int c = 0; c < kPeers; ++c) S = fmaf(peers[c].y, weight(peers[c].x), S);
