@@ -593,8 +593,8 @@ enum { SPEC_F32 = 2 };   /* dtype of the calls below, beside KV8_BF16 and KV8_F1
 int spec_probs(const void* logits, long long logits_stride, const float* inv_temp, float* out,
                long long out_stride, int rows, int vocab, int dtype, void* stream);
 
-/* Workspace bytes of spec_verify (0 for arguments it would reject).  Like the attention side's it is not
- * for other calls. */
+/* Workspace bytes of spec_verify for up to `seqs` sequences and `vocab` tokens (0 for arguments it would
+ * reject).  Like the attention side's it is not for other calls. */
 size_t spec_workspace_bytes(int seqs, int vocab);
 
 /* Verification of drafted tokens.  Sequence b has rows row0[b] ... row0[b + 1] - 1 of the call's `rows`:

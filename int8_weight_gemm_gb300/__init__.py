@@ -899,7 +899,7 @@ def spec_probs(logits, inv_temp=None, out=None, stream=None):
 
 
 def spec_workspace_bytes(seqs: int, vocab: int) -> int:
-    """Bytes of the workspace of spec_verify on the current device."""
+    """Bytes of the workspace of spec_verify for up to `seqs` sequences and `vocab` tokens, on the current device."""
     return int(lib().spec_workspace_bytes(seqs, vocab))
 
 

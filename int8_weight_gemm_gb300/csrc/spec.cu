@@ -621,9 +621,16 @@ constexpr int kMaxSeqs = 65535;
 constexpr size_t kCounterBytes = ((size_t)kMaxSeqs * sizeof(uint32_t) + 255) / 256 * 256;
 
 // A sequence's CTAs: as many as the SMs hold for all sequences together, of segments that are worth a warp.
+static int most_ctas(int vocab) { return (vocab + kMinSegment * kVWarps - 1) / (kMinSegment * kVWarps); }
 static int verify_ctas(int seqs, int vocab, int sms) {
-  const int most = (vocab + kMinSegment * kVWarps - 1) / (kMinSegment * kVWarps), want = sms * kCtasPerSm / seqs;
+  const int most = most_ctas(vocab), want = sms * kCtasPerSm / seqs;
   return want < 1 ? 1 : want < most ? want : most;
+}
+// All sequences' CTAs at most, of any call with up to as many sequences and tokens (the quotient above rounds down, so the
+// product itself may be larger for fewer sequences).
+static size_t most_places(int seqs, int vocab, int sms) {
+  const long long all = (long long)seqs * most_ctas(vocab), held = (long long)sms * kCtasPerSm, places = all < held ? all : held;
+  return (size_t)(places > seqs ? places : seqs);
 }
 
 }  // namespace spec
@@ -668,7 +675,7 @@ extern "C" int spec_probs(const void* logits, long long logits_stride, const flo
 
 extern "C" size_t spec_workspace_bytes(int seqs, int vocab) {
   if (seqs < 1 || seqs > spec::kMaxSeqs || vocab < 1 || vocab > spec::kMaxVocab) return 0;
-  return kWsHeaderBytes + spec::kCounterBytes + (size_t)seqs * spec::verify_ctas(seqs, vocab, device_sm_count()) * spec::kVWarps * sizeof(long long);
+  return kWsHeaderBytes + spec::kCounterBytes + spec::most_places(seqs, vocab, device_sm_count()) * spec::kVWarps * sizeof(long long);
 }
 
 extern "C" int spec_verify(const void* p, long long p_stride, const void* q, long long q_stride, const int32_t* tokens, const int32_t* row0,
