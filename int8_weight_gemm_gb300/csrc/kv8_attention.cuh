@@ -79,26 +79,28 @@ struct Rows : Seq {
   int lo, table;
 };
 
+// (The loads from here to prefix_sms are ordinary ones: kOwn makes them before it has waited, and so does the join.)
+
 // The group of sequence b (-1: of none).
 __device__ __forceinline__ int group_of(const Params& p, int b) {
   int lo = 0, n = p.groups;   // the last group that begins at or before b
   while (n > 1) {
     const int half = n >> 1;
-    if (__ldg(p.seq0 + lo + half) <= b) lo += half;
+    if (load<true>(p.seq0 + lo + half) <= b) lo += half;
     n -= half;
   }
-  return __ldg(p.seq0 + lo) <= b && b < __ldg(p.seq0 + lo + 1) ? lo : -1;
+  return load<true>(p.seq0 + lo) <= b && b < load<true>(p.seq0 + lo + 1) ? lo : -1;
 }
 
 // Group g as a sequence: the rows of all its sequences over their shared prefix, in whole pages; `table`: its first
 // sequence.  No rows and no tokens where nothing is shared: a single sequence, or a first one that does not hold the
 // prefix.  (Two rounds of loads: what depends on the first is asked for at once, at indices held in range.)
 __device__ __forceinline__ void load_group(const Params& p, int g, Rows& s) {
-  const int first = __ldg(p.seq0 + g), last = __ldg(p.seq0 + g + 1);
-  const int whole = __ldg(p.prefix + g) & ~((1 << p.page_shift) - 1);
+  const int first = load<true>(p.seq0 + g), last = load<true>(p.seq0 + g + 1);
+  const int whole = load<true>(p.prefix + g) & ~((1 << p.page_shift) - 1);
   const bool ok = first >= 0 && last >= first && last <= p.step.seqs;
   const int f = ok ? min(first, p.step.seqs - 1) : 0;
-  const int len = __ldg(p.step.kv_len + f), r0 = __ldg(p.step.row0 + f), r1 = __ldg(p.step.row0 + (ok ? last : 0));
+  const int len = load<true>(p.step.kv_len + f), r0 = load<true>(p.step.row0 + f), r1 = load<true>(p.step.row0 + (ok ? last : 0));
   if (!ok) atomicOr(p.status, W8A8_DEV_BAD_INDEX);
   s.lo = 0;
   s.table = f;
@@ -123,7 +125,7 @@ __device__ __forceinline__ void load_rows(const Params& p, int b, Rows& s) {
   if (kMode == kPrefixes) return load_group(p, b, s);
   s.lo = 0;
   s.table = b;
-  load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  load_seq<kMode == kOwn>(p.step, b, 1 << p.page_shift, false, p.status, s);
   if (kMode == kOwn) {
     int g;
     Rows of;
@@ -184,13 +186,13 @@ __device__ __forceinline__ int prefix_sms(const Params& p, void* scratch) {
   uint32_t* const best_sm = reinterpret_cast<uint32_t*>(sums_sm + 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long units = 0, own = 0;
-  for (int b = threadIdx.x; b < p.step.seqs; b += kThreads) own += max(0, __ldg(p.step.kv_len + b));
+  for (int b = threadIdx.x; b < p.step.seqs; b += kThreads) own += max(0, load<true>(p.step.kv_len + b));
   for (int g = kThreads - 1 - (int)threadIdx.x; g < p.groups; g += kThreads) {   // (by other warps: their loads go side by side)
     Rows s;
     load_group(p, g, s);
     if (s.n > 0) {
       units += ((long long)s.n * p.group + p.tile_rows - 1) / p.tile_rows * (3 + (s.len + p.block - 1) / p.block);
-      own -= (long long)s.len * (__ldg(p.seq0 + g + 1) - s.table);
+      own -= (long long)s.len * (load<true>(p.seq0 + g + 1) - s.table);
     }
   }
 #pragma unroll

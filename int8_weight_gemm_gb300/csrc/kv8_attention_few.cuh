@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(Layout<D, NT, kMode>::kThreads, Layout<D, NT, 
   }
   pdl_trigger();
   // (kOwn starts beside the groups' launch, every CTA of which has seen the work before it complete when this one
-  // begins; it waits for that launch at its end.  The fence, of acquire too, leaves nothing older in this SM's L1 cache.)
+  // begins; it waits for that launch at its end.  The fence, of acquire too, leaves nothing older in this SM's L1 cache for the
+  // ordinary loads behind it.)
   if (kMode != kOwn) pdl_wait();
   else __threadfence();
   // CTAs that take part.
@@ -265,13 +266,13 @@ __global__ void __launch_bounds__(Layout<D, NT, kMode>::kThreads, Layout<D, NT, 
       float a = 0.f, v = 0.f;
       row_r = 0;
       if (j < mine_n) {
-        const int page = __ldg(table + (t >> p.page_shift));
+        const int page = load<kMode == kOwn>(table + (t >> p.page_shift));
         bad = page < 0 || page >= p.pages;
         if (!bad) {
           const size_t at = (size_t)page * p.kv_heads + h;
           row_r = (int)(at << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-          a = __ldg(p.ks + at);
-          v = __ldg(p.vs + at);
+          a = load<kMode == kOwn>(p.ks + at);
+          v = load<kMode == kOwn>(p.vs + at);
         } else {
           atomicOr(p.status, W8A8_DEV_BAD_INDEX);
         }
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(Layout<D, NT, kMode>::kThreads, Layout<D, NT, 
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
         const int d = D == 256 ? 128 * (w >> 2) + 32 * c + 8 * (w & 3) : (D / 4) * c + 8 * w;
-        rows_raw[i][w] = live ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        rows_raw[i][w] = live ? load<kMode == kOwn>(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
       }
     }
     if (!dead && mine_n > 0) {

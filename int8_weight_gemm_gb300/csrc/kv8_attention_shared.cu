@@ -51,25 +51,25 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const __grid_con
   int b = 0;
   for (int n = p.step.seqs; n > 1;) {
     const int step = (n + 31) / 32;
-    const bool in = lane * step < n && __ldg(p.step.row0 + b + lane * step) <= row;
+    const bool in = lane * step < n && load<true>(p.step.row0 + b + lane * step) <= row;
     const uint32_t mask = __ballot_sync(0xffffffffu, in);
     const int k = mask ? 31 - __clz(mask) : 0;
     b += k * step;
     n = min(step, n - k * step);
   }
   Seq s;
-  load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+  load_seq<true>(p.step, b, 1 << p.page_shift, false, p.status, s);
   auto holds_row = [&]() { return s.n > 0 && row >= s.row0 && row - s.row0 < s.n; };
   if (!holds_row()) {
     // Behind the last sequence, as a step's unused rows are (1000 sequences, 8000 rows: looked for all the same 235 us a call,
     // not 100); or the search met the offset of a sequence that is left out, and the row is another's.
-    const int rows = __ldg(p.step.row0 + p.step.seqs);
+    const int rows = load<true>(p.step.row0 + p.step.seqs);
     for (int b0 = row >= rows && rows >= 0 ? p.step.seqs : 0; b0 < p.step.seqs && !holds_row(); b0 += 32) {
       const int at = b0 + lane;
-      const bool in = at < p.step.seqs && __ldg(p.step.row0 + at) <= row && row < __ldg(p.step.row0 + at + 1);
+      const bool in = at < p.step.seqs && load<true>(p.step.row0 + at) <= row && row < load<true>(p.step.row0 + at + 1);
       for (uint32_t mask = __ballot_sync(0xffffffffu, in); mask && !holds_row(); mask &= mask - 1) {
         b = b0 + __ffs(mask) - 1;
-        load_seq(p.step, b, 1 << p.page_shift, false, p.status, s);
+        load_seq<true>(p.step, b, 1 << p.page_shift, false, p.status, s);
       }
     }
   }
