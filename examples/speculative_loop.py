@@ -7,7 +7,9 @@
     python examples/speculative_loop.py [--batch 24] [--prompt 2048] [--window 5] [--steps 64]
 
 Weights are random.  Drafts are looked up: a table of each token's likely successor, learnt from what the model has said.
-A step is captured once in a CUDA graph; lengths, page tables and windows change in device memory."""
+A step is captured once in a CUDA graph; lengths, page tables and windows change in device memory.  (At these sizes
+kv8_attention_shared leaves a step to kv8_attention's launch; from a table with room for some 400,000 tokens times kv heads on
+it reads the prompt once for all requests.)"""
 import argparse
 import os
 import sys

@@ -502,11 +502,13 @@ size_t kv8_shared_workspace_bytes(int tokens, int groups, int q_heads, int kv_he
  * common are read once, from the pages of the group's first sequence, for the rows of all of them.
  * The result is that of kv8_attention, with its arguments, where the sequences of each group do hold
  * the same tokens there.  Nothing is shared, and each sequence reads its own pages, in a group of one
- * sequence, in one whose first sequence holds less than the prefix, and for a sequence with a row that
- * does not see all of the prefix; sequences of no group are read on their own.  Nor is anything shared in a
+ * sequence, in one whose first sequence holds less than the prefix (so also once that one has ended and
+ * kv8_plan has made its kv_len 0: put another first), and for a sequence with a row that does not see all of
+ * the prefix; sequences of no group are read on their own.  Nor is anything shared in a
  * step that kv8_attention reads as fast by itself: one of many rows a sequence (80 of a kv head), or of a page
  * table with room for few tokens (seqs * table_width * page_tokens * kv_heads up to 400,000 or 700,000, by
- * rows); the table need be no wider than the step.
+ * rows).  The lengths are on the device, so this goes by the table alone: a short step in a wide table, as in a
+ * captured graph, takes the three launches, some 10 us more than kv8_attention.
  * Three launches (one where nothing is shared), otherwise as kv8_attention.  Errors as above. */
 int kv8_attention_shared(const kv8_cache_t* cache, const kv8_step_t* step, const kv8_groups_t* groups,
                          const void* q, long long q_stride, int q_heads, void* out, long long out_stride,
@@ -582,14 +584,16 @@ enum { SPEC_F32 = 2 };   /* dtype of the calls below, beside KV8_BF16 and KV8_F1
 
 /* out[r][i] = exp((x[r][i] - max) * inv_temp[r]) / sum_j exp((x[r][j] - max) * inv_temp[r]), fp32, of
  * logits x [rows][vocab] of `dtype`, in one pass with fp32 sums; weights below 2^-126 of a row's largest
- * may be 0, and differences beyond fp32's range count as -infinity.  Strides in elements, any that hold a row; rows that begin on boundaries of four values are
- * read and written four at a time.  out = logits (fp32, same strides) works in place; other overlaps are
+ * may be 0, and differences beyond fp32's range count as -infinity.  Strides in elements, any that hold a row; where both tensors' rows lie in
+ * whole 16 bytes (address, stride and vocabulary) they are copied ahead and taken four values at a time, else
+ * one by one.  out = logits (fp32, same strides) works in place; other overlaps are
  * not allowed.
  *  inv_temp  [rows] fp32: 1 / temperature, NULL: 1 everywhere.  +infinity (temperature 0): 1 for the
  *            first of the row's largest logits and 0 for the others.  Below 0 or NaN: taken as 0
  * A logit of -infinity (a mask) or NaN has probability 0, logits of +infinity share the row; a row
  * without anything else than -infinity and NaN is all 0.
- * 1 <= vocab <= 2^18, rows <= 2^22.  One launch, no workspace.  Errors: INVALID_ARG, MISALIGNED, CUDA. */
+ * 1 <= vocab <= 2^18 = 262144 (a row lies in a cluster's registers; larger ones are refused), rows <= 2^22.
+ * One launch, no workspace: a row whose bounded waits run out, which no valid call causes, is NaN.  Errors: INVALID_ARG, MISALIGNED, CUDA. */
 int spec_probs(const void* logits, long long logits_stride, const float* inv_temp, float* out,
                long long out_stride, int rows, int vocab, int dtype, void* stream);
 

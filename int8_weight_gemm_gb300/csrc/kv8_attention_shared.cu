@@ -17,7 +17,7 @@
 // what that work wrote; it waits for the groups' at its end, so that the join, which waits for it, sees both.
 //
 // Measured (32 query heads, 8 kv heads of 128; in brackets kv8_attention, whose re-reads hit L2): 64 sequences of 6101-8191
-// tokens behind one prefix of 6016 62 us (141), some 35 us of it 148 MB of own tokens' stream and products beside it, 5 the
+// tokens behind one prefix of 6016 61 us (141), some 35 us of it 148 MB of own tokens' stream and products beside it, 5 the
 // start, 5 the join; behind 16000 with up to 400 own tokens 69 (299).  One launch after the other took 89, with the parts joined by
 // rows (uncoalesced) 70, with eight warps a CTA of the second launch 66.
 #include "kv8_attention_few.cuh"
@@ -261,7 +261,9 @@ static void set_costs(Params& p, int head_dim, long long rows) {
 // And the re-reads of a prefix hit L2, so a small cache, by what the page table has room for, is read in less time than the
 // three launches take (128-wide heads): 16 sequences on 1200 tokens, 4 kv heads (20 MB) 11.7 / 24; 64 of
 // 1700, 8 (213 MB) 46 / 42.5; 64 of 2700 (341 MB) 64 / 45; 64 of 7000 (897 MB) 141 / 62; 16 windows of 6 on 4300 (134 MB, 24
-// rows) 48 / 45; heads of 64, 32 of 3000, 16 kv heads (196 MB) 50 / 41.
+// rows) 48 / 45; heads of 64, 32 of 3000, 16 kv heads (196 MB) 50 / 41.  It is not always right: four groups of four windows of
+// 6 behind 1001 to 4003 42.2 / 43.8; and a short step in a wide table, which the host cannot tell from a long one, 4 sequences on 700
+// 8.4 / 18.1, 16 on 1400 11.7 / 24.2.
 static bool worth_sharing(const kv8_cache_t* cache, const kv8_step_t* step, long long rows) {
   const long long tokens = (long long)step->seqs * step->table_width * cache->page_tokens * cache->kv_heads;
   return rows < kManyRows && tokens > (rows <= 16 ? kFewTokens : kFewTokensWide);

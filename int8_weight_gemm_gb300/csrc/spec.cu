@@ -46,7 +46,9 @@ struct Type<SPEC_F32> {
 // the row after that is fetched into L2, so that loads hide behind a whole row's work (320 rows of 131072: loads into
 // registers behind the stores 58 us, without the fetch into L2 94).
 //
-// Measured: 320 rows of 131072 (bf16) 47 us, 5.3 TB/s, 79 % of a copy's rate; 16 rows of 32000 3.6 us.
+// Measured (bf16): 320 rows of 131072 48 us, 5.2 TB/s, 77 % of a copy's rate; 16 rows of 32000 3.7 us.  Beyond 131072 a thread
+// holds 64 values and an SM one CTA: 320 rows of 151936 74 us (58 %), 201088 83 (69 %), 262144 95 (78 %).  Rows not in whole 16
+// bytes, one value a load: 50257 in a stride of 50304 27.8 us (51 %; 50304 21.7), 131071 67.7.
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;

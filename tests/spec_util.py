@@ -94,11 +94,13 @@ def verify(p, q, tokens, row0, accept, sample):
 def probs(x, inv):
     """(probabilities, bound of |gpu - p|) of logits x [rows, V], in 64 bits.
 
-    The bound follows the arithmetic, with u = 2^-24 and t = (x - ref) inv <= 0 of a value or of a CTA's maximum: t is
-    two roundings, 2 u |t| of the exponential; the exponential is off by 2^-22 (the instruction's) and u for its last
-    step; a sum of positive terms by 96 roundings at most (64 of a thread, 5 of a warp, 16 warps, 8 CTAs); the factor
-    and the product by 3 more.  A value's t and its CTA's together are at most twice the value's.  What is below 2^-126 of
-    a CTA's maximum may be 0."""
+    The bound follows the arithmetic, with u = 2^-24 and t = (x - ref) inv <= 0 of a value (ref: its warp's maximum) or of a
+    warp's maximum (ref: the row's): the difference, log2 e, its product with inv and the product of the two are four
+    roundings at most, 4 u |t| of the exponential, which is off by 2^-22 (the instruction's) and u for its last step.  A
+    value's t and its warp's add up to the value's in the row.  Sums of positive terms: 32 of a thread at most in one chain
+    (16 in each of two where no value is NaN), 2 to join its four, 5 of a warp, 4 products added by a lane over the warps'
+    sums, 5 of the lanes; the quotient, the factor and the product 3 more: 51, under the 99 that are taken.  What is below
+    2^-126 of a warp's maximum may be 0."""
     u = 2.0 ** -24
     x = x.astype(np.float64)
     out, bound = np.zeros_like(x), np.full_like(x, 2.0 ** -125)
